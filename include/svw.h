@@ -7,7 +7,8 @@
  * (spec_verify_early: stops reading each request at its first rejection;
  * spec_verify_filtered: top-k / top-p filtered distributions), plus the
  * adaptive length head that sets the next round's verified lengths
- * (length_head, length_head_label):
+ * (length_head, length_head_label), and the steps of a round that precede the
+ * verification (kv_append, paged_attention, logits_adjust):
  *
  *  spec_verify  batched speculative verification of a ragged batch.  Defined
  *               by "DFlash 阅读笔记：并行起草、目标特征与精确验证" §5.1 (greedy
@@ -39,7 +40,8 @@
  *    V * sizeof(dtype) is a multiple of 16 with 16-byte aligned bases take the
  *    vectorised / bulk-copy path; any other shape takes a scalar path with the
  *    same results.
- *  - Inputs are read-only; outputs must not alias inputs.
+ *  - Inputs are read-only; outputs must not alias inputs, except where an
+ *    entry point says so (logits_adjust, kv_append's queries).
  */
 #ifndef SVW_H_
 #define SVW_H_
@@ -351,6 +353,176 @@ svw_status length_head_label(const int32_t *accept_len, const int32_t *cu_draft,
                              float *a_star, float *loss, void *stream);
 
 /*
+ * The steps around a verification on the same ragged batch: the target's
+ * forward pass writes the new tokens' keys and values into a paged cache
+ * (kv_append), attends from them (paged_attention), and its logits are
+ * adjusted (logits_adjust) before spec_verify reads them ("AdaFlash：基于在策略
+ * 蒸馏扩散草稿器的自适应投机解码" §2.3: the verified positions of all requests
+ * are packed, sum of L_i + 1 tokens, without padding).  No counterpart on the
+ * pages; the formulas below are the definitions.
+ */
+
+/*
+ * logits_adjust -- penalties for repeated tokens, biases and grammar masks on
+ * the logits of every drafted position.
+ *
+ * Row j of request i (0 <= j < L_i, and j = L_i when has_bonus_row) has seen
+ * the request's history and its drafted tokens x_0 .. x_{j-1}.  With
+ * n(v) = the occurrences of v in the history after its first prompt_len[i]
+ * tokens and in that drafted prefix, and seen(v) = n(v) > 0 or v in the
+ * prompt part, in fp32 and in this order:
+ *   y = logits[row, v]
+ *   seen(v):  y = y > 0 ? y / repetition[i] : y * repetition[i]
+ *   n(v) > 0: y = y - frequency[i] n(v) - presence[i]
+ *   v listed in the request's biases: y = y + its value (the last one listed)
+ *   mask bit of v is 0: y = -inf (whatever y is, NaN too)
+ * rounded once to the logits' type; an entry that none of these touches is
+ * copied bit for bit.  A row whose mask allows nothing is all -inf (which
+ * spec_verify reports as a bad request at T > 0).
+ *
+ *   logits         device [rows, V], row pitch logits_stride elements (>= V);
+ *                  rows = total_draft_rows (+ N when has_bonus_row), request
+ *                  i's first row at cu_draft[i] (+ i).
+ *   cu_draft       device int32 [N+1], as for spec_verify; 0 <= L_i <=
+ *                  SVW_MAX_LEN (L_i = 0 with has_bonus_row: a request that
+ *                  decodes one token without a draft).
+ *   draft_tokens   device int32 [total_draft_rows]; may be NULL when that is 0.
+ *   history        device int32 [total_history], request i's tokens at
+ *                  cu_history[i] .. cu_history[i+1]-1; cu_history NULL: none.
+ *   prompt_len     device int32 [N], 0 <= prompt_len[i] <= its history's
+ *                  length; NULL: 0.
+ *   repetition     device float [N], finite and > 0; NULL: 1.
+ *   frequency, presence  device float [N], finite; NULL: 0.
+ *   bias_tokens, bias_values  device int32 / float [total_bias], request i's
+ *                  at cu_bias[i] .. cu_bias[i+1]-1; values < +inf (-inf bans
+ *                  the token); cu_bias NULL: none.
+ *   mask           device uint32 [mask_rows, ceil(V / 32)], bit v % 32 of
+ *                  word v / 32 set: v is allowed; NULL: none.
+ *   mask_row       device int32 [rows]: the mask row of each logit row, -1:
+ *                  unmasked; NULL: row r has mask row r (mask_rows = rows).
+ *   out            device [rows, V], row pitch out_stride; equal to logits
+ *                  (same pitch): in place, only what changes is written.  Any
+ *                  other overlap of the two ranges is SVW_ERR_INVALID_ARG.
+ *   status         as for spec_verify; SVW_DEV_BAD_INPUT when a request's
+ *                  lists are inconsistent, hold a token outside [0, V) or a
+ *                  factor outside its range (its rows become NaN, which
+ *                  spec_verify reports as a bad request), a mask row is
+ *                  outside [-1, mask_rows) (that row becomes NaN), or its
+ *                  CSR range is invalid (its rows are not written).
+ * One kernel launch, no workspace.
+ */
+svw_status logits_adjust(const void *logits, int64_t logits_stride, svw_dtype dtype, int32_t V, int32_t N,
+                         const int32_t *cu_draft, int64_t total_draft_rows, int32_t has_bonus_row,
+                         const int32_t *draft_tokens, const int32_t *history, const int32_t *cu_history,
+                         int64_t total_history, const int32_t *prompt_len, const float *repetition,
+                         const float *frequency, const float *presence, const int32_t *bias_tokens,
+                         const float *bias_values, const int32_t *cu_bias, int64_t total_bias,
+                         const uint32_t *mask, int64_t mask_rows, const int32_t *mask_row, void *out,
+                         int64_t out_stride, int32_t *status, void *stream);
+
+/*
+ * A paged key / value cache: n_pages pages of page_size tokens for each of
+ * n_kv_heads heads of head_dim elements.  Element e of head h of the token in
+ * row r of page p is at p * stride[0] + h * stride[1] + r * stride[2] + e
+ * (strides in elements, so that pages may hold heads of tokens or tokens of
+ * heads).  A request's tokens lie in the pages of its row of the block table:
+ * token t in page block_table[i * table_stride + t / page_size], row
+ * t % page_size.  Entries of pages that no token of the request needs may
+ * hold anything.
+ */
+typedef struct svw_paged_kv {
+  void *k;
+  void *v;
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  const int32_t *block_table; /* device int32 [N, max_pages], row pitch table_stride */
+  int64_t table_stride;
+  int32_t max_pages;
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+} svw_paged_kv;
+
+/*
+ * kv_append -- the new tokens' keys, rotated by their positions, and values
+ * written to the paged cache; optionally their queries rotated too.
+ *
+ * Request i owns the new tokens cu_new[i] .. cu_new[i+1]-1 (n_i of them, 0
+ * allowed); they are its last ones: token t sits at place
+ * kv_len[i] - n_i + t of the cache, kv_len[i] counting the new tokens.  The
+ * position rotated by is that place, or positions[token].  With c, s the
+ * first and second half of cos_sin's row of that position, pair u of
+ * 0 .. rot_dim/2 - 1 of each head of k (and q) becomes
+ *   (a, b) -> (a c_u - b s_u, b c_u + a s_u)        (fp32, rounded once)
+ * with (a, b) the elements (u, u + rot_dim/2), or (2u, 2u + 1) when
+ * interleaved; elements from rot_dim on are copied, as is all of v.
+ *
+ *   k, v       device [total_new, n_kv_heads, head_dim], of type dtype as the
+ *              cache is; strides of tokens and heads in elements.
+ *   q, q_out   device [total_new, n_q_heads, head_dim], q strided like k,
+ *              q_out contiguous; both NULL: no queries.  q_out may be q
+ *              itself when q is contiguous.
+ *   cu_new     device int32 [N+1], cu_new[0] = 0, cu_new[N] = total_new.
+ *   cos_sin    device float [max_pos, rot_dim]; NULL with rot_dim = 0: no
+ *              rotation.  rot_dim even, <= head_dim <= 1024.
+ *   status     SVW_DEV_BAD_INPUT when a token's place is negative or beyond
+ *              its block table, its page is not one of the cache's, or its
+ *              position is outside [0, max_pos): such a token is not written
+ *              (its query, if its position is bad, becomes NaN).
+ * Two new tokens never share a place; pages shared by requests must not be
+ * written.  One kernel launch, no workspace.
+ */
+svw_status kv_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                     int64_t v_token_stride, int64_t v_head_stride, const void *q, int64_t q_token_stride,
+                     int64_t q_head_stride, void *q_out, svw_dtype dtype, int32_t n_q_heads, int32_t N,
+                     const int32_t *cu_new, int64_t total_new, const int32_t *kv_len, const int32_t *positions,
+                     const float *cos_sin, int64_t max_pos, int32_t rot_dim, int32_t interleaved,
+                     const svw_paged_kv *cache, int32_t *status, void *stream);
+
+/*
+ * paged_attention -- attention of each request's new tokens over its cached
+ * keys (the new tokens' own ones included, as kv_append leaves them).
+ *
+ * New token t of request i (at place p = kv_len[i] - n_i + t) and query head
+ * h see the keys j of head h / (n_q_heads / n_kv_heads) with
+ *   0 <= j < kv_len[i],  causal: j <= p,  window > 0: j > p - window;
+ *   out = sum_j softmax_j(scale q . k_j) v_j,  lse = log sum_j exp(scale q . k_j)
+ * causal = 0: every new token sees the whole block (a diffusion drafter's).
+ * A token that sees no key has out = 0 and lse = -inf.  kv_len[i] < n_i is
+ * allowed: the tokens at negative places see nothing (causal).
+ *
+ *   q          device bf16 [total_new, n_q_heads, head_dim], strides of
+ *              tokens and heads in elements; n_q_heads a multiple of
+ *              n_kv_heads, at most 64 times it.
+ *   cache      bf16; head_dim 64 or 128; page_size a power of two, 16 to 1024.
+ *              Keys and values at places below kv_len must be finite (a row
+ *              that a mask hides from a token may still reach it as 0 times
+ *              its value); what lies beyond in the last page is not read into
+ *              any result.
+ *   scale      finite, > 0;  window >= 0, 0 unless causal.
+ *   out        device bf16 [total_new, n_q_heads, head_dim], contiguous.
+ *   lse        device float [total_new, n_q_heads], natural logarithm; may be NULL.
+ *   workspace  device, 256-byte aligned, >= svw_paged_attention_workspace_size
+ *              bytes; contents need not be initialised; not preserved.
+ *   status     SVW_DEV_BAD_INPUT when a request's new-token range is invalid
+ *              (nothing of it is written), its kv_len exceeds its block table
+ *              or a page that it needs is not one of the cache's (its out and
+ *              lse become NaN).
+ * q and the caches: 16-byte aligned, strides positive multiples of 8 elements
+ * (those of dimensions of one do not count).
+ * Scores and sums are fp32; the weights enter the second product in bf16.
+ */
+size_t svw_paged_attention_workspace_size(int64_t total_new, int32_t n_q_heads, int32_t n_kv_heads,
+                                          int32_t head_dim);
+
+svw_status paged_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, svw_dtype dtype,
+                           int32_t n_q_heads, int32_t N, const int32_t *cu_new, int64_t total_new,
+                           const int32_t *kv_len, const svw_paged_kv *cache, float scale, int32_t causal,
+                           int32_t window, void *out, float *lse, int32_t *status, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/*
  * spec_verify_noalloc -- spec_verify for callers that cannot allocate device
  * memory.  No counterpart on the pages: it exists only because some callers
  * have no allocator to hand over a workspace (a plain C serving loop, a
@@ -390,7 +562,8 @@ svw_status spec_verify_noalloc(const void *target_logits, const void *draft_logi
  * kernel made from this thread ("early_plan", "verify_stats",
  * "verify_finalize", "verify_early_cluster", "filter_rows", "filtered_finalize",
  * "opd_fast_kernel", "opd_fix_parts", "opd_fix_grad", "opd_exact_kernel",
- * "fused_finalize", "length_head_mma", "length_head_final") records
+ * "fused_finalize", "length_head_mma", "length_head_final", "logits_adjust",
+ * "kv_append", "paged_attention") records
  * begin_event just before it and end_event just after it on the launch stream (cudaEvent_t handles passed as void*, owned
  * by the caller).  kernel = NULL disarms.  The library records nothing
  * unless armed.  Lets a benchmark time one kernel of a multi-kernel call with

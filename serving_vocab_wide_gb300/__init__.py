@@ -33,6 +33,14 @@ class SvwError(RuntimeError):
     pass
 
 
+class _PagedKV(ctypes.Structure):
+    """svw_paged_kv"""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3), ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
 def lib():
     """The loaded shared library (raises if it has not been built)."""
     global _lib
@@ -82,6 +90,17 @@ def lib():
             L.length_head.restype = ctypes.c_int
             L.length_head_label.argtypes = [P, P, P, I32, P, P, P]
             L.length_head_label.restype = ctypes.c_int
+            L.logits_adjust.argtypes = [P, I64, ctypes.c_int, I32, I32, P, I64, I32, P, P, P, I64, P, P, P, P,
+                                        P, P, P, I64, P, I64, P, P, I64, P, P]
+            L.logits_adjust.restype = ctypes.c_int
+            L.kv_append.argtypes = [P, I64, I64, P, I64, I64, P, I64, I64, P, ctypes.c_int, I32, I32, P, I64, P,
+                                    P, P, I64, I32, I32, P, P, P]
+            L.kv_append.restype = ctypes.c_int
+            L.svw_paged_attention_workspace_size.argtypes = [I64, I32, I32, I32]
+            L.svw_paged_attention_workspace_size.restype = SZ
+            L.paged_attention.argtypes = [P, I64, I64, ctypes.c_int, I32, I32, P, I64, P, P, F, I32, I32, P, P, P,
+                                          P, SZ, P]
+            L.paged_attention.restype = ctypes.c_int
             L.svw_time_next_launch.argtypes = [ctypes.c_char_p, P, P]
             L.svw_time_next_launch.restype = ctypes.c_int
             L.svw_set_wait_limit.argtypes = [I64]
@@ -422,3 +441,210 @@ def opd_loss(target, draft, temperature: float = 1.0, clip_c: float = 1.0,
                         0 if workspace is None else workspace.numel(), _stream_ptr(stream))
     _check(rc)
     return loss, (dlogits if want_grad else None)
+
+
+def _need_typed(dev, dtype, **ts):
+    """Each given tensor is contiguous, of this type and on this device."""
+    for name, t in ts.items():
+        if t is not None and (t.dtype != dtype or t.device != dev or not t.is_contiguous()):
+            raise SvwError(f"{name} must be a contiguous {dtype} tensor on {dev}")
+
+
+def _lent(stream, *ts):
+    """Tensors allocated here and used on another stream than the current one
+    stay the allocator's to reuse only after that stream is done with them."""
+    if stream is not None:
+        for t in ts:
+            t.record_stream(stream)
+
+
+def logits_adjust(logits, cu_draft, draft_tokens=None, *, history=None, cu_history=None, prompt_len=None,
+                  repetition=None, frequency=None, presence=None, bias_tokens=None, bias_values=None, cu_bias=None,
+                  mask=None, mask_row=None, has_bonus: bool = True, total_draft_rows: int | None = None, out=None,
+                  status=None, stream=None):
+    """Penalties for repeated tokens, biases and grammar masks on the logits of
+    every drafted position (a position has seen the request's history and the
+    drafted tokens before it).  Returns the adjusted logits.
+
+    logits: [total_draft_rows + N, V] (the verify layout; [total_draft_rows, V]
+    with has_bonus=False), bf16 or fp32, rows any pitch apart; cu_draft, the
+    other cu_*: int32 CSR offsets; history, prompt_len, bias_tokens, mask_row:
+    int32; repetition, frequency, presence, bias_values: float32; mask: int32
+    [mask rows, ceil(V / 32)] of 32 tokens' bits each, the row of each logit row
+    in mask_row (-1: unmasked; without mask_row, its own).  out may be logits
+    (in place).  `total_draft_rows` (= cu_draft[-1]) may be passed to avoid a
+    device read.
+    """
+    import torch
+    code = _dtype_code(logits)
+    if not logits.is_cuda or logits.dim() != 2 or logits.stride(1) != 1:
+        raise SvwError("logits must be a CUDA matrix with contiguous rows")
+    dev = logits.device
+    rows, V = logits.shape
+    N = cu_draft.numel() - 1
+    R = int(cu_draft[-1].item()) if total_draft_rows is None else int(total_draft_rows)
+    if rows != R + (N if has_bonus else 0):
+        raise SvwError(f"logits have {rows} rows for {R} draft rows of {N} requests")
+    if (history is None) != (cu_history is None) or (prompt_len is not None and history is None):
+        raise SvwError("history comes with cu_history, prompt_len with a history")
+    if (bias_tokens is None) != (cu_bias is None) or (bias_values is None) != (cu_bias is None):
+        raise SvwError("bias_tokens, bias_values and cu_bias come together")
+    if mask is None and mask_row is not None:
+        raise SvwError("mask_row comes with a mask")
+    _need_typed(dev, torch.int32, cu_draft=cu_draft, draft_tokens=draft_tokens, history=history,
+                cu_history=cu_history, prompt_len=prompt_len, bias_tokens=bias_tokens, cu_bias=cu_bias, mask=mask,
+                mask_row=mask_row, status=status)
+    _need_typed(dev, torch.float32, repetition=repetition, frequency=frequency, presence=presence,
+                bias_values=bias_values)
+    for name, t, n in (("draft_tokens", draft_tokens, R), ("prompt_len", prompt_len, N), ("repetition", repetition, N),
+                       ("frequency", frequency, N), ("presence", presence, N), ("cu_history", cu_history, N + 1),
+                       ("cu_bias", cu_bias, N + 1), ("mask_row", mask_row, rows)):
+        if t is not None and t.numel() != n:
+            raise SvwError(f"{name} must have {n} elements")
+    if bias_tokens is not None and bias_tokens.numel() != bias_values.numel():
+        raise SvwError("bias_tokens and bias_values must have one length")
+    if mask is not None and (mask.dim() != 2 or mask.shape[1] != (V + 31) // 32):
+        raise SvwError(f"mask must be [mask rows, {(V + 31) // 32}]")
+    if out is None:
+        out = torch.empty((rows, V), dtype=logits.dtype, device=dev)
+        _lent(stream, out)
+    elif out.dtype != logits.dtype or out.device != dev or out.shape != logits.shape or out.stride(1) != 1:
+        raise SvwError("out must be like logits")
+    # a single row has no pitch of its own
+    pitch = logits.stride(0) if rows > 1 else V
+    out_pitch = out.stride(0) if rows > 1 else V
+    rc = lib().logits_adjust(logits.data_ptr(), pitch, code, V, N, cu_draft.data_ptr(), R, 1 if has_bonus else 0,
+                             _ptr(draft_tokens), _ptr(history), _ptr(cu_history),
+                             0 if history is None else history.numel(), _ptr(prompt_len), _ptr(repetition),
+                             _ptr(frequency), _ptr(presence), _ptr(bias_tokens), _ptr(bias_values), _ptr(cu_bias),
+                             0 if bias_tokens is None else bias_tokens.numel(), _ptr(mask),
+                             0 if mask is None else mask.shape[0], _ptr(mask_row), out.data_ptr(), out_pitch,
+                             _ptr(status), _stream_ptr(stream))
+    _check(rc)
+    return out
+
+
+def _paged(k_cache, v_cache, block_table, N):
+    """The svw_paged_kv of two [n_pages, heads, page_size, head_dim] tensors
+    (any strides but the last) and their block table."""
+    import torch
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise SvwError("k_cache and v_cache must be alike: [n_pages, heads, page_size, head_dim]")
+    if not k_cache.is_cuda or v_cache.device != k_cache.device or k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
+        raise SvwError("the caches must be CUDA tensors with contiguous head vectors")
+    if (block_table.dtype != torch.int32 or block_table.device != k_cache.device or block_table.dim() != 2
+            or block_table.shape[0] != N or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
+        raise SvwError(f"block_table must be an int32 [{N}, max_pages] CUDA tensor with contiguous rows")
+    pages, heads, size, dim = k_cache.shape
+    ks, vs = k_cache.stride(), v_cache.stride()
+    mp = block_table.shape[1]
+    return _PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), ks[:3], vs[:3], block_table.data_ptr(),
+                    max(block_table.stride(0), mp) if N > 1 else mp, mp, pages, size, heads, dim)
+
+
+def _heads(name, t, dim, like):
+    if t.dim() != 3 or t.shape[2] != dim or t.stride(2) != 1 or t.dtype != like.dtype or t.device != like.device:
+        raise SvwError(f"{name} must be [new tokens, heads, {dim}], of the cache's type and device, with contiguous heads")
+
+
+def kv_append(k, v, k_cache, v_cache, block_table, cu_new, kv_len, *, cos_sin=None, interleaved: bool = False,
+              positions=None, q=None, q_out=None, status=None, stream=None):
+    """The new tokens' keys, rotated by their positions, and values written to
+    the paged cache.  Returns their rotated queries (None without q).
+
+    k, v: [total_new, heads, head_dim], q: [total_new, query heads, head_dim],
+    strided as a split of one projection's output is; k_cache, v_cache:
+    [n_pages, heads, page_size, head_dim], any strides (a cache of tokens of
+    heads is passed transposed); block_table: int32 [N, max_pages]; cu_new:
+    int32 [N + 1]; kv_len: int32 [N], the new tokens counted; cos_sin: float32
+    [max_pos, rot_dim], cosines then sines (None: no rotation).  Request i's new
+    token t is written at place kv_len[i] - n_i + t and rotated by that
+    position, or by positions (int32 [total_new]).
+    """
+    import torch
+    N = cu_new.numel() - 1
+    cache = _paged(k_cache, v_cache, block_table, N)
+    dev, T, dim = k_cache.device, k.shape[0], k_cache.shape[3]
+    _heads("k", k, dim, k_cache)
+    _heads("v", v, dim, k_cache)
+    if k.shape[1] != k_cache.shape[1] or v.shape != k.shape:
+        raise SvwError("k and v must have the cache's heads and one length")
+    _need_typed(dev, torch.int32, cu_new=cu_new, kv_len=kv_len, positions=positions, status=status)
+    if kv_len.numel() != N or (positions is not None and positions.numel() != T):
+        raise SvwError(f"kv_len must have {N} elements, positions {T}")
+    _need_typed(dev, torch.float32, cos_sin=cos_sin)
+    if cos_sin is not None and cos_sin.dim() != 2:
+        raise SvwError("cos_sin must be [max_pos, rot_dim]")
+    qs = (0, 0, 0)
+    if q is not None:
+        _heads("q", q, dim, k_cache)
+        if q.shape[0] != T:
+            raise SvwError("q must have as many tokens as k")
+        qs = q.stride()
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            _lent(stream, q_out)
+        elif q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.device != dev or not q_out.is_contiguous():
+            raise SvwError("q_out must be like q, contiguous")
+    elif q_out is not None:
+        raise SvwError("q_out comes with q")
+    ks, vs = k.stride(), v.stride()
+    rc = lib().kv_append(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _ptr(q), qs[0], qs[1], _ptr(q_out),
+                         _dtype_code(k_cache), 0 if q is None else q.shape[1], N, cu_new.data_ptr(), T,
+                         kv_len.data_ptr(), _ptr(positions), _ptr(cos_sin),
+                         0 if cos_sin is None else cos_sin.shape[0], 0 if cos_sin is None else cos_sin.shape[1],
+                         1 if interleaved else 0, ctypes.byref(cache), _ptr(status), _stream_ptr(stream))
+    _check(rc)
+    return q_out
+
+
+def paged_attention_workspace_size(total_new: int, n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(lib().svw_paged_attention_workspace_size(total_new, n_q_heads, n_kv_heads, head_dim))
+
+
+def paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, *, scale: float | None = None,
+                    causal: bool = True, window: int = 0, out=None, lse=None, want_lse: bool = True, status=None,
+                    workspace=None, stream=None):
+    """Attention of each request's new tokens over its cached keys, their own
+    included (as kv_append leaves them).  Returns (out, lse): bf16 [total_new,
+    query heads, head_dim] and float32 [total_new, query heads] (None without
+    want_lse).
+
+    q: bf16 [total_new, query heads, head_dim]; the caches, block_table, cu_new
+    and kv_len as for kv_append.  causal=False: a new token sees its whole
+    block; window > 0: only the last `window` keys up to its own.  scale
+    defaults to head_dim ** -0.5.
+    """
+    import torch
+    N = cu_new.numel() - 1
+    cache = _paged(k_cache, v_cache, block_table, N)
+    dev, dim = k_cache.device, k_cache.shape[3]
+    _heads("q", q, dim, k_cache)
+    T, hq, _ = q.shape
+    _need_typed(dev, torch.int32, cu_new=cu_new, kv_len=kv_len, status=status)
+    if kv_len.numel() != N:
+        raise SvwError(f"kv_len must have {N} elements")
+    if out is None:
+        out = torch.empty((T, hq, dim), dtype=q.dtype, device=dev)
+        _lent(stream, out)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
+        raise SvwError("out must be like q, contiguous")
+    if lse is None and want_lse:
+        lse = torch.empty((T, hq), dtype=torch.float32, device=dev)
+        _lent(stream, lse)
+    _need_typed(dev, torch.float32, lse=lse)
+    if lse is not None and lse.numel() != T * hq:
+        raise SvwError(f"lse must be [{T}, {hq}]")
+    if workspace is None:
+        need = paged_attention_workspace_size(T, hq, k_cache.shape[1], dim)
+        workspace = torch.empty(max(1, need), dtype=torch.uint8, device=dev)
+        _lent(stream, workspace)
+    _need_cuda(workspace)
+    qs = q.stride()
+    rc = lib().paged_attention(q.data_ptr(), qs[0], qs[1], _dtype_code(q), hq, N, cu_new.data_ptr(), T,
+                               kv_len.data_ptr(), ctypes.byref(cache),
+                               float(dim ** -0.5 if scale is None else scale), 1 if causal else 0, int(window),
+                               out.data_ptr(), _ptr(lse), _ptr(status), workspace.data_ptr(), workspace.numel(),
+                               _stream_ptr(stream))
+    _check(rc)
+    return out, lse

@@ -534,4 +534,225 @@ svw_status length_head_label(const int32_t *accept_len, const int32_t *cu_draft,
   return rc == 0 ? SVW_OK : SVW_ERR_CUDA;
 }
 
+svw_status logits_adjust(const void *logits, int64_t logits_stride, svw_dtype dtype, int32_t V, int32_t N,
+                         const int32_t *cu_draft, int64_t total_draft_rows, int32_t has_bonus_row,
+                         const int32_t *draft_tokens, const int32_t *history, const int32_t *cu_history,
+                         int64_t total_history, const int32_t *prompt_len, const float *repetition,
+                         const float *frequency, const float *presence, const int32_t *bias_tokens,
+                         const float *bias_values, const int32_t *cu_bias, int64_t total_bias,
+                         const uint32_t *mask, int64_t mask_rows, const int32_t *mask_row, void *out,
+                         int64_t out_stride, int32_t *status, void *stream) {
+  if (dtype != SVW_F32 && dtype != SVW_BF16) return SVW_ERR_UNSUPPORTED;
+  if (V <= 0 || N <= 0 || total_draft_rows < 0 || total_history < 0 || total_bias < 0 || mask_rows < 0)
+    return SVW_ERR_INVALID_ARG;
+  if (V > kMaxV || total_history > INT32_MAX || total_bias >= INT32_MAX || total_draft_rows > INT32_MAX - N ||
+      mask_rows > INT32_MAX)
+    return SVW_ERR_UNSUPPORTED;
+  if (!logits || !out || !cu_draft || (total_draft_rows > 0 && !draft_tokens) ||
+      (cu_history && total_history > 0 && !history) || (cu_bias && total_bias > 0 && (!bias_tokens || !bias_values)))
+    return SVW_ERR_INVALID_ARG;
+  const int64_t rows = total_draft_rows + (has_bonus_row ? N : 0);
+  if (logits_stride < V || out_stride < V) return SVW_ERR_INVALID_ARG;
+  // a mask row for each row, named or by its own number
+  if (mask && !mask_row && mask_rows != rows) return SVW_ERR_INVALID_ARG;
+  const int es = esize_of(dtype);
+  if (!aligned(logits, es) || !aligned(out, es) || !aligned(cu_draft, 4) || !aligned(draft_tokens, 4) ||
+      !aligned(history, 4) || !aligned(cu_history, 4) || !aligned(prompt_len, 4) || !aligned(repetition, 4) ||
+      !aligned(frequency, 4) || !aligned(presence, 4) || !aligned(bias_tokens, 4) || !aligned(bias_values, 4) ||
+      !aligned(cu_bias, 4) || !aligned(mask, 4) || !aligned(mask_row, 4) || !aligned(status, 4))
+    return SVW_ERR_MISALIGNED;
+  if (rows == 0) return SVW_OK;  // no drafts and no bonus rows
+  if (rows > INT64_MAX / 8 / std::max(logits_stride, out_stride)) return SVW_ERR_INVALID_ARG;
+  // in place, or apart
+  const char *i0 = static_cast<const char *>(logits), *o0 = static_cast<const char *>(out);
+  const int64_t ib = ((rows - 1) * logits_stride + V) * es, ob = ((rows - 1) * out_stride + V) * es;
+  if (i0 == o0 ? logits_stride != out_stride && rows > 1 : (i0 < o0 ? o0 - i0 < ib : i0 - o0 < ob))
+    return SVW_ERR_INVALID_ARG;
+  svw::AdjustArgs a{};
+  a.logits = logits;
+  a.out = out;
+  a.in_stride = logits_stride;
+  a.out_stride = out_stride;
+  a.V = V;
+  a.N = N;
+  a.cu = cu_draft;
+  a.R = total_draft_rows;
+  a.bonus = has_bonus_row ? 1 : 0;
+  a.tokens = draft_tokens;
+  a.history = history;
+  a.cu_history = cu_history;
+  a.total_history = total_history;
+  a.prompt_len = prompt_len;
+  a.repetition = repetition;
+  a.frequency = frequency;
+  a.presence = presence;
+  a.bias_tokens = bias_tokens;
+  a.bias_values = bias_values;
+  a.cu_bias = cu_bias;
+  a.total_bias = total_bias;
+  a.mask = mask;
+  a.mask_rows = mask_rows;
+  a.mask_words = (static_cast<int64_t>(V) + 31) / 32;
+  a.mask_row = mask_row;
+  a.status = status;
+  return svw::launch_adjust(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SVW_OK : SVW_ERR_CUDA;
+}
+
+// the cache's own fields, checked once for both of its calls
+static svw_status check_cache(const svw_paged_kv *c) {
+  if (!c || !c->k || !c->v || !c->block_table) return SVW_ERR_INVALID_ARG;
+  if (c->n_pages <= 0 || c->page_size <= 0 || c->max_pages <= 0 || c->n_kv_heads <= 0 || c->head_dim <= 0 ||
+      c->table_stride < c->max_pages)
+    return SVW_ERR_INVALID_ARG;
+  for (int d = 0; d < 3; ++d)
+    if (c->k_stride[d] < 0 || c->v_stride[d] < 0) return SVW_ERR_INVALID_ARG;
+  if (!aligned(c->block_table, 4)) return SVW_ERR_MISALIGNED;
+  return SVW_OK;
+}
+
+svw_status kv_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                     int64_t v_token_stride, int64_t v_head_stride, const void *q, int64_t q_token_stride,
+                     int64_t q_head_stride, void *q_out, svw_dtype dtype, int32_t n_q_heads, int32_t N,
+                     const int32_t *cu_new, int64_t total_new, const int32_t *kv_len, const int32_t *positions,
+                     const float *cos_sin, int64_t max_pos, int32_t rot_dim, int32_t interleaved,
+                     const svw_paged_kv *cache, int32_t *status, void *stream) {
+  if (dtype != SVW_F32 && dtype != SVW_BF16) return SVW_ERR_UNSUPPORTED;
+  if (N <= 0 || total_new < 0 || n_q_heads < 0) return SVW_ERR_INVALID_ARG;
+  const svw_status cs = check_cache(cache);
+  if (cs != SVW_OK) return cs;
+  const int es = esize_of(dtype);
+  if (cache->head_dim > 1024 || total_new > INT32_MAX || n_q_heads > 4096 || cache->n_kv_heads > 4096)
+    return SVW_ERR_UNSUPPORTED;
+  if (!cu_new || !kv_len || (total_new > 0 && (!k || !v)) || (q == nullptr) != (q_out == nullptr))
+    return SVW_ERR_INVALID_ARG;
+  if (q && n_q_heads == 0) return SVW_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim % 2 != 0 || rot_dim > cache->head_dim || (rot_dim > 0 && (!cos_sin || max_pos <= 0)))
+    return SVW_ERR_INVALID_ARG;
+  if (k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 || v_head_stride < 0 || q_token_stride < 0 ||
+      q_head_stride < 0)
+    return SVW_ERR_INVALID_ARG;
+  // rotated in place only where every element keeps its place
+  if (q && q == q_out &&
+      (q_head_stride != cache->head_dim || q_token_stride != static_cast<int64_t>(n_q_heads) * cache->head_dim))
+    return SVW_ERR_INVALID_ARG;
+  if (!aligned(k, es) || !aligned(v, es) || !aligned(q, es) || !aligned(q_out, es) || !aligned(cache->k, es) ||
+      !aligned(cache->v, es) || !aligned(cu_new, 4) || !aligned(kv_len, 4) || !aligned(positions, 4) ||
+      !aligned(cos_sin, 4) || !aligned(status, 4))
+    return SVW_ERR_MISALIGNED;
+  if (total_new == 0) return SVW_OK;
+  svw::AppendArgs a{};
+  a.k = k;
+  a.v = v;
+  a.q = q;
+  a.q_out = q_out;
+  a.k_ts = k_token_stride;
+  a.k_hs = k_head_stride;
+  a.v_ts = v_token_stride;
+  a.v_hs = v_head_stride;
+  a.q_ts = q_token_stride;
+  a.q_hs = q_head_stride;
+  a.Hq = q ? n_q_heads : 0;
+  a.Hkv = cache->n_kv_heads;
+  a.D = cache->head_dim;
+  a.N = N;
+  a.cu = cu_new;
+  a.T = total_new;
+  a.kv_len = kv_len;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.max_pos = max_pos;
+  a.rot = rot_dim;
+  a.interleaved = interleaved ? 1 : 0;
+  a.k_cache = cache->k;
+  a.v_cache = cache->v;
+  for (int d = 0; d < 3; ++d) {
+    a.kc[d] = cache->k_stride[d];
+    a.vc[d] = cache->v_stride[d];
+  }
+  a.table = cache->block_table;
+  a.table_stride = cache->table_stride;
+  a.max_pages = cache->max_pages;
+  a.n_pages = cache->n_pages;
+  a.page_size = cache->page_size;
+  a.status = status;
+  return svw::launch_append(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SVW_OK : SVW_ERR_CUDA;
+}
+
+size_t svw_paged_attention_workspace_size(int64_t total_new, int32_t n_q_heads, int32_t n_kv_heads,
+                                          int32_t head_dim) {
+  if (total_new < 0 || n_kv_heads <= 0 || n_q_heads <= 0 || n_q_heads % n_kv_heads != 0 ||
+      n_q_heads / n_kv_heads > 64 || (head_dim != 64 && head_dim != 128))
+    return 0;
+  return svw::attention_workspace(total_new, n_q_heads, n_kv_heads, head_dim);
+}
+
+svw_status paged_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, svw_dtype dtype,
+                           int32_t n_q_heads, int32_t N, const int32_t *cu_new, int64_t total_new,
+                           const int32_t *kv_len, const svw_paged_kv *cache, float scale, int32_t causal,
+                           int32_t window, void *out, float *lse, int32_t *status, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+  if (dtype != SVW_BF16) return SVW_ERR_UNSUPPORTED;
+  if (N <= 0 || total_new < 0 || n_q_heads <= 0) return SVW_ERR_INVALID_ARG;
+  const svw_status cs = check_cache(cache);
+  if (cs != SVW_OK) return cs;
+  const int32_t Hkv = cache->n_kv_heads, D = cache->head_dim, ps = cache->page_size;
+  if (n_q_heads % Hkv != 0) return SVW_ERR_INVALID_ARG;
+  if (n_q_heads / Hkv > 64 || (D != 64 && D != 128) || ps < 16 || ps > 1024 || (ps & (ps - 1)) != 0 ||
+      total_new > INT32_MAX / n_q_heads || static_cast<int64_t>(cache->max_pages) * ps > INT32_MAX)
+    return SVW_ERR_UNSUPPORTED;
+  if (!cu_new || !kv_len || (total_new > 0 && (!q || !out))) return SVW_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale) || window < 0 || (window > 0 && !causal)) return SVW_ERR_INVALID_ARG;
+  if (q_token_stride < 0 || q_head_stride < 0) return SVW_ERR_INVALID_ARG;
+  // the stride of a dimension of one is never used: any multiple of 8 will do
+  svw_paged_kv c = *cache;
+  if (total_new <= 1) q_token_stride = D;
+  if (n_q_heads == 1) q_head_stride = D;
+  if (c.n_pages == 1) c.k_stride[0] = c.v_stride[0] = D;
+  if (c.n_kv_heads == 1) c.k_stride[1] = c.v_stride[1] = D;
+  int64_t odd = q_token_stride | q_head_stride;
+  bool shared = q_token_stride == 0 || q_head_stride == 0;  // a dimension repeated by a stride of zero
+  for (int d = 0; d < 3; ++d) {
+    odd |= c.k_stride[d] | c.v_stride[d];
+    shared |= c.k_stride[d] == 0 || c.v_stride[d] == 0;
+  }
+  if (shared) return SVW_ERR_UNSUPPORTED;
+  if (!aligned(q, 16) || !aligned(cache->k, 16) || !aligned(cache->v, 16) || (odd & 7) || !aligned(out, 16) ||
+      !aligned(lse, 4) || !aligned(cu_new, 4) || !aligned(kv_len, 4) || !aligned(status, 4) ||
+      !aligned(workspace, 256))
+    return SVW_ERR_MISALIGNED;
+  if (total_new == 0) return SVW_OK;
+  if (!workspace || workspace_bytes < svw_paged_attention_workspace_size(total_new, n_q_heads, Hkv, D))
+    return SVW_ERR_WORKSPACE;
+  svw::AttendArgs a{};
+  a.q = q;
+  a.q_ts = q_token_stride;
+  a.q_hs = q_head_stride;
+  a.Hq = n_q_heads;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.N = N;
+  a.cu = cu_new;
+  a.T = total_new;
+  a.kv_len = kv_len;
+  a.k_cache = cache->k;
+  a.v_cache = cache->v;
+  for (int d = 0; d < 3; ++d) {
+    a.kc[d] = c.k_stride[d];
+    a.vc[d] = c.v_stride[d];
+  }
+  a.table = cache->block_table;
+  a.table_stride = cache->table_stride;
+  a.max_pages = cache->max_pages;
+  a.n_pages = cache->n_pages;
+  a.page_size = ps;
+  a.scale = scale;
+  a.causal = causal ? 1 : 0;
+  a.window = window;
+  a.out = out;
+  a.lse = lse;
+  a.status = status;
+  a.ws = workspace;
+  return svw::launch_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SVW_OK : SVW_ERR_CUDA;
+}
+
 }  // extern "C"

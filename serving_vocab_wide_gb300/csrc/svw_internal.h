@@ -209,4 +209,76 @@ cudaError_t launch_opd_fused_fast(const OpdArgs &a, int dtype, int *grid, cudaSt
 constexpr int kFixNone = 0, kFixBoth = 1, kFixParts = 2, kFixGradLast = 3;
 cudaError_t launch_opd_fix(const OpdArgs &a, int dtype, int which, cudaStream_t stream);
 
+// logits_adjust (adjust.cu)
+struct AdjustArgs {
+  const void *logits;
+  void *out;
+  int64_t in_stride, out_stride;  // row pitches in elements
+  int32_t V, N;
+  const int32_t *cu;
+  int64_t R;
+  int32_t bonus;  // 1: verify layout (a bonus row per request)
+  const int32_t *tokens;
+  const int32_t *history, *cu_history;
+  int64_t total_history;
+  const int32_t *prompt_len;
+  const float *repetition, *frequency, *presence;
+  const int32_t *bias_tokens;
+  const float *bias_values;
+  const int32_t *cu_bias;
+  int64_t total_bias;
+  const uint32_t *mask;
+  int64_t mask_rows, mask_words;
+  const int32_t *mask_row;
+  int32_t *status;
+  int32_t chunk_len, chunks, groups;  // set by the launcher
+};
+cudaError_t launch_adjust(const AdjustArgs &a, int dtype, cudaStream_t stream);
+
+// kv_append (append.cu)
+struct AppendArgs {
+  const void *k, *v, *q;
+  void *q_out;
+  int64_t k_ts, k_hs, v_ts, v_hs, q_ts, q_hs;  // token and head strides in elements
+  int32_t Hq, Hkv, D;
+  int32_t N;
+  const int32_t *cu;
+  int64_t T;
+  const int32_t *kv_len, *positions;
+  const float *cos_sin;
+  int64_t max_pos;
+  int32_t rot, interleaved;
+  void *k_cache, *v_cache;
+  int64_t kc[3], vc[3];  // page, head, row strides in elements
+  const int32_t *table;
+  int64_t table_stride;
+  int32_t max_pages, n_pages, page_size;
+  int32_t *status;
+};
+cudaError_t launch_append(const AppendArgs &a, int dtype, cudaStream_t stream);
+
+// paged_attention (attention.cu)
+struct AttendArgs {
+  const void *q;
+  int64_t q_ts, q_hs;
+  int32_t Hq, Hkv, D;
+  int32_t N;
+  const int32_t *cu;
+  int64_t T;
+  const int32_t *kv_len;
+  const void *k_cache, *v_cache;
+  int64_t kc[3], vc[3];
+  const int32_t *table;
+  int64_t table_stride;
+  int32_t max_pages, n_pages, page_size;
+  float scale;
+  int32_t causal, window;
+  void *out;
+  float *lse;
+  int32_t *status;
+  void *ws;
+};
+size_t attention_workspace(int64_t T, int32_t Hq, int32_t Hkv, int32_t D);
+cudaError_t launch_attention(const AttendArgs &a, cudaStream_t stream);
+
 }  // namespace svw
