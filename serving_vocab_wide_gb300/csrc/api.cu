@@ -698,7 +698,7 @@ svw_status paged_attention(const void *q, int64_t q_token_stride, int64_t q_head
   const int32_t Hkv = cache->n_kv_heads, D = cache->head_dim, ps = cache->page_size;
   if (n_q_heads % Hkv != 0) return SVW_ERR_INVALID_ARG;
   if (n_q_heads / Hkv > 64 || (D != 64 && D != 128) || ps < 16 || ps > 1024 || (ps & (ps - 1)) != 0 ||
-      total_new > INT32_MAX / n_q_heads || static_cast<int64_t>(cache->max_pages) * ps > INT32_MAX)
+      total_new > INT32_MAX / n_q_heads || static_cast<int64_t>(cache->max_pages) * ps > (int64_t{1} << 30))
     return SVW_ERR_UNSUPPORTED;
   if (!cu_new || !kv_len || (total_new > 0 && (!q || !out))) return SVW_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale) || window < 0 || (window > 0 && !causal)) return SVW_ERR_INVALID_ARG;

@@ -258,6 +258,12 @@ struct AppendArgs {
 cudaError_t launch_append(const AppendArgs &a, int dtype, cudaStream_t stream);
 
 // paged_attention (attention.cu)
+// the unit that a CTA's last segment begins and does not finish
+struct alignas(16) AttendJoint {
+  int64_t total;  // length of the line of work (for the other CTAs' stretches)
+  int32_t last;   // the CTA that finishes the unit; -1: there is no such unit
+  int32_t tok0, ntok0, ntok1, hk, pad;
+};
 struct AttendArgs {
   const void *q;
   int64_t q_ts, q_hs;
@@ -277,6 +283,12 @@ struct AttendArgs {
   float *lse;
   int32_t *status;
   void *ws;
+  // set by the launcher
+  int32_t tile_tokens;  // tokens of a row tile
+  int32_t part_rows;    // rows of a workspace part
+  AttendJoint *joints;  // [CTAs]
+  float2 *part_ml;      // [2 CTAs][part_rows] reference and sum
+  float *part_o;        // [2 CTAs][part_rows][D] unnormalised output
 };
 size_t attention_workspace(int64_t T, int32_t Hq, int32_t Hkv, int32_t D);
 cudaError_t launch_attention(const AttendArgs &a, cudaStream_t stream);
