@@ -12,6 +12,7 @@ Build the library with ``serving_vocab_wide_gb300.build()`` (nvcc, sm_103a).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -44,6 +45,8 @@ class _PagedKV(ctypes.Structure):
 def lib():
     """The loaded shared library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -443,11 +446,27 @@ def opd_loss(target, draft, temperature: float = 1.0, clip_c: float = 1.0,
     return loss, (dlogits if want_grad else None)
 
 
-def _need_typed(dev, dtype, **ts):
-    """Each given tensor is contiguous, of this type and on this device."""
-    for name, t in ts.items():
-        if t is not None and (t.dtype != dtype or t.device != dev or not t.is_contiguous()):
-            raise SvwError(f"{name} must be a contiguous {dtype} tensor on {dev}")
+def _need_like(index, dtype, names, ts):
+    """Each given tensor is contiguous, of this type and on this GPU."""
+    for name, t in zip(names, ts):
+        if t is not None and (t.dtype != dtype or t.get_device() != index or not t.is_contiguous()):
+            raise SvwError(f"{name} must be a contiguous {dtype} tensor on cuda:{index}")
+
+
+def _need_numel(names, ts, n):
+    for name, t in zip(names, ts):
+        if t is not None and t.numel() != n:
+            raise SvwError(f"{name} must have {n} elements")
+
+
+def _addr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _stream_of(stream, index):
+    """The handle of `stream`, or of the current stream of GPU `index`."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _lent(stream, *ts):
@@ -479,7 +498,7 @@ def logits_adjust(logits, cu_draft, draft_tokens=None, *, history=None, cu_histo
     code = _dtype_code(logits)
     if not logits.is_cuda or logits.dim() != 2 or logits.stride(1) != 1:
         raise SvwError("logits must be a CUDA matrix with contiguous rows")
-    dev = logits.device
+    gpu = logits.get_device()
     rows, V = logits.shape
     N = cu_draft.numel() - 1
     R = int(cu_draft[-1].item()) if total_draft_rows is None else int(total_draft_rows)
@@ -491,35 +510,34 @@ def logits_adjust(logits, cu_draft, draft_tokens=None, *, history=None, cu_histo
         raise SvwError("bias_tokens, bias_values and cu_bias come together")
     if mask is None and mask_row is not None:
         raise SvwError("mask_row comes with a mask")
-    _need_typed(dev, torch.int32, cu_draft=cu_draft, draft_tokens=draft_tokens, history=history,
-                cu_history=cu_history, prompt_len=prompt_len, bias_tokens=bias_tokens, cu_bias=cu_bias, mask=mask,
-                mask_row=mask_row, status=status)
-    _need_typed(dev, torch.float32, repetition=repetition, frequency=frequency, presence=presence,
-                bias_values=bias_values)
-    for name, t, n in (("draft_tokens", draft_tokens, R), ("prompt_len", prompt_len, N), ("repetition", repetition, N),
-                       ("frequency", frequency, N), ("presence", presence, N), ("cu_history", cu_history, N + 1),
-                       ("cu_bias", cu_bias, N + 1), ("mask_row", mask_row, rows)):
-        if t is not None and t.numel() != n:
-            raise SvwError(f"{name} must have {n} elements")
+    _need_like(gpu, torch.int32, ("cu_draft", "draft_tokens", "history", "cu_history", "prompt_len", "bias_tokens",
+                                  "cu_bias", "mask", "mask_row", "status"),
+               (cu_draft, draft_tokens, history, cu_history, prompt_len, bias_tokens, cu_bias, mask, mask_row, status))
+    _need_like(gpu, torch.float32, ("repetition", "frequency", "presence", "bias_values"),
+               (repetition, frequency, presence, bias_values))
+    _need_numel(("prompt_len", "repetition", "frequency", "presence"), (prompt_len, repetition, frequency, presence), N)
+    _need_numel(("cu_history", "cu_bias"), (cu_history, cu_bias), N + 1)
+    _need_numel(("draft_tokens",), (draft_tokens,), R)
+    _need_numel(("mask_row",), (mask_row,), rows)
     if bias_tokens is not None and bias_tokens.numel() != bias_values.numel():
         raise SvwError("bias_tokens and bias_values must have one length")
     if mask is not None and (mask.dim() != 2 or mask.shape[1] != (V + 31) // 32):
         raise SvwError(f"mask must be [mask rows, {(V + 31) // 32}]")
     if out is None:
-        out = torch.empty((rows, V), dtype=logits.dtype, device=dev)
+        out = torch.empty((rows, V), dtype=logits.dtype, device=logits.device)
         _lent(stream, out)
-    elif out.dtype != logits.dtype or out.device != dev or out.shape != logits.shape or out.stride(1) != 1:
+    elif out.dtype != logits.dtype or out.get_device() != gpu or out.shape != logits.shape or out.stride(1) != 1:
         raise SvwError("out must be like logits")
     # a single row has no pitch of its own
     pitch = logits.stride(0) if rows > 1 else V
     out_pitch = out.stride(0) if rows > 1 else V
     rc = lib().logits_adjust(logits.data_ptr(), pitch, code, V, N, cu_draft.data_ptr(), R, 1 if has_bonus else 0,
-                             _ptr(draft_tokens), _ptr(history), _ptr(cu_history),
-                             0 if history is None else history.numel(), _ptr(prompt_len), _ptr(repetition),
-                             _ptr(frequency), _ptr(presence), _ptr(bias_tokens), _ptr(bias_values), _ptr(cu_bias),
-                             0 if bias_tokens is None else bias_tokens.numel(), _ptr(mask),
-                             0 if mask is None else mask.shape[0], _ptr(mask_row), out.data_ptr(), out_pitch,
-                             _ptr(status), _stream_ptr(stream))
+                             _addr(draft_tokens), _addr(history), _addr(cu_history),
+                             0 if history is None else history.numel(), _addr(prompt_len), _addr(repetition),
+                             _addr(frequency), _addr(presence), _addr(bias_tokens), _addr(bias_values), _addr(cu_bias),
+                             0 if bias_tokens is None else bias_tokens.numel(), _addr(mask),
+                             0 if mask is None else mask.shape[0], _addr(mask_row), out.data_ptr(), out_pitch,
+                             _addr(status), _stream_of(stream, gpu))
     _check(rc)
     return out
 
@@ -530,20 +548,21 @@ def _paged(k_cache, v_cache, block_table, N):
     import torch
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
         raise SvwError("k_cache and v_cache must be alike: [n_pages, heads, page_size, head_dim]")
-    if not k_cache.is_cuda or v_cache.device != k_cache.device or k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
+    ks, vs, gpu = k_cache.stride(), v_cache.stride(), k_cache.get_device()
+    if gpu < 0 or v_cache.get_device() != gpu or ks[3] != 1 or vs[3] != 1:
         raise SvwError("the caches must be CUDA tensors with contiguous head vectors")
-    if (block_table.dtype != torch.int32 or block_table.device != k_cache.device or block_table.dim() != 2
+    if (block_table.dtype != torch.int32 or block_table.get_device() != gpu or block_table.dim() != 2
             or block_table.shape[0] != N or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
         raise SvwError(f"block_table must be an int32 [{N}, max_pages] CUDA tensor with contiguous rows")
     pages, heads, size, dim = k_cache.shape
-    ks, vs = k_cache.stride(), v_cache.stride()
     mp = block_table.shape[1]
     return _PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), ks[:3], vs[:3], block_table.data_ptr(),
-                    max(block_table.stride(0), mp) if N > 1 else mp, mp, pages, size, heads, dim)
+                    block_table.stride(0) if N > 1 else mp, mp, pages, size, heads, dim), gpu
 
 
 def _heads(name, t, dim, like):
-    if t.dim() != 3 or t.shape[2] != dim or t.stride(2) != 1 or t.dtype != like.dtype or t.device != like.device:
+    if (t.dim() != 3 or t.shape[2] != dim or t.stride(2) != 1 or t.dtype != like.dtype
+            or t.get_device() != like.get_device()):
         raise SvwError(f"{name} must be [new tokens, heads, {dim}], of the cache's type and device, with contiguous heads")
 
 
@@ -563,16 +582,16 @@ def kv_append(k, v, k_cache, v_cache, block_table, cu_new, kv_len, *, cos_sin=No
     """
     import torch
     N = cu_new.numel() - 1
-    cache = _paged(k_cache, v_cache, block_table, N)
-    dev, T, dim = k_cache.device, k.shape[0], k_cache.shape[3]
+    cache, gpu = _paged(k_cache, v_cache, block_table, N)
+    T, dim = k.shape[0], k_cache.shape[3]
     _heads("k", k, dim, k_cache)
     _heads("v", v, dim, k_cache)
     if k.shape[1] != k_cache.shape[1] or v.shape != k.shape:
         raise SvwError("k and v must have the cache's heads and one length")
-    _need_typed(dev, torch.int32, cu_new=cu_new, kv_len=kv_len, positions=positions, status=status)
-    if kv_len.numel() != N or (positions is not None and positions.numel() != T):
-        raise SvwError(f"kv_len must have {N} elements, positions {T}")
-    _need_typed(dev, torch.float32, cos_sin=cos_sin)
+    _need_like(gpu, torch.int32, ("cu_new", "kv_len", "positions", "status"), (cu_new, kv_len, positions, status))
+    _need_numel(("kv_len",), (kv_len,), N)
+    _need_numel(("positions",), (positions,), T)
+    _need_like(gpu, torch.float32, ("cos_sin",), (cos_sin,))
     if cos_sin is not None and cos_sin.dim() != 2:
         raise SvwError("cos_sin must be [max_pos, rot_dim]")
     qs = (0, 0, 0)
@@ -582,22 +601,24 @@ def kv_append(k, v, k_cache, v_cache, block_table, cu_new, kv_len, *, cos_sin=No
             raise SvwError("q must have as many tokens as k")
         qs = q.stride()
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
             _lent(stream, q_out)
-        elif q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.device != dev or not q_out.is_contiguous():
+        elif (q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.get_device() != gpu
+              or not q_out.is_contiguous()):
             raise SvwError("q_out must be like q, contiguous")
     elif q_out is not None:
         raise SvwError("q_out comes with q")
     ks, vs = k.stride(), v.stride()
-    rc = lib().kv_append(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _ptr(q), qs[0], qs[1], _ptr(q_out),
+    rc = lib().kv_append(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _addr(q), qs[0], qs[1], _addr(q_out),
                          _dtype_code(k_cache), 0 if q is None else q.shape[1], N, cu_new.data_ptr(), T,
-                         kv_len.data_ptr(), _ptr(positions), _ptr(cos_sin),
+                         kv_len.data_ptr(), _addr(positions), _addr(cos_sin),
                          0 if cos_sin is None else cos_sin.shape[0], 0 if cos_sin is None else cos_sin.shape[1],
-                         1 if interleaved else 0, ctypes.byref(cache), _ptr(status), _stream_ptr(stream))
+                         1 if interleaved else 0, ctypes.byref(cache), _addr(status), _stream_of(stream, gpu))
     _check(rc)
     return q_out
 
 
+@functools.lru_cache(maxsize=64)
 def paged_attention_workspace_size(total_new: int, n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
     return int(lib().svw_paged_attention_workspace_size(total_new, n_q_heads, n_kv_heads, head_dim))
 
@@ -617,34 +638,32 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, *, scale: 
     """
     import torch
     N = cu_new.numel() - 1
-    cache = _paged(k_cache, v_cache, block_table, N)
-    dev, dim = k_cache.device, k_cache.shape[3]
+    cache, gpu = _paged(k_cache, v_cache, block_table, N)
+    dim = k_cache.shape[3]
     _heads("q", q, dim, k_cache)
     T, hq, _ = q.shape
-    _need_typed(dev, torch.int32, cu_new=cu_new, kv_len=kv_len, status=status)
-    if kv_len.numel() != N:
-        raise SvwError(f"kv_len must have {N} elements")
+    _need_like(gpu, torch.int32, ("cu_new", "kv_len", "status"), (cu_new, kv_len, status))
+    _need_numel(("kv_len",), (kv_len,), N)
     if out is None:
-        out = torch.empty((T, hq, dim), dtype=q.dtype, device=dev)
+        out = torch.empty((T, hq, dim), dtype=q.dtype, device=q.device)
         _lent(stream, out)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
+    elif out.shape != q.shape or out.dtype != q.dtype or out.get_device() != gpu or not out.is_contiguous():
         raise SvwError("out must be like q, contiguous")
     if lse is None and want_lse:
-        lse = torch.empty((T, hq), dtype=torch.float32, device=dev)
+        lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
         _lent(stream, lse)
-    _need_typed(dev, torch.float32, lse=lse)
-    if lse is not None and lse.numel() != T * hq:
-        raise SvwError(f"lse must be [{T}, {hq}]")
+    _need_like(gpu, torch.float32, ("lse",), (lse,))
+    _need_numel(("lse",), (lse,), T * hq)
     if workspace is None:
         need = paged_attention_workspace_size(T, hq, k_cache.shape[1], dim)
-        workspace = torch.empty(max(1, need), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(max(1, need), dtype=torch.uint8, device=q.device)
         _lent(stream, workspace)
-    _need_cuda(workspace)
+    _need_like(gpu, torch.uint8, ("workspace",), (workspace,))
     qs = q.stride()
     rc = lib().paged_attention(q.data_ptr(), qs[0], qs[1], _dtype_code(q), hq, N, cu_new.data_ptr(), T,
                                kv_len.data_ptr(), ctypes.byref(cache),
                                float(dim ** -0.5 if scale is None else scale), 1 if causal else 0, int(window),
-                               out.data_ptr(), _ptr(lse), _ptr(status), workspace.data_ptr(), workspace.numel(),
-                               _stream_ptr(stream))
+                               out.data_ptr(), _addr(lse), _addr(status), workspace.data_ptr(), workspace.numel(),
+                               _stream_of(stream, gpu))
     _check(rc)
     return out, lse
