@@ -9,16 +9,19 @@
 // Bound by bytes: a row is read and written once, and few of its entries
 // change.  One CTA owns a chunk of the vocabulary of one request: it counts
 // the history's tokens that fall into its chunk in shared memory (32-bit
-// integer atomics: the order does not matter) and marks them, the biased and
-// the drafted ones in a bitmap; then it walks the request's rows over that
-// chunk in 16-byte vectors.  A vector whose entries are all allowed and
-// unmarked is copied (in place: left alone), one whose entries are all masked
-// is written without being read, and only the others are looked at entry by
-// entry.  The drafted prefix differs from row to row and is not counted: the
-// chunk's drafted tokens (at most SVW_MAX_LEN) are kept as a list and compared
-// by the marked entries.  Every chunk of a request reads the whole history
-// (from L2): at 8192 tokens that is 32 KB beside the ~140 KB of logits that
-// a chunk of 4096 entries moves for nine bf16 rows.
+// integer atomics: the order does not matter) and lists them, the biased and
+// the drafted ones, each once.  Then it walks the request's rows over that
+// chunk twice: all entries in 16-byte vectors, copied with the mask applied by
+// selection (a vector that is all masked is written without being read; in
+// place, one that is all allowed is left alone), and after a barrier the
+// listed entries one by one.  (Looking at listed entries inside the first walk
+// cost more: some lane of nearly every warp has one, and 929 us against the
+// two walks' time on the benchmark batch.)  The drafted prefix differs from
+// row to row and is not counted: the chunk's drafted tokens (at most
+// SVW_MAX_LEN) are kept as a list and compared by the listed entries.  Every
+// chunk of a request reads the whole history (from L2): at 8192 tokens that is
+// 32 KB beside the ~140 KB of logits that a chunk of 4096 entries moves for
+// nine bf16 rows.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -66,7 +69,11 @@ template <>
 struct Bits<1> {
   using T = uint16_t;
   static constexpr uint32_t kNegInf = 0xff80u, kNaN = 0x7fffu;
-  static constexpr uint32_t kNegInfWord = 0xff80ff80u;  // 32 bits of the vector
+  // word w of a vector (entries 2 w, 2 w + 1) with the entries whose bit of ok is 0 made -inf
+  __device__ static uint32_t hide(uint32_t x, uint32_t ok, int w) {
+    const uint32_t keep = ((ok >> (2 * w)) & 1u) * 0xffffu + ((ok >> (2 * w + 1)) & 1u) * 0xffff0000u;
+    return (x & keep) | (0xff80ff80u & ~keep);
+  }
   __device__ static float value(uint32_t b) { return __uint_as_float(b << 16); }
   __device__ static uint32_t bits(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 };
@@ -74,7 +81,7 @@ template <>
 struct Bits<0> {
   using T = uint32_t;
   static constexpr uint32_t kNegInf = 0xff800000u, kNaN = 0x7fffffffu;
-  static constexpr uint32_t kNegInfWord = 0xff800000u;
+  __device__ static uint32_t hide(uint32_t x, uint32_t ok, int w) { return ((ok >> w) & 1u) ? x : kNegInf; }
   __device__ static float value(uint32_t b) { return __uint_as_float(b); }
   __device__ static uint32_t bits(float x) { return __float_as_uint(x); }
 };
@@ -94,17 +101,18 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjustArgs a
   constexpr int EPV = 16 / sizeof(T);
   constexpr uint32_t kAll = (1u << EPV) - 1u;
   extern __shared__ int32_t dyn[];
-  __shared__ int32_t dtok[SVW_MAX_LEN], dpos[SVW_MAX_LEN], nd;
+  __shared__ int32_t dtok[SVW_MAX_LEN], dpos[SVW_MAX_LEN], nd, nlist;
   const int tid = threadIdx.x;
   const unsigned item = blockIdx.x / static_cast<unsigned>(a.groups);
   const int group = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.groups));
   const int32_t i = static_cast<int32_t>(item / static_cast<unsigned>(a.chunks));
   const int32_t v0 = static_cast<int32_t>(item % static_cast<unsigned>(a.chunks)) * a.chunk_len;
   const int32_t len = min(a.chunk_len, a.V - v0);
-  // counts | bias places (if any) | bitmap of the entries to look at
+  // counts | bias places (if any) | bitmap of the listed entries | their list
   int32_t *cnt = dyn, *bidx = dyn + a.chunk_len;
   uint32_t *mark = reinterpret_cast<uint32_t *>(dyn + a.chunk_len * (a.cu_bias ? 2 : 1));
   const int mark_words = a.chunk_len / 32;
+  uint16_t *list = reinterpret_cast<uint16_t *>(mark + mark_words);
 
   // the request's offsets and factors, all under way at once
   const int32_t d0 = __ldg(a.cu + i), d1 = __ldg(a.cu + i + 1);
@@ -124,7 +132,7 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjustArgs a
   ch.pres = a.presence ? __ldg(a.presence + i) : 0.f;
   for (int u = tid * 4; u < a.chunk_len * (a.cu_bias ? 2 : 1) + mark_words; u += kAdjThreads * 4)
     *reinterpret_cast<int4 *>(dyn + u) = make_int4(0, 0, 0, 0);
-  if (tid == 0) nd = 0;
+  if (tid == 0) nd = nlist = 0;
   const int64_t L = static_cast<int64_t>(d1) - d0;
   const bool range_ok = d0 >= 0 && L >= 0 && d1 <= a.R && L <= SVW_MAX_LEN;
   if (tid == 0 && a.status && (!range_ok || (i == 0 && d0 != 0) || (i == a.N - 1 && d1 != a.R)))
@@ -137,7 +145,10 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjustArgs a
   bad |= b0 < 0 || b1 < b0 || b1 > a.total_bias;
   if (bad) h1 = h0, b1 = b0;
   __syncthreads();
-  auto look_at = [&](int32_t u) { atomicOr(mark + (u >> 5), 1u << (u & 31)); };
+  auto look_at = [&](int32_t u) {
+    const uint32_t bit = 1u << (u & 31);
+    if (!(atomicOr(mark + (u >> 5), bit) & bit)) list[atomicAdd(&nlist, 1)] = static_cast<uint16_t>(u);
+  };
   {
     auto count = [&](int32_t v, int32_t p) {
       const int32_t u = v - v0;
@@ -207,16 +218,9 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjustArgs a
       continue;
     }
     const uint32_t *mw = (mr >= 0) ? a.mask + static_cast<int64_t>(mr) * a.mask_words : nullptr;
-    auto entry = [&](int u, uint32_t allowed, uint32_t marked, uint32_t x) {
-      if (!allowed) return B::kNegInf;
-      float y = B::value(x);
-      return (marked && adjust_entry(ch, u, j, y)) ? B::bits(y) : x;
-    };
     auto single = [&](int u) {
-      const uint32_t ok = mw ? (__ldg(mw + ((v0 + u) >> 5)) >> ((v0 + u) & 31)) & 1u : 1u;
-      const uint32_t at = (mark[u >> 5] >> (u & 31)) & 1u;
-      if (in_place && ok && !at) return;
-      out[u] = static_cast<T>(entry(u, ok, at, in[u]));
+      const bool ok = !mw || ((__ldg(mw + ((v0 + u) >> 5)) >> ((v0 + u) & 31)) & 1u);
+      if (!(in_place && ok)) out[u] = ok ? in[u] : static_cast<T>(B::kNegInf);
     };
     if (!VEC) {
       for (int u = tid; u < len; u += kAdjThreads) single(u);
@@ -230,43 +234,47 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjustArgs a
     const uint4 *vin = reinterpret_cast<const uint4 *>(in + head);
     uint4 *vout = reinterpret_cast<uint4 *>(out + head);
     for (int k0 = tid; k0 < nvec; k0 += kAdjThreads * kAdjBatch) {
-      uint32_t ok[kAdjBatch], at[kAdjBatch];
+      uint32_t ok[kAdjBatch];
       uint4 x[kAdjBatch];
 #pragma unroll
       for (int q = 0; q < kAdjBatch; ++q) {
-        const int k = k0 + q * kAdjThreads, u = head + k * EPV;
+        const int k = k0 + q * kAdjThreads, v = v0 + head + k * EPV;
         ok[q] = kAll;
-        at[q] = 0;
-        if (k >= nvec) continue;
-        if (mw) {
-          ok[q] = (head == 0) ? (__ldg(mw + ((v0 + u) >> 5)) >> ((v0 + u) & 31)) & kAll
-                              : bits_at(mw, a.mask_words, v0 + u, EPV);
-        }
-        at[q] = (head == 0) ? (mark[u >> 5] >> (u & 31)) & kAll : bits_at(mark, mark_words, u, EPV);
-        at[q] &= ok[q];
-        if (ok[q] != 0 && !(in_place && ok[q] == kAll && at[q] == 0)) x[q] = __ldcs(vin + k);
+        if (mw && k < nvec)
+          ok[q] = (head == 0) ? (__ldg(mw + (v >> 5)) >> (v & 31)) & kAll : bits_at(mw, a.mask_words, v, EPV);
       }
 #pragma unroll
       for (int q = 0; q < kAdjBatch; ++q) {
-        const int k = k0 + q * kAdjThreads, u = head + k * EPV;
-        if (k >= nvec || (in_place && ok[q] == kAll && at[q] == 0)) continue;
-        if (ok[q] == 0) {
-          x[q] = make_uint4(B::kNegInfWord, B::kNegInfWord, B::kNegInfWord, B::kNegInfWord);
-        } else if (ok[q] != kAll || at[q] != 0) {
-          uint32_t w[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+        const int k = k0 + q * kAdjThreads;
+        if (k < nvec && ok[q] != 0 && !(in_place && ok[q] == kAll)) x[q] = __ldcs(vin + k);
+      }
 #pragma unroll
-          for (int e = 0; e < EPV; ++e) {
-            constexpr int kPer = 4 / sizeof(T);  // entries of a word
-            const int sh = (e % kPer) * 16;
-            const uint32_t old = (kPer == 2) ? (w[e / kPer] >> sh) & 0xffffu : w[e / kPer];
-            const uint32_t now = entry(u + e, (ok[q] >> e) & 1u, (at[q] >> e) & 1u, old);
-            w[e / kPer] = (kPer == 2) ? (w[e / kPer] & ~(0xffffu << sh)) | (now << sh) : now;
-          }
-          x[q] = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int q = 0; q < kAdjBatch; ++q) {
+        const int k = k0 + q * kAdjThreads;
+        if (k >= nvec || (in_place && ok[q] == kAll)) continue;
+        if (ok[q] != kAll) {
+          x[q].x = B::hide(x[q].x, ok[q], 0);
+          x[q].y = B::hide(x[q].y, ok[q], 1);
+          x[q].z = B::hide(x[q].z, ok[q], 2);
+          x[q].w = B::hide(x[q].w, ok[q], 3);
         }
         __stcs(vout + k, x[q]);
       }
     }
+  }
+  if (bad || nlist == 0) return;
+  __syncthreads();  // the listed entries are written again after their vectors
+  const int n = nlist, mine = (rows - group + a.groups - 1) / a.groups;  // this CTA's rows
+  for (int m = tid; m < n * mine; m += kAdjThreads) {
+    const int q = m / n, u = list[m - q * n], j = group + q * a.groups;
+    const int64_t r = row0 + j;
+    const int32_t mr = a.mask ? (a.mask_row ? __ldg(a.mask_row + r) : static_cast<int32_t>(r)) : -1;
+    if (mr < -1 || (mr >= 0 && mr >= a.mask_rows)) continue;  // a bad row: NaN
+    if (mr >= 0 && !((__ldg(a.mask + static_cast<int64_t>(mr) * a.mask_words + ((v0 + u) >> 5)) >> ((v0 + u) & 31)) & 1u))
+      continue;  // masked: -inf
+    float y = B::value((reinterpret_cast<const T *>(a.logits) + r * a.in_stride + v0)[u]);
+    if (adjust_entry(ch, u, j, y))
+      (reinterpret_cast<T *>(a.out) + r * a.out_stride + v0)[u] = static_cast<T>(B::bits(y));
   }
 }
 
@@ -275,7 +283,7 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjustArgs a
 cudaError_t launch_adjust(const AdjustArgs &args, int dtype, cudaStream_t st) {
   AdjustArgs a = args;
   const int es = dtype == SVW_BF16 ? 2 : 4;
-  // 4096 entries a chunk (33 KB of shared memory with biases: six CTAs per SM);
+  // 4096 entries a chunk (41 KB of shared memory with biases: five CTAs per SM);
   // fewer where the batch would leave SMs without work, then the rows of a
   // request are shared out too
   constexpr int64_t kFull = 2 * 152;
@@ -287,7 +295,7 @@ cudaError_t launch_adjust(const AdjustArgs &args, int dtype, cudaStream_t st) {
   a.groups = static_cast<int32_t>(want < 1 ? 1 : (want > rows ? (rows < 1 ? 1 : rows) : want));
   const int64_t grid = static_cast<int64_t>(a.N) * a.chunks * a.groups;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  const size_t smem = static_cast<size_t>(a.chunk_len) * 4 * (a.cu_bias ? 2 : 1) + a.chunk_len / 8;
+  const size_t smem = static_cast<size_t>(a.chunk_len) * (4 * (a.cu_bias ? 2 : 1) + 2) + a.chunk_len / 8;
   const uintptr_t apart = reinterpret_cast<uintptr_t>(a.logits) - reinterpret_cast<uintptr_t>(a.out);
   const bool vec = (apart & 15u) == 0 && ((a.in_stride - a.out_stride) * es) % 16 == 0;
   void *tm = timer_before("logits_adjust", st);
