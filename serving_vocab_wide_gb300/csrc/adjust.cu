@@ -10,11 +10,12 @@
 // change.  One CTA owns a chunk of the vocabulary of one request: it counts
 // the history's tokens that fall into its chunk in shared memory (32-bit
 // integer atomics: the order does not matter) and lists them, the biased and
-// the drafted ones, each once.  Then it walks the request's rows over that
-// chunk twice: all entries in 16-byte vectors, copied with the mask applied by
+// the drafted ones, each once.  It walks the request's rows over that chunk
+// twice: all entries in 16-byte vectors, copied with the mask applied by
 // selection (a vector that is all masked is written without being read; in
-// place, one that is all allowed is left alone), and after a barrier the
-// listed entries one by one.  (Looking at listed entries inside the first walk
+// place, one that is all allowed is left alone), and, once the history is
+// counted, the listed entries one by one.  A thread keeps four vectors under
+// way, of several rows where the chunk is short.  (Looking at listed entries inside the first walk
 // cost more: some lane of nearly every warp has one, and 929 us against the
 // two walks' time on the benchmark batch.)  The drafted prefix differs from
 // row to row and is not counted: the chunk's drafted tokens (at most
@@ -35,7 +36,9 @@ namespace svw {
 namespace {
 
 constexpr int kAdjThreads = 256;
-constexpr int kAdjBatch = 4;  // vectors of a thread in flight
+constexpr int kAdjBatch = 4;  // vectors of a thread under way
+constexpr int kAhead = 8;     // history tokens of a thread under way
+constexpr uint32_t kNothing = 0x100;  // no vector to write
 constexpr int32_t kPromptBit = static_cast<int32_t>(0x80000000u);
 
 // what a CTA knows of its request and chunk
@@ -93,15 +96,18 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t *map, int64_t words, 
   return __funnelshift_r(lo, hi, static_cast<uint32_t>(at & 31)) & ((1u << count) - 1u);
 }
 
-// VEC: the two rows of every row pair lie equally far from a 16-byte boundary
-template <int DT, bool VEC>
-__global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjustArgs a) {
+// kRowVecs: vectors of a chunk's row per thread; 0: the input and output rows
+// do not lie equally far from a 16-byte boundary, entry by entry
+template <int DT, int kRowVecs>
+__global__ void __launch_bounds__(kAdjThreads, 4) logits_adjust_kernel(AdjustArgs a) {
+  constexpr bool VEC = kRowVecs > 0;
   using B = Bits<DT>;
   using T = typename B::T;
   constexpr int EPV = 16 / sizeof(T);
   constexpr uint32_t kAll = (1u << EPV) - 1u;
   extern __shared__ int32_t dyn[];
   __shared__ int32_t dtok[SVW_MAX_LEN], dpos[SVW_MAX_LEN], nd, nlist;
+  __shared__ int32_t mask_of[SVW_MAX_LEN + 1];  // mask row of each of this CTA's rows; -1: none, -2: a bad row
   const int tid = threadIdx.x;
   const unsigned item = blockIdx.x / static_cast<unsigned>(a.groups);
   const int group = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.groups));
@@ -138,13 +144,94 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjustArgs a
   if (tid == 0 && a.status && (!range_ok || (i == 0 && d0 != 0) || (i == a.N - 1 && d1 != a.R)))
     atomicOr(a.status, SVW_DEV_BAD_INPUT);
   if (!range_ok) return;
-  const int rows = static_cast<int>(L) + a.bonus;
-  const int64_t row0 = static_cast<int64_t>(d0) + (a.bonus ? i : 0);
+  // this CTA's rows: group, group + groups, ... of the request's
+  const int rows = (static_cast<int>(L) + a.bonus - group + a.groups - 1) / a.groups;
+  const int64_t row0 = static_cast<int64_t>(d0) + (a.bonus ? i : 0) + group;
+  if (tid < rows) {
+    const int64_t r = row0 + static_cast<int64_t>(tid) * a.groups;
+    const int32_t m = a.mask ? (a.mask_row ? __ldg(a.mask_row + r) : static_cast<int32_t>(r)) : -1;
+    const bool row_bad = m < -1 || (m >= 0 && m >= a.mask_rows);
+    mask_of[tid] = row_bad ? -2 : m;
+    if (row_bad && a.status) atomicOr(a.status, SVW_DEV_BAD_INPUT);
+  }
   bool bad = !(ch.rep > 0.f && ch.rep < INFINITY && fabsf(ch.freq) < INFINITY && fabsf(ch.pres) < INFINITY);
   bad |= h0 < 0 || h1 < h0 || h1 > a.total_history || pl < 0 || pl > h1 - h0;
   bad |= b0 < 0 || b1 < b0 || b1 > a.total_bias;
   if (bad) h1 = h0, b1 = b0;
+  const int32_t *hist = a.history + h0;
+  const int32_t hn = h1 - h0;
   __syncthreads();
+
+  // ---- every entry: copied, masked ----
+
+  const bool in_place = (a.out == a.logits);
+  const T *in = reinterpret_cast<const T *>(a.logits) + row0 * a.in_stride + v0;
+  T *out = reinterpret_cast<T *>(a.out) + row0 * a.out_stride + v0;
+  const int64_t in_step = a.in_stride * a.groups, out_step = a.out_stride * a.groups;
+  auto words_of = [&](int32_t m) { return a.mask + static_cast<int64_t>(m) * a.mask_words; };
+  auto allowed = [&](int32_t m, int32_t v) { return m < 0 || ((__ldg(words_of(m) + (v >> 5)) >> (v & 31)) & 1u); };
+  auto single = [&](int q, int u) {
+    const bool ok = allowed(mask_of[q], v0 + u);
+    if (!(in_place && ok)) out[q * out_step + u] = ok ? in[q * in_step + u] : static_cast<T>(B::kNegInf);
+  };
+  // entries of row q before its first 16-byte boundary
+  auto head_of = [&](int q) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(in + q * in_step) & 15u;
+    return min(len, static_cast<int>(((16u - at) & 15u) / sizeof(T)));
+  };
+  if (!VEC) {
+    for (int q = 0; q < rows; ++q)
+      for (int u = tid; u < len; u += kAdjThreads) single(q, u);
+  } else {
+    // kRowVecs vectors of a row per thread, kAdjBatch / kRowVecs rows at a time
+    constexpr int kPerRow = VEC ? kRowVecs : 1, kRowsAtOnce = kAdjBatch / kPerRow;
+    for (int q0 = 0; q0 < rows; q0 += kRowsAtOnce) {
+      uint32_t ok[kAdjBatch];
+      uint4 x[kAdjBatch];
+#pragma unroll
+      for (int b = 0; b < kAdjBatch; ++b) {
+        const int q = q0 + b / kPerRow, k = tid + (b % kPerRow) * kAdjThreads;
+        ok[b] = kNothing;
+        if (q < rows) {
+          const int head = head_of(q), v = v0 + head + k * EPV;
+          if (head + (k + 1) * EPV <= len) {
+            const int32_t m = mask_of[q];
+            ok[b] = kAll;
+            if (m >= 0)
+              ok[b] = (head == 0) ? (__ldg(words_of(m) + (v >> 5)) >> (v & 31)) & kAll
+                                  : bits_at(words_of(m), a.mask_words, v, EPV);
+            if (in_place && ok[b] == kAll) ok[b] = kNothing;
+          }
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kAdjBatch; ++b) {
+        const int q = q0 + b / kPerRow, k = tid + (b % kPerRow) * kAdjThreads;
+        if (ok[b] != 0 && ok[b] != kNothing) x[b] = *(reinterpret_cast<const uint4 *>(in + q * in_step + head_of(q)) + k);
+      }
+#pragma unroll
+      for (int b = 0; b < kAdjBatch; ++b) {
+        const int q = q0 + b / kPerRow, k = tid + (b % kPerRow) * kAdjThreads;
+        if (ok[b] == kNothing) continue;
+        if (ok[b] != kAll) {
+          x[b].x = B::hide(x[b].x, ok[b], 0);
+          x[b].y = B::hide(x[b].y, ok[b], 1);
+          x[b].z = B::hide(x[b].z, ok[b], 2);
+          x[b].w = B::hide(x[b].w, ok[b], 3);
+        }
+        *(reinterpret_cast<uint4 *>(out + q * out_step + head_of(q)) + k) = x[b];
+      }
+    }
+    // what lies before the first and after the last boundary of each row
+    for (int m = tid; m < rows * 2 * EPV; m += kAdjThreads) {
+      const int r = m / (2 * EPV), e = m % (2 * EPV), head = head_of(r);
+      const int tail = head + (len - head) / EPV * EPV;
+      if (e < EPV ? e < head : tail + e - EPV < len) single(r, e < EPV ? e : tail + e - EPV);
+    }
+  }
+
+  // ---- what the request has seen of the chunk ----
+
   auto look_at = [&](int32_t u) {
     const uint32_t bit = 1u << (u & 31);
     if (!(atomicOr(mark + (u >> 5), bit) & bit)) list[atomicAdd(&nlist, 1)] = static_cast<uint16_t>(u);
@@ -162,22 +249,20 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjustArgs a
         look_at(u);
       }
     };
-    const int32_t *hist = a.history + h0;
-    const int32_t n = h1 - h0;
-    int32_t p = tid;
-    for (; p + 3 * kAdjThreads < n; p += 4 * kAdjThreads) {
-      int32_t v[4];
+    for (int32_t p0 = tid; p0 < hn; p0 += kAhead * kAdjThreads) {
+      int32_t ahead[kAhead];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = __ldg(hist + p + q * kAdjThreads);
+      for (int q = 0; q < kAhead; ++q) ahead[q] = (p0 + q * kAdjThreads < hn) ? __ldg(hist + p0 + q * kAdjThreads) : 0;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) count(v[q], p + q * kAdjThreads);
+      for (int q = 0; q < kAhead; ++q)
+        if (p0 + q * kAdjThreads < hn) count(ahead[q], p0 + q * kAdjThreads);
     }
-    for (; p < n; p += kAdjThreads) count(__ldg(hist + p), p);
   }
   for (int32_t p = b0 + tid; p < b1; p += kAdjThreads) {
-    const int32_t v = __ldg(a.bias_tokens + p);
-    const int32_t u = v - v0;
-    if (static_cast<uint32_t>(v) >= static_cast<uint32_t>(a.V) || !(__ldg(a.bias_values + p) < INFINITY))
+    const int32_t bias_v = __ldg(a.bias_tokens + p);
+    const float bias_x = __ldg(a.bias_values + p);
+    const int32_t u = bias_v - v0;
+    if (static_cast<uint32_t>(bias_v) >= static_cast<uint32_t>(a.V) || !(bias_x < INFINITY))
       bad = true;
     else if (u >= 0 && u < len) {
       atomicMax(bidx + u, p + 1);
@@ -185,9 +270,9 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjustArgs a
     }
   }
   if (tid < static_cast<int>(L)) {
-    const int32_t v = __ldg(a.tokens + d0 + tid);
-    const int32_t u = v - v0;
-    if (static_cast<uint32_t>(v) >= static_cast<uint32_t>(a.V))
+    const int32_t draft = __ldg(a.tokens + d0 + tid);
+    const int32_t u = draft - v0;
+    if (static_cast<uint32_t>(draft) >= static_cast<uint32_t>(a.V))
       bad = true;
     else if (u >= 0 && u < len) {
       const int s = atomicAdd(&nd, 1);
@@ -196,85 +281,44 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjustArgs a
       look_at(u);
     }
   }
-  bad = __syncthreads_or(bad);
+  bad = __syncthreads_or(bad);  // also: every vector is written
   if (bad && tid == 0 && a.status) atomicOr(a.status, SVW_DEV_BAD_INPUT);
+
+  // ---- the listed entries again, or a bad request's or row's NaN ----
+  for (int q = 0; q < rows; ++q)
+    if (bad || mask_of[q] == -2)
+      for (int u = tid; u < len; u += kAdjThreads) out[q * out_step + u] = static_cast<T>(B::kNaN);
+  if (bad) return;
   ch.cnt = cnt;
   ch.bidx = a.cu_bias ? bidx : nullptr;
   ch.bias_values = a.bias_values;
   ch.nd = nd;
   ch.dtok = dtok;
   ch.dpos = dpos;
-
-  const bool in_place = (a.out == a.logits);
-  for (int j = group; j < rows; j += a.groups) {
-    const int64_t r = row0 + j;
-    const T *in = reinterpret_cast<const T *>(a.logits) + r * a.in_stride + v0;
-    T *out = reinterpret_cast<T *>(a.out) + r * a.out_stride + v0;
-    const int32_t mr = a.mask ? (a.mask_row ? __ldg(a.mask_row + r) : static_cast<int32_t>(r)) : -1;
-    const bool row_bad = mr < -1 || (mr >= 0 && mr >= a.mask_rows);
-    if (row_bad && tid == 0 && a.status) atomicOr(a.status, SVW_DEV_BAD_INPUT);
-    if (bad || row_bad) {
-      for (int u = tid; u < len; u += kAdjThreads) out[u] = static_cast<T>(B::kNaN);
-      continue;
-    }
-    const uint32_t *mw = (mr >= 0) ? a.mask + static_cast<int64_t>(mr) * a.mask_words : nullptr;
-    auto single = [&](int u) {
-      const bool ok = !mw || ((__ldg(mw + ((v0 + u) >> 5)) >> ((v0 + u) & 31)) & 1u);
-      if (!(in_place && ok)) out[u] = ok ? in[u] : static_cast<T>(B::kNegInf);
-    };
-    if (!VEC) {
-      for (int u = tid; u < len; u += kAdjThreads) single(u);
-      continue;
-    }
-    // the row's entries before its first 16-byte boundary and after its last
-    const int head = min(len, static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(in) & 15u)) & 15u) / sizeof(T)));
-    const int nvec = (len - head) / EPV;
-    if (tid < head) single(tid);
-    if (tid < len - head - nvec * EPV) single(head + nvec * EPV + tid);
-    const uint4 *vin = reinterpret_cast<const uint4 *>(in + head);
-    uint4 *vout = reinterpret_cast<uint4 *>(out + head);
-    for (int k0 = tid; k0 < nvec; k0 += kAdjThreads * kAdjBatch) {
-      uint32_t ok[kAdjBatch];
-      uint4 x[kAdjBatch];
+  const int n = nlist;
+  constexpr int kMany = 4;
+  for (int m0 = tid; m0 < n * rows; m0 += kMany * kAdjThreads) {
+    uint32_t x[kMany];
+    int qs[kMany], us[kMany];
 #pragma unroll
-      for (int q = 0; q < kAdjBatch; ++q) {
-        const int k = k0 + q * kAdjThreads, v = v0 + head + k * EPV;
-        ok[q] = kAll;
-        if (mw && k < nvec)
-          ok[q] = (head == 0) ? (__ldg(mw + (v >> 5)) >> (v & 31)) & kAll : bits_at(mw, a.mask_words, v, EPV);
-      }
-#pragma unroll
-      for (int q = 0; q < kAdjBatch; ++q) {
-        const int k = k0 + q * kAdjThreads;
-        if (k < nvec && ok[q] != 0 && !(in_place && ok[q] == kAll)) x[q] = __ldcs(vin + k);
-      }
-#pragma unroll
-      for (int q = 0; q < kAdjBatch; ++q) {
-        const int k = k0 + q * kAdjThreads;
-        if (k >= nvec || (in_place && ok[q] == kAll)) continue;
-        if (ok[q] != kAll) {
-          x[q].x = B::hide(x[q].x, ok[q], 0);
-          x[q].y = B::hide(x[q].y, ok[q], 1);
-          x[q].z = B::hide(x[q].z, ok[q], 2);
-          x[q].w = B::hide(x[q].w, ok[q], 3);
+    for (int b = 0; b < kMany; ++b) {
+      const int m = m0 + b * kAdjThreads;
+      qs[b] = -1;
+      if (m < n * rows) {
+        const int q = m / n, u = list[m - q * n];
+        if (mask_of[q] != -2 && allowed(mask_of[q], v0 + u)) {
+          qs[b] = q;
+          us[b] = u;
+          x[b] = in[q * in_step + u];
         }
-        __stcs(vout + k, x[q]);
       }
     }
-  }
-  if (bad || nlist == 0) return;
-  __syncthreads();  // the listed entries are written again after their vectors
-  const int n = nlist, mine = (rows - group + a.groups - 1) / a.groups;  // this CTA's rows
-  for (int m = tid; m < n * mine; m += kAdjThreads) {
-    const int q = m / n, u = list[m - q * n], j = group + q * a.groups;
-    const int64_t r = row0 + j;
-    const int32_t mr = a.mask ? (a.mask_row ? __ldg(a.mask_row + r) : static_cast<int32_t>(r)) : -1;
-    if (mr < -1 || (mr >= 0 && mr >= a.mask_rows)) continue;  // a bad row: NaN
-    if (mr >= 0 && !((__ldg(a.mask + static_cast<int64_t>(mr) * a.mask_words + ((v0 + u) >> 5)) >> ((v0 + u) & 31)) & 1u))
-      continue;  // masked: -inf
-    float y = B::value((reinterpret_cast<const T *>(a.logits) + r * a.in_stride + v0)[u]);
-    if (adjust_entry(ch, u, j, y))
-      (reinterpret_cast<T *>(a.out) + r * a.out_stride + v0)[u] = static_cast<T>(B::bits(y));
+#pragma unroll
+    for (int b = 0; b < kMany; ++b) {
+      if (qs[b] < 0) continue;
+      float y = B::value(x[b]);
+      if (adjust_entry(ch, us[b], group + qs[b] * a.groups, y)) out[qs[b] * out_step + us[b]] = static_cast<T>(B::bits(y));
+    }
   }
 }
 
@@ -300,17 +344,26 @@ cudaError_t launch_adjust(const AdjustArgs &args, int dtype, cudaStream_t st) {
   const bool vec = (apart & 15u) == 0 && ((a.in_stride - a.out_stride) * es) % 16 == 0;
   void *tm = timer_before("logits_adjust", st);
   const dim3 g(static_cast<unsigned>(grid)), b(kAdjThreads);
+  const int row_vecs = vec ? (a.chunk_len * es / 16 + kAdjThreads - 1) / kAdjThreads : 0;  // 0, 1, 2 or 4
+#define SVW_ADJUST(DT, RV) logits_adjust_kernel<DT, RV><<<g, b, smem, st>>>(a)
   if (dtype == SVW_BF16) {
-    if (vec)
-      logits_adjust_kernel<1, true><<<g, b, smem, st>>>(a);
+    if (row_vecs == 0)
+      SVW_ADJUST(1, 0);
+    else if (row_vecs == 1)
+      SVW_ADJUST(1, 1);
     else
-      logits_adjust_kernel<1, false><<<g, b, smem, st>>>(a);
+      SVW_ADJUST(1, 2);
   } else {
-    if (vec)
-      logits_adjust_kernel<0, true><<<g, b, smem, st>>>(a);
+    if (row_vecs == 0)
+      SVW_ADJUST(0, 0);
+    else if (row_vecs == 1)
+      SVW_ADJUST(0, 1);
+    else if (row_vecs == 2)
+      SVW_ADJUST(0, 2);
     else
-      logits_adjust_kernel<0, false><<<g, b, smem, st>>>(a);
+      SVW_ADJUST(0, 4);
   }
+#undef SVW_ADJUST
   timer_after(tm, st);
   return cudaGetLastError();
 }
