@@ -7,28 +7,38 @@
 // lse = log sum_j exp(scale q . k_j).
 //
 // Work.  The G = n_q_heads / n_kv_heads query heads of a key head share its
-// keys, so the rows of a tile are (token, head of the group) pairs: a unit is
-// (request, up to two tiles of 128 rows, key head), and its keys are cut into
-// tiles of 128.  All units' key tiles form one line, in a fixed order, that
-// the CTAs (one per SM) share out evenly: lengths may be as ragged as they
-// like, and one long request fills the GPU.  A CTA walks its stretch of the
-// line unit by unit ("segments"); a unit that several CTAs share is left as
-// partial results in the workspace (unnormalised output, reference and sum of
-// each row) and joined by attention_join, in the order of the line, so results
-// do not depend on timing.
+// keys, so the rows of a tile are (token, head of the group) pairs, 128 of
+// them (the tensor core's M).  A unit is (request, row tile or pair of row
+// tiles, key head), and its keys are cut into tiles.  All units' key tiles form
+// one line, in a fixed order, that the workers share out evenly: lengths may
+// be as ragged as they like, and one long request fills the GPU.  A worker
+// walks its stretch of the line unit by unit ("segments"); a unit that several
+// workers share is left as partial results in the workspace (unnormalised
+// output, reference and sum of each row) and joined by attention_join, in the
+// order of the line, so results do not depend on timing.
 //
-// A CTA.  One warp loads (TMA: queries once per segment, each page's keys and
-// values as 128-byte-swizzled boxes into a ring), one thread issues the
-// products on the tensor cores (tcgen05.mma, fp32 accumulators in tensor
-// memory), two warpgroups ("stages") do the softmax, each with a score tile
-// and an output accumulator of its own, so that one's exponentials run beside
-// the other's products.  With two row tiles, stage s owns tile s and both
-// read the same keys; with one, the stages take alternate key tiles and their
-// two accumulators are added at the end.
-//   scores  S[128 rows, 128 keys] = Q K^T, both K-major from shared memory;
-//   softmax a thread per row: running reference M and sum l in base 2;
+// A CTA (one per SM) has two stages, each with a score tile and an output
+// accumulator in tensor memory and softmax warps of its own, so that one's
+// exponentials run beside the other's products.  Per worker one warp loads
+// (TMA: queries once per segment, each page's keys and values as
+// 128-byte-swizzled boxes into a ring) and one thread issues the products
+// (tcgen05.mma, fp32 accumulators in tensor memory):
+//   scores  S[128 rows, keys] = Q K^T, both K-major from shared memory;
+//   softmax running reference M and sum l of each row in base 2;
 //   output  O[128 rows, D] += P V with P (bf16) written over S in tensor
 //           memory and V read as it lies, keys along K (MN-major).
+// Two ways to use the stages, by the rows that a request brings on average:
+//   narrow  (up to 128: decoding, verifying; bound by the bytes of the keys) a
+//           stage is a worker: its own units, its own loads, key tiles of 64,
+//           two score buffers so that the next scores are there when a softmax
+//           ends.  Small tiles keep bytes in flight while values wait for their
+//           weights: with key tiles of 128 shared by the stages (alternating)
+//           the ring held 160 KB of which two slots were under way, 2.0 us a
+//           tile against 1.47 us of its bytes' time.
+//   wide    (more: prompts; bound by the products) the CTA is one worker, a unit
+//           is two row tiles, one a stage, reading the same key tiles of 128;
+//           two threads share a row, 64 keys each, and exchange their maxima
+//           through shared memory.
 // The reference: exp2(x - M) is exact algebra for any M, so M follows the
 // row's maximum only when that has outgrown it by more than 8 (a factor 256:
 // far from overflow, and the same relative rounding of P); only then are l
@@ -55,29 +65,39 @@ namespace svw {
 namespace {
 
 constexpr int kRows = 128;     // rows of a score tile (the MMA's M)
-constexpr int kKeys = 128;     // keys of a tile
-constexpr int kThreads = 384;  // loader, MMA issuer, two idle warps; two softmax warpgroups
-constexpr int kSoftWarps = 8;
+constexpr int kCols = 64;      // keys of a softmax thread
 constexpr int kSegRing = 4;
-constexpr int kMaxGrid = 152;   // CTAs: one per SM
-constexpr int kUnitCost = 1;    // a unit's fixed cost on the line, in key tiles
-constexpr float kGrow = 8.f;    // the reference lags the maximum by at most this (base 2)
+constexpr int kMaxGrid = 152;  // CTAs: one per SM
+constexpr float kGrow = 8.f;   // the reference lags the maximum by at most this (base 2)
 constexpr float kNaN = __builtin_nanf("");
 
-template <int D>
+template <int D, bool kWide>
 struct Shape {
-  static constexpr int kHalves = D / 64;                // 128-byte columns of a tile
-  static constexpr int kTile = kRows * D * 2;           // bytes of a query, key or value tile
-  static constexpr int kHalf = kRows * 128;             // bytes of one of its halves
-  static constexpr int kRing = (D == 128) ? 5 : 12;     // key and value tiles in flight
+  static constexpr int kWorkers = kWide ? 1 : 2;           // of a CTA
+  static constexpr int kKeys = kWide ? 128 : 64;           // keys of a tile
+  static constexpr int kTiles = kWide ? 2 : 1;             // row tiles of a unit, at most
+  static constexpr int kGroups = kWide ? 2 : 1;            // softmax warpgroups of a stage
+  static constexpr int kSoftWarps = 4 * kGroups * (kWide ? 2 : 1);  // softmax warps of a worker
+  static constexpr int kThreads = 128 + 256 * kGroups;     // loaders and issuers; softmax
+  static constexpr int kUnitCost = kWide ? 1 : 2;          // a unit's fixed cost on the line, in key tiles
+  static constexpr int kHalves = D / 64;                   // 128-byte columns of a tile
+  static constexpr int kQTile = kRows * D * 2;             // bytes of a query tile
+  static constexpr int kQHalf = kRows * 128;               // bytes of one of its columns
+  static constexpr int kTile = kKeys * D * 2;              // of a key or value tile
+  static constexpr int kHalf = kKeys * 128;
+  static constexpr int kRing = (D == 128) ? 5 : 11;        // key and value tiles in flight of a worker
+  static constexpr int kControl = (D == 128) ? 3072 : 4096;
+  static constexpr int kSmem = kControl + 2 * kQTile + kWorkers * kRing * kTile;
 };
+static_assert(Shape<128, true>::kSmem <= 232448 && Shape<128, false>::kSmem <= 232448, "shared memory");
+static_assert(Shape<64, true>::kSmem <= 232448 && Shape<64, false>::kSmem <= 232448, "shared memory");
 
 // one stretch of a unit
 struct Segment {
-  int32_t tiles;   // key tiles (0: the end of the CTA's work)
+  int32_t tiles;   // key tiles (0: the end of the worker's stretch)
   int32_t tok0;    // first token of row tile 0
   int32_t ntok0;   // tokens of row tile 0
-  int32_t ntok1;   // tokens of row tile 1 (0: one row tile, stages alternate)
+  int32_t ntok1;   // tokens of row tile 1
   int32_t pos0;    // place of tok0
   int32_t key0;    // first key of the segment
   int32_t kv;      // keys of the request
@@ -85,24 +105,27 @@ struct Segment {
   int32_t part;    // workspace part (-1: the unit is complete)
 };
 
-struct Control {
-  unsigned long long full[12], empty[12];
-  unsigned long long q_full[2], q_empty[2];
-  unsigned long long s_full[2], p_full[2];
-  unsigned long long o_full, o_free;
+template <int kRing>
+struct Lane {  // of a worker
+  unsigned long long full[kRing], empty[kRing];
   unsigned long long seg_full[kSegRing], seg_empty[kSegRing];
+  unsigned long long o_full, o_free, o_step;
   Segment seg[kSegRing];
   int32_t seg_bad[kSegRing];
-  uint32_t tmem;
-  int32_t err;
-  int64_t total, scan[kThreads / 32];
+  int32_t issued, q_issued;  // ring tiles, query tiles
   int32_t first_req;
   int64_t first_at;
-  int32_t issued, q_issued;  // ring tiles, query tiles
-  float2 ml[2][kRows];       // reference and sum of each stage's rows
 };
-constexpr int kControlBytes = 3072;
-static_assert(sizeof(Control) <= kControlBytes, "control block");
+template <int kRing, int kWorkers>
+struct Control {
+  Lane<kRing> lane[kWorkers];
+  unsigned long long q_full[2], q_empty[2];
+  unsigned long long s_full[4], p_full[4];  // by score buffer: stage, or 2 * worker + buffer
+  uint32_t tmem;
+  int32_t err;
+  int64_t scan[20];
+  float row[kWorkers == 1 ? 2 : 1][2][kWorkers == 1 ? kRows : 1];  // what the two threads of a row tell each other
+};
 
 using Joint = AttendJoint;
 
@@ -156,24 +179,28 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *r) {
         "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float *r) {
-  const uint32_t *u = reinterpret_cast<const uint32_t *>(r);
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float *r) {
+  uint32_t *u = reinterpret_cast<uint32_t *>(r);
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
-      "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]),
-      "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]),
-      "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+      : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *u) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float *r) {
+  const uint32_t *u = reinterpret_cast<const uint32_t *>(r);
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
       "%15, %16};" ::"r"(taddr),
       "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
       "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
       : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *u) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(u[0]),
+               "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -219,24 +246,27 @@ __device__ __forceinline__ bool read_request(const AttendArgs &a, int32_t i, Req
   if (r.bad) r.kv = 0;
   return c0 >= 0 && c1 >= c0 && c1 <= a.T;
 }
-// the key tiles [k0, k1) * 128 that the unit of tokens [t0, t0 + nt) sees: at least one (which may be empty)
+// the key tiles [k0, k1) that the unit of tokens [t0, t0 + nt) sees: at least one (which may be empty)
+template <int kKeys>
 __device__ __forceinline__ void unit_keys(const AttendArgs &a, const Request &r, int32_t t0, int32_t nt, int32_t &k0,
                                           int32_t &k1) {
   const int32_t first = r.kv - r.n + t0;  // place of the unit's first token
   int32_t hi = r.kv;
   if (a.causal) hi = min(hi, first + nt);
   int32_t lo = 0;
-  if (a.window > 0) lo = max(0, first + 1 - min(a.window, first + 1 > 0 ? first + 1 : 1));
+  if (a.window > 0) lo = max(0, first + 1 - min(a.window, max(first + 1, 1)));
   k0 = lo / kKeys;
   k1 = max(k0 + 1, (hi + kKeys - 1) / kKeys);
 }
-// the length of request i's part of the line
+// the length of request r's part of the line
+template <typename Sh>
 __device__ __forceinline__ int64_t request_cost(const AttendArgs &a, const Request &r) {
+  const int32_t step = Sh::kTiles * a.tile_tokens;
   int64_t c = 0;
-  for (int32_t t0 = 0; t0 < r.n; t0 += 2 * a.tile_tokens) {
+  for (int32_t t0 = 0; t0 < r.n; t0 += step) {
     int32_t k0, k1;
-    unit_keys(a, r, t0, min(2 * a.tile_tokens, r.n - t0), k0, k1);
-    c += k1 - k0 + kUnitCost;
+    unit_keys<Sh::kKeys>(a, r, t0, min(step, r.n - t0), k0, k1);
+    c += k1 - k0 + Sh::kUnitCost;
   }
   return c * a.Hkv;
 }
@@ -247,18 +277,405 @@ __device__ __forceinline__ bool warp_wait(unsigned long long *bar, uint32_t pari
   if ((threadIdx.x & 31) == 0) ok = mbar_wait_bounded(bar, parity) ? 1 : 0;
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
+// the parity of a barrier's n-th completion
+__device__ __forceinline__ uint32_t par(int32_t n) { return static_cast<uint32_t>(n & 1); }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+// -------------------------------- the loader --------------------------------
+template <int D, bool kWide, typename C>
+__device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtensorMap &tmK, const CUtensorMap &tmV,
+                                            const AttendArgs &a, C &sm, int wk, int worker, int64_t W, int64_t b,
+                                            int64_t e, int64_t workers, uint32_t q_smem, uint32_t ring) {
+  using Sh = Shape<D, kWide>;
+  auto &ln = sm.lane[wk];
+  const int lane = threadIdx.x & 31;
+  const int G = a.Hq / a.Hkv;
+  const int box = min(a.page_size, Sh::kKeys);  // rows of a page's box
+  const int shift = 31 - __clz(a.page_size);
+  const int32_t step = Sh::kTiles * a.tile_tokens;
+  int64_t at = ln.first_at;
+  int32_t count = 0, qc = 0, k = 0;  // ring tiles, query tiles, segments so far
+  bool ok = true;
+  Joint joint = {W, -1, 0, 0, 0, 0, 0};
+  for (int32_t i = ln.first_req; i < a.N && at < e && ok; ++i) {
+    Request r;
+    if (!read_request(a, i, r)) continue;
+    const int32_t *table = a.table + i * a.table_stride;
+    for (int32_t t0 = 0; t0 < r.n && at < e && ok; t0 += step) {
+      const int32_t nt = min(step, r.n - t0);
+      int32_t k0, k1;
+      unit_keys<Sh::kKeys>(a, r, t0, nt, k0, k1);
+      const int64_t cost = k1 - k0 + Sh::kUnitCost;
+      if (at + cost * a.Hkv <= b) {  // all heads of these tokens lie before the stretch
+        at += cost * a.Hkv;
+        continue;
+      }
+      for (int32_t hk = 0; hk < a.Hkv && at < e && ok; ++hk, at += cost) {
+        const int32_t j0 = static_cast<int32_t>(max(static_cast<int64_t>(0), b - at - Sh::kUnitCost));
+        const int32_t j1 = static_cast<int32_t>(min(static_cast<int64_t>(k1 - k0), e - at - Sh::kUnitCost));
+        if (j0 >= j1) continue;
+        // the segment's pages, 32 ids at a time, the next 32 under way
+        const int32_t p_end = (min(r.kv, (k0 + j1) * Sh::kKeys) + a.page_size - 1) >> shift;
+        int32_t p_base = ((k0 + j0) * Sh::kKeys) >> shift;
+        int32_t ids = (p_base + lane < p_end) ? __ldg(table + p_base + lane) : 0;
+        int32_t next_ids = (p_base + 32 + lane < p_end) ? __ldg(table + p_base + 32 + lane) : 0;
+        const int sl = k % kSegRing;
+        ok = k < kSegRing || warp_wait(&ln.seg_empty[sl], par(k / kSegRing - 1));
+        if (!ok) break;
+        const bool whole = (j0 == 0 && j1 == k1 - k0);
+        const int32_t ntok0 = min(nt, a.tile_tokens), ntok1 = nt - ntok0;
+        if (lane == 0) {
+          Segment &s = ln.seg[sl];
+          s.tiles = j1 - j0;
+          s.tok0 = r.c0 + t0;
+          s.ntok0 = ntok0;
+          s.ntok1 = ntok1;
+          s.pos0 = r.kv - r.n + t0;
+          s.key0 = (k0 + j0) * Sh::kKeys;
+          s.kv = r.kv;
+          s.hk = hk;
+          s.part = whole ? -1 : 2 * worker + (j0 == 0 ? 1 : 0);
+          ln.seg_bad[sl] = r.bad ? 1 : 0;
+          if (j0 == 0 && !whole) {
+            joint.last = static_cast<int32_t>(((at + cost) * workers + W - 1) / W - 1);
+            joint.tok0 = s.tok0;
+            joint.ntok0 = ntok0;
+            joint.ntok1 = ntok1;
+            joint.hk = hk;
+          }
+          mbar_arrive(&ln.seg_full[sl]);
+        }
+        ++k;
+        // the queries: the two tiles of a wide unit, one buffer each; the worker's one otherwise
+        ok = qc == 0 || warp_wait(&sm.q_empty[wk], par(qc - 1));
+        if (ok && lane == 0) {
+          const int tiles = kWide ? 2 : 1;
+          mbar_arrive_expect_tx(&sm.q_full[wk], static_cast<uint32_t>(tiles * G * a.tile_tokens * D * 2));
+          for (int s = 0; s < tiles; ++s)
+            for (int h = 0; h < Sh::kHalves; ++h)
+              tma_load_3d(q_smem + s * Sh::kQTile + h * Sh::kQHalf, &tmQ, h * 64, hk * G, r.c0 + t0 + s * a.tile_tokens,
+                          smem_u32(&sm.q_full[wk]));
+        }
+        ++qc;
+        // the keys and values, a lane per page
+        bool bad = false;
+        for (int32_t j = j0; j < j1 && ok; ++j) {
+          const int32_t key = (k0 + j) * Sh::kKeys;
+          const int32_t have = max(0, min(Sh::kKeys, r.kv - key));
+          const int need = (have + box - 1) / box;  // pages that hold keys of the request
+          if ((key >> shift) >= p_base + 32) {      // a tile's pages never straddle 32: it has a power of two of them
+            p_base += 32;
+            ids = next_ids;
+            next_ids = (p_base + 32 + lane < p_end) ? __ldg(table + p_base + 32 + lane) : 0;
+          }
+          int32_t page = __shfl_sync(0xffffffffu, ids, min(31, ((key + lane * box) >> shift) - p_base));
+          if (lane < need && (page < 0 || page >= a.n_pages)) {
+            bad = true;
+            page = a.n_pages;  // outside the tensor: reads as zeros
+          }
+          const int row = key & (a.page_size - 1);  // 0 unless a page holds several tiles
+          for (int v = 0; v < 2 && ok; ++v, ++count) {
+            const int s = count % Sh::kRing;
+            ok = count < Sh::kRing || warp_wait(&ln.empty[s], par(count / Sh::kRing - 1));
+            if (!ok) break;
+            if (v == 1 && j == j1 - 1 && __any_sync(0xffffffffu, bad) && lane == 0) {
+              ln.seg_bad[sl] = 1;  // the last arrival of the segment carries this to its epilogue
+              if (a.status) atomicOr(a.status, SVW_DEV_BAD_INPUT);
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&ln.full[s], static_cast<uint32_t>(need * box * D * 2));
+            __syncwarp();
+            if (lane < need) {
+              const uint32_t dst = ring + s * Sh::kTile + lane * box * 128;
+              for (int h = 0; h < Sh::kHalves; ++h)
+                tma_load_4d(dst + h * Sh::kHalf, v ? &tmV : &tmK, h * 64, row, hk, page, smem_u32(&ln.full[s]));
+            }
+          }
+        }
+      }
+    }
+  }
+  // the end marker
+  if (ok) ok = k < kSegRing || warp_wait(&ln.seg_empty[k % kSegRing], par(k / kSegRing - 1));
+  if (lane == 0) {
+    if (ok) {
+      ln.seg[k % kSegRing].tiles = 0;
+      mbar_arrive(&ln.seg_full[k % kSegRing]);
+    } else {
+      atomicOr(&sm.err, 1);
+    }
+    ln.issued = count;
+    ln.q_issued = qc;
+    a.joints[worker] = joint;
+  }
+}
+
+// ------------------------------ the MMA issuer ------------------------------
+// (one thread)
+template <int D, bool kWide, typename C>
+__device__ __forceinline__ void issue_worker(C &sm, int wk, uint32_t q_smem, uint32_t ring, uint32_t tmem) {
+  using Sh = Shape<D, kWide>;
+  constexpr uint32_t id_s = idesc(Sh::kKeys, false), id_o = idesc(D, true);
+  auto &ln = sm.lane[wk];
+  int32_t count = 0, k = 0, sc[2] = {0, 0};
+  bool ok = true;
+  auto wait = [&](unsigned long long *bar, int32_t n) {  // the n-th completion of bar
+    if (ok && !mbar_wait_bounded(bar, par(n))) ok = false;
+    return ok;
+  };
+  auto wait_ring = [&](int32_t c) {
+    const bool r = wait(&ln.full[c % Sh::kRing], c / Sh::kRing);
+    tc_after();
+    return r;
+  };
+  // score buffer u: stage u (wide), buffer u of worker wk (narrow)
+  auto s_col = [&](int u) { return tmem + (kWide ? u * 128 : wk * 128 + u * 64); };
+  auto s_bar = [&](int u) { return kWide ? u : 2 * wk + u; };
+  auto scores = [&](int u, int32_t c) {
+    const uint32_t qa = q_smem + (kWide ? u * Sh::kQTile : 0), ka = ring + (c % Sh::kRing) * Sh::kTile;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+      mma_ss(s_col(u), sw128(qa + (kk / 4) * Sh::kQHalf + (kk % 4) * 32, 16),
+             sw128(ka + (kk / 4) * Sh::kHalf + (kk % 4) * 32, 16), id_s, kk > 0 ? 1u : 0u);
+    tc_commit(smem_u32(&sm.s_full[s_bar(u)]));
+  };
+  auto output = [&](int u, int32_t c, bool acc) {
+    const uint32_t va = ring + (c % Sh::kRing) * Sh::kTile;
+    // the weights of 64 keys lie in 32 columns over the first half of their scores
+#pragma unroll
+    for (int kk = 0; kk < Sh::kKeys / 16; ++kk)
+      mma_ts(tmem + 256 + (kWide ? u : wk) * D, s_col(u) + (kk / 4) * kCols + (kk % 4) * 8,
+             sw128(va + kk * 2048, Sh::kHalf), id_o, (acc || kk > 0) ? 1u : 0u);
+  };
+  auto release = [&](int32_t c) { tc_commit(smem_u32(&ln.empty[c % Sh::kRing])); };
+  while (ok) {
+    const int sl = k % kSegRing;
+    if (!wait(&ln.seg_full[sl], k / kSegRing)) break;
+    const int32_t n = ln.seg[sl].tiles;
+    if (n == 0) break;
+    mbar_arrive(&ln.seg_empty[sl]);
+    if (!wait(&sm.q_full[wk], k)) break;
+    // key tile j is ring tile count + 2 j, its values one behind
+    if (!wait_ring(count)) break;
+    scores(0, count);
+    if (kWide) scores(1, count);
+    release(count);
+    if (!kWide && n > 1) {
+      if (!wait_ring(count + 2)) break;
+      scores(1, count + 2);
+      release(count + 2);
+    }
+    constexpr int kLead = kWide ? 1 : 2;  // a score buffer's next key tile
+    for (int32_t j = 0; j < n && ok; ++j) {
+      const int32_t vt = count + 2 * j + 1, kt = count + 2 * (j + kLead);
+      for (int u = kWide ? 0 : (j & 1); u < (kWide ? 2 : (j & 1) + 1) && ok; ++u) {
+        if (!wait(&sm.p_full[s_bar(u)], sc[u])) break;
+        ++sc[u];
+        if (j == 0 && k > 0 && u == 0 && !wait(&ln.o_free, k - 1)) break;
+        if (!wait_ring(vt)) break;
+        output(u, vt, j > 0);
+        if (!kWide) tc_commit(smem_u32(&ln.o_step));
+        if (!kWide || u == 1) release(vt);
+        if (j + kLead < n) {
+          if (!wait_ring(kt)) break;
+          scores(u, kt);
+          if (!kWide || u == 1) release(kt);
+        }
+        // every score of the segment is under way: the query buffer may be refilled after them
+        if (j == max(0, n - 1 - kLead) && (!kWide || u == 1)) tc_commit(smem_u32(&sm.q_empty[wk]));
+      }
+    }
+    if (!ok) break;
+    tc_commit(smem_u32(&ln.o_full));
+    mbar_arrive(&ln.o_full);  // carries what the loader wrote about the segment
+    count += 2 * n;
+    ++k;
+  }
+  if (!ok) atomicOr(&sm.err, 1);
+}
+
+// ------------------------------- the softmax --------------------------------
+// Stage s; half h of the keys (wide).  A thread has one row and 64 keys.
+template <int D, bool kWide, typename C>
+__device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s, int h, unsigned char *ring_ptr,
+                                              uint32_t tmem) {
+  using Sh = Shape<D, kWide>;
+  auto &ln = sm.lane[kWide ? 0 : s];
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
+  const int row = quad * 32 + lane;
+  const int G = a.Hq / a.Hkv;
+  const int tok_of_row = row / G, head_of_row = row - tok_of_row * G;
+  const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+  const uint32_t t_s = tmem + lanes + s * 128 + (kWide ? h * kCols : 0);
+  const uint32_t t_o = tmem + lanes + 256 + s * D;
+  const float k2 = a.scale * kLog2e;
+  constexpr int kMyCols = kWide ? D / 2 : D;  // columns of the output that this thread looks after
+  const int oc0 = kWide ? h * kMyCols : 0;
+  // the two threads of a row
+  auto meet = [&] { named_sync(1 + s * 4 + quad, 64); };
+  int32_t count = 0, k = 0, steps = 0, sc[2] = {0, 0};  // ring tiles, segments, outputs, score tiles by buffer
+  bool ok = true;
+  while (true) {
+    const int sl = k % kSegRing;
+    if (!(ok = warp_wait(&ln.seg_full[sl], par(k / kSegRing)))) break;
+    const Segment g = ln.seg[sl];
+    if (g.tiles == 0) break;
+    const int tile = kWide ? s : 0;
+    const int32_t pos = g.pos0 + tile * a.tile_tokens + tok_of_row;
+    int32_t hi = g.kv, lo = 0;
+    if (a.causal) hi = min(hi, pos + 1);
+    if (a.window > 0) lo = max(0, pos + 1 - min(a.window, max(pos + 1, 1)));
+    const bool live = tok_of_row < (tile ? g.ntok1 : g.ntok0);
+    const bool warp_live = __any_sync(0xffffffffu, live);
+    if (!live) hi = lo;  // rows of no token see nothing
+    float M = -INFINITY, l = 0.f;
+    for (int32_t j = 0; j < g.tiles; ++j) {
+      const int u = kWide ? 0 : (j & 1);  // score buffer
+      const int32_t key = g.key0 + j * Sh::kKeys;
+      if (!(ok = warp_wait(&sm.s_full[kWide ? s : 2 * s + u], par(sc[u])))) break;
+      ++sc[u];
+      tc_after();
+      const uint32_t t_su = t_s + u * kCols;
+      if (warp_live) {
+        const int32_t c0 = key + (kWide ? h * kCols : 0);  // this thread's first key
+        float x[kCols];
+        tmem_ld32(t_su, x);
+        tmem_ld32(t_su + 32, x + 32);
+        tmem_wait_ld();
+        if (!__all_sync(0xffffffffu, c0 >= lo && c0 + kCols <= hi)) {
+#pragma unroll
+          for (int c = 0; c < kCols; ++c)
+            if (c0 + c < lo || c0 + c >= hi) x[c] = -INFINITY;
+        }
+        float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int c = 4; c < kCols; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
+        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * k2;
+        if (kWide) {
+          sm.row[s][h][row] = top;
+          meet();
+          top = fmaxf(top, sm.row[s][1 - h][row]);
+        }
+        const bool grow = top > M + kGrow || (M == -INFINITY && top > M);
+        const float f = grow ? (M == -INFINITY ? 0.f : ex2(M - top)) : 1.f;
+        if (grow) M = top;
+        l *= f;
+        if (j > 0 && __any_sync(0xffffffffu, grow)) {
+          // the outputs so far are complete (wide: the scores' arrival said so)
+          if (!kWide && !(ok = warp_wait(&ln.o_step, par(steps + j - 1)))) break;
+          if (!kWide) tc_after();
+#pragma unroll
+          for (int c = 0; c < kMyCols; c += 16) {
+            float o[16];
+            tmem_ld16(t_o + oc0 + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int v = 0; v < 16; ++v) o[v] *= f;
+            tmem_st16(t_o + oc0 + c, o);
+          }
+        }
+        const float ref = (M == -INFINITY) ? 0.f : M;
+        const float2 kk = make_float2(k2, k2), nr = make_float2(-ref, -ref);
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16) {
+          uint32_t w[8];
+#pragma unroll
+          for (int v = 0; v < 8; ++v) {
+            const float2 d = __ffma2_rn(make_float2(x[c + 2 * v], x[c + 2 * v + 1]), kk, nr);
+            const float2 p = make_float2(ex2(d.x), ex2(d.y));
+            if (v & 1)
+              sum1 = __fadd2_rn(sum1, p);
+            else
+              sum0 = __fadd2_rn(sum0, p);
+            w[v] = pack_bf16(p.x, p.y);
+          }
+          tmem_st8(t_su + c / 2, w);
+        }
+        const float2 t = __fadd2_rn(sum0, sum1);
+        l += t.x + t.y;
+      }
+      if (key + Sh::kKeys > g.kv) {
+        // value rows beyond the request's keys: whatever is there must not meet a weight of zero
+        const int32_t vt = count + 2 * j + 1;
+        if (!(ok = warp_wait(&ln.full[vt % Sh::kRing], par(vt / Sh::kRing)))) break;
+        unsigned char *v = ring_ptr + (vt % Sh::kRing) * Sh::kTile;
+        for (int w = max(0, g.kv - key) * 8 + row; w < Sh::kKeys * 8; w += kRows)
+#pragma unroll
+          for (int q = 0; q < Sh::kHalves; ++q) *reinterpret_cast<uint4 *>(v + q * Sh::kHalf + w * 16) = make_uint4(0, 0, 0, 0);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      tmem_wait_st();
+      tc_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.p_full[kWide ? s : 2 * s + u]);
+    }
+    if (!ok) break;
+    // ---- the segment's results ----
+    if (!(ok = warp_wait(&ln.o_full, par(k)))) break;
+    tc_after();
+    if (warp_live) {
+      if (kWide) {
+        sm.row[s][h][row] = l;  // the maxima have been read: the outputs waited for it
+        meet();
+        const float l0 = sm.row[s][0][row], l1 = sm.row[s][1][row];
+        l = l0 + l1;
+        meet();  // before the next segment's maxima
+      }
+      if (*reinterpret_cast<volatile int32_t *>(&ln.seg_bad[sl]) != 0) l = kNaN;
+      const int32_t tok = g.tok0 + tile * a.tile_tokens + tok_of_row;
+      const int64_t orow = static_cast<int64_t>(tok) * a.Hq + g.hk * G + head_of_row;
+      const int64_t prow = static_cast<int64_t>(max(g.part, 0)) * a.part_rows + tile * kRows + row;
+      const float inv = (g.part >= 0) ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+#pragma unroll 1
+      for (int c = oc0; c < oc0 + kMyCols; c += 32) {
+        float o[32];
+        tmem_ld32(t_o + c, o);
+        tmem_wait_ld();
+        if (!live) continue;
+        if (g.part < 0) {
+          uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + orow * D + c);
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            dst[v] = make_uint4(pack_bf16(o[8 * v] * inv, o[8 * v + 1] * inv), pack_bf16(o[8 * v + 2] * inv, o[8 * v + 3] * inv),
+                                pack_bf16(o[8 * v + 4] * inv, o[8 * v + 5] * inv), pack_bf16(o[8 * v + 6] * inv, o[8 * v + 7] * inv));
+        } else {
+          float4 *dst = reinterpret_cast<float4 *>(a.part_o + prow * D + c);
+#pragma unroll
+          for (int v = 0; v < 8; ++v) dst[v] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+        }
+      }
+      if (live && h == 0) {
+        if (g.part >= 0)
+          a.part_ml[prow] = make_float2(M, l);
+        else if (a.lse)
+          a.lse[orow] = (l == 0.f) ? -INFINITY : (M + log2f(l)) * kLn2;
+      }
+    }
+    tc_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&ln.o_free);
+      mbar_arrive(&ln.seg_empty[sl]);
+    }
+    count += 2 * g.tiles;
+    steps += g.tiles;
+    ++k;
+  }
+  if (!ok && lane == 0) atomicOr(&sm.err, 1);
+}
+
+template <int D, bool kWide>
+__global__ void __launch_bounds__(Shape<D, kWide>::kThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                           const __grid_constant__ CUtensorMap tmV, AttendArgs a) {
-  using Sh = Shape<D>;
+                           const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttendArgs a) {
+  using Sh = Shape<D, kWide>;
+  using C = Control<Sh::kRing, Sh::kWorkers>;
+  static_assert(sizeof(C) <= Sh::kControl, "control block");
+  constexpr int kWarps = Sh::kThreads / 32;
   extern __shared__ __align__(1024) unsigned char dyn[];
-  Control &sm = *reinterpret_cast<Control *>(dyn);
+  C &sm = *reinterpret_cast<C *>(dyn);
   const uint32_t base = smem_u32(dyn);
-  const uint32_t q_smem = base + kControlBytes, ring = q_smem + 2 * Sh::kTile;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int P = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+  const int64_t workers = static_cast<int64_t>(gridDim.x) * Sh::kWorkers;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (base & 1023u) {  // the swizzle atoms need it; never seen
@@ -266,27 +683,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   if (tid == 0) {
-    for (int s = 0; s < Sh::kRing; ++s) {
-      mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], 1);
+    for (int w = 0; w < Sh::kWorkers; ++w) {
+      auto &ln = sm.lane[w];
+      for (int s = 0; s < Sh::kRing; ++s) {
+        mbar_init(&ln.full[s], 1);
+        mbar_init(&ln.empty[s], 1);
+      }
+      for (int s = 0; s < kSegRing; ++s) {
+        mbar_init(&ln.seg_full[s], 1);
+        mbar_init(&ln.seg_empty[s], Sh::kSoftWarps + 1);
+      }
+      mbar_init(&ln.o_full, 2);
+      mbar_init(&ln.o_free, Sh::kSoftWarps);
+      mbar_init(&ln.o_step, 1);
+      ln.issued = 0;
+      ln.q_issued = 0;
+      ln.first_req = a.N;
+      ln.first_at = 0;
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.q_full[s], 1);
       mbar_init(&sm.q_empty[s], 1);
-      mbar_init(&sm.s_full[s], 1);
-      mbar_init(&sm.p_full[s], kSoftWarps / 2);
     }
-    mbar_init(&sm.o_full, 2);
-    mbar_init(&sm.o_free, kSoftWarps);
-    for (int s = 0; s < kSegRing; ++s) {
-      mbar_init(&sm.seg_full[s], 1);
-      mbar_init(&sm.seg_empty[s], kSoftWarps + 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&sm.s_full[s], 1);
+      mbar_init(&sm.p_full[s], 4 * Sh::kGroups);
     }
     sm.err = 0;
-    sm.issued = 0;
-    sm.q_issued = 0;
-    sm.first_req = a.N;
-    sm.first_at = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmQ)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmK)) : "memory");
@@ -299,20 +722,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
 
-  // ---- this CTA's stretch of the line ----
-  const int32_t per = (a.N + kThreads - 1) / kThreads;
+  // ---- the line, and the workers' stretches of it ----
+  const int32_t per = (a.N + Sh::kThreads - 1) / Sh::kThreads;
   const int32_t r0 = min(a.N, tid * per), r1 = min(a.N, r0 + per);
   int64_t mine = 0;
   bool wrong = false;
   for (int32_t i = r0; i < r1; ++i) {
     Request r;
     if (read_request(a, i, r))
-      mine += request_cost(a, r);
+      mine += request_cost<Sh>(a, r);
     else
       wrong = true;
     wrong |= r.bad || (i == 0 && r.c0 != 0) || (i == a.N - 1 && r.c0 + r.n != a.T);
   }
-  if (wrong && cta == 0 && a.status) atomicOr(a.status, SVW_DEV_BAD_INPUT);
+  if (wrong && blockIdx.x == 0 && a.status) atomicOr(a.status, SVW_DEV_BAD_INPUT);
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -322,412 +745,71 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (lane == 31) sm.scan[warp] = incl;
   __syncthreads();
   int64_t before = incl - mine, W = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += sm.scan[w];
     W += sm.scan[w];
   }
-  const int64_t b = W * cta / P, e = W * (cta + 1) / P;
-  if (b < e && before <= b && b < before + mine) {
-    for (int32_t i = r0; i < r1; ++i) {
-      Request r;
-      const int64_t c = read_request(a, i, r) ? request_cost(a, r) : 0;
-      if (b < before + c) {
-        sm.first_req = i;
-        sm.first_at = before;
-        break;
+  for (int w = 0; w < Sh::kWorkers; ++w) {
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * Sh::kWorkers + w;
+    const int64_t b = W * id / workers, e = W * (id + 1) / workers;
+    if (b < e && before <= b && b < before + mine) {
+      int64_t at = before;
+      for (int32_t i = r0; i < r1; ++i) {
+        Request r;
+        const int64_t c = read_request(a, i, r) ? request_cost<Sh>(a, r) : 0;
+        if (b < at + c) {
+          sm.lane[w].first_req = i;
+          sm.lane[w].first_at = at;
+          break;
+        }
+        at += c;
       }
-      before += c;
     }
   }
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = sm.tmem;
-  const int G = a.Hq / a.Hkv;
+  const uint32_t q_smem = base + Sh::kControl, ring = q_smem + 2 * Sh::kQTile;
+  constexpr int kRingBytes = Sh::kRing * Sh::kTile;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 0) {
-      // ------------------------------- loader -------------------------------
-      const int box = min(a.page_size, kKeys);       // rows of a page's box
-      const int boxes = kKeys / box;                 // pages of a key tile
-      const int shift = 31 - __clz(a.page_size);
-      int64_t at = sm.first_at;
-      int32_t count = 0, qc = 0, k = 0;  // ring tiles, query tiles, segments so far
-      bool ok = true;
-      Joint joint = {W, -1, 0, 0, 0, 0, 0};
-      for (int32_t i = sm.first_req; i < a.N && at < e && ok; ++i) {
-        Request r;
-        if (!read_request(a, i, r)) continue;
-        for (int32_t t0 = 0; t0 < r.n && at < e && ok; t0 += 2 * a.tile_tokens) {
-          const int32_t nt = min(2 * a.tile_tokens, r.n - t0);
-          int32_t k0, k1;
-          unit_keys(a, r, t0, nt, k0, k1);
-          const int64_t cost = k1 - k0 + kUnitCost;
-          if (at + cost * a.Hkv <= b) {  // all heads of these tokens lie before the stretch
-            at += cost * a.Hkv;
-            continue;
-          }
-          for (int32_t hk = 0; hk < a.Hkv && at < e && ok; ++hk, at += cost) {
-            const int32_t j0 = static_cast<int32_t>(max(static_cast<int64_t>(0), b - at - kUnitCost));
-            const int32_t j1 = static_cast<int32_t>(min(static_cast<int64_t>(k1 - k0), e - at - kUnitCost));
-            if (j0 >= j1) continue;
-            const int sl = k % kSegRing;
-            ok = k < kSegRing || warp_wait(&sm.seg_empty[sl], static_cast<uint32_t>((k / kSegRing - 1) & 1));
-            if (!ok) break;
-            const bool whole = (j0 == 0 && j1 == k1 - k0);
-            const int32_t ntok0 = min(nt, a.tile_tokens), ntok1 = nt - ntok0;
-            if (lane == 0) {
-              Segment &s = sm.seg[sl];
-              s.tiles = j1 - j0;
-              s.tok0 = r.c0 + t0;
-              s.ntok0 = ntok0;
-              s.ntok1 = ntok1;
-              s.pos0 = r.kv - r.n + t0;
-              s.key0 = (k0 + j0) * kKeys;
-              s.kv = r.kv;
-              s.hk = hk;
-              s.part = whole ? -1 : 2 * cta + (j0 == 0 ? 1 : 0);
-              sm.seg_bad[sl] = r.bad ? 1 : 0;
-              if (j0 == 0 && !whole) {
-                joint.last = static_cast<int32_t>(((at + cost) * P + W - 1) / W - 1);
-                joint.tok0 = s.tok0;
-                joint.ntok0 = ntok0;
-                joint.ntok1 = ntok1;
-                joint.hk = hk;
-              }
-              mbar_arrive(&sm.seg_full[sl]);
-            }
-            ++k;
-            // the queries
-            for (int s = 0; s < (ntok1 > 0 ? 2 : 1) && ok; ++s, ++qc) {
-              const int qs = qc & 1;
-              ok = qc < 2 || warp_wait(&sm.q_empty[qs], static_cast<uint32_t>((qc / 2 - 1) & 1));
-              if (ok && lane == 0) {
-                mbar_arrive_expect_tx(&sm.q_full[qs], static_cast<uint32_t>(G * a.tile_tokens * D * 2));
-                for (int h = 0; h < Sh::kHalves; ++h)
-                  tma_load_3d(q_smem + qs * Sh::kTile + h * Sh::kHalf, &tmQ, h * 64, hk * G,
-                              r.c0 + t0 + s * a.tile_tokens, smem_u32(&sm.q_full[qs]));
-              }
-            }
-            // the keys and values, a lane per page
-            bool bad = false;
-            for (int32_t j = j0; j < j1 && ok; ++j) {
-              const int32_t key = (k0 + j) * kKeys;
-              const int32_t have = max(0, min(kKeys, r.kv - key));
-              const int need = (have + box - 1) / box;  // pages that hold keys of the request
-              int32_t page = 0;
-              if (lane < need) {
-                page = __ldg(a.table + i * a.table_stride + ((key + lane * box) >> shift));
-                if (page < 0 || page >= a.n_pages) {
-                  bad = true;
-                  page = a.n_pages;  // outside the tensor: reads as zeros
-                }
-              }
-              const int row = key & (a.page_size - 1);  // 0 unless a page holds several tiles
-              for (int v = 0; v < 2 && ok; ++v, ++count) {
-                const int s = count % Sh::kRing;
-                ok = count < Sh::kRing || warp_wait(&sm.empty[s], static_cast<uint32_t>((count / Sh::kRing - 1) & 1));
-                if (!ok) break;
-                if (v == 1 && j == j1 - 1) {
-                  // the last arrival of the segment carries this to its epilogue
-                  const bool any = __any_sync(0xffffffffu, bad);
-                  if (any && lane == 0) {
-                    sm.seg_bad[sl] = 1;
-                    if (a.status) atomicOr(a.status, SVW_DEV_BAD_INPUT);
-                  }
-                }
-                if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], static_cast<uint32_t>(need * box * D * 2));
-                __syncwarp();
-                if (lane < need && lane < boxes) {
-                  const uint32_t dst = ring + s * Sh::kTile + lane * box * 128;
-                  for (int h = 0; h < Sh::kHalves; ++h)
-                    tma_load_4d(dst + h * Sh::kHalf, v ? &tmV : &tmK, h * 64, row, hk, page, smem_u32(&sm.full[s]));
-                }
-              }
-            }
-          }
-        }
+    if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    const int wk = warp >> 1;
+    if (wk < Sh::kWorkers) {
+      if ((warp & 1) == 0) {
+        const int64_t id = static_cast<int64_t>(blockIdx.x) * Sh::kWorkers + wk;
+        load_worker<D, kWide>(tmQ, tmK, tmV, a, sm, wk, static_cast<int>(id), W, W * id / workers,
+                              W * (id + 1) / workers, workers, q_smem + wk * Sh::kQTile, ring + wk * kRingBytes);
+      } else if (lane == 0) {
+        issue_worker<D, kWide>(sm, wk, q_smem + wk * Sh::kQTile, ring + wk * kRingBytes, tmem);
       }
-      // the end marker
-      if (ok) ok = k < kSegRing || warp_wait(&sm.seg_empty[k % kSegRing], static_cast<uint32_t>((k / kSegRing - 1) & 1));
-      if (lane == 0) {
-        if (ok) {
-          sm.seg[k % kSegRing].tiles = 0;
-          mbar_arrive(&sm.seg_full[k % kSegRing]);
-        } else {
-          atomicOr(&sm.err, 1);
-        }
-        sm.issued = count;
-        sm.q_issued = qc;
-        a.joints[cta] = joint;
-      }
-    } else if (warp == 1 && lane == 0) {
-      // ----------------------------- MMA issuer -----------------------------
-      constexpr uint32_t id_s = idesc(kKeys, false), id_o = idesc(D, true);
-      int32_t count = 0, qc = 0, k = 0, sc[2] = {0, 0};
-      bool ok = true;
-      auto wait = [&](unsigned long long *bar, int32_t n) {  // the n-th completion of bar
-        if (ok && !mbar_wait_bounded(bar, static_cast<uint32_t>(n & 1))) ok = false;
-        return ok;
-      };
-      auto wait_ring = [&](int32_t c) {
-        const bool r = wait(&sm.full[c % Sh::kRing], c / Sh::kRing);
-        tc_after();
-        return r;
-      };
-      auto scores = [&](int s, int32_t q, int32_t c) {
-        const uint32_t qa = q_smem + (q & 1) * Sh::kTile, ka = ring + (c % Sh::kRing) * Sh::kTile;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * Sh::kHalf + (kk % 4) * 32;
-          mma_ss(tmem + s * kKeys, sw128(qa + off, 16), sw128(ka + off, 16), id_s, kk > 0 ? 1u : 0u);
-        }
-        tc_commit(smem_u32(&sm.s_full[s]));
-      };
-      auto output = [&](int s, int32_t c, bool acc) {
-        const uint32_t va = ring + (c % Sh::kRing) * Sh::kTile;
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_ts(tmem + 2 * kKeys + s * D, tmem + s * kKeys + kk * 8, sw128(va + kk * 2048, Sh::kHalf), id_o,
-                 (acc || kk > 0) ? 1u : 0u);
-      };
-      auto release = [&](int32_t c) { tc_commit(smem_u32(&sm.empty[c % Sh::kRing])); };
-      while (ok) {
-        const int sl = k % kSegRing;
-        if (!wait(&sm.seg_full[sl], k / kSegRing)) break;
-        const int32_t n = sm.seg[sl].tiles;
-        const bool two = sm.seg[sl].ntok1 > 0;
-        if (n == 0) break;
-        mbar_arrive(&sm.seg_empty[sl]);
-        if (!wait(&sm.q_full[qc & 1], qc / 2)) break;
-        if (two && !wait(&sm.q_full[(qc + 1) & 1], (qc + 1) / 2)) break;
-        // key tile j: ring tile count + 2 j, values one behind
-        const int lead = two ? 1 : 2;  // a stage's next key tile
-        if (!wait_ring(count)) break;
-        scores(0, qc, count);
-        if (two) scores(1, qc + 1, count);
-        release(count);
-        if (!two && n > 1) {
-          if (!wait_ring(count + 2)) break;
-          scores(1, qc, count + 2);
-          release(count + 2);
-        }
-        for (int32_t j = 0; j < n && ok; ++j) {
-          const int32_t vt = count + 2 * j + 1, kt = count + 2 * (j + lead);
-          const bool more = j + lead < n;
-          for (int s = two ? 0 : (j & 1); s < (two ? 2 : (j & 1) + 1) && ok; ++s) {
-            if (!wait(&sm.p_full[s], sc[s])) break;
-            ++sc[s];
-            if (j == 0 && k > 0 && s == 0 && !wait(&sm.o_free, k - 1)) break;
-            if (!wait_ring(vt)) break;
-            output(s, vt, j >= lead);
-            if (!two || s == 1) release(vt);
-            if (more) {
-              if (!wait_ring(kt)) break;
-              scores(s, two ? qc + s : qc, kt);
-              if (!two || s == 1) release(kt);
-            }
-          }
-        }
-        if (!ok) break;
-        // every product of the segment: its queries and accumulators
-        tc_commit(smem_u32(&sm.q_empty[qc & 1]));
-        if (two) tc_commit(smem_u32(&sm.q_empty[(qc + 1) & 1]));
-        tc_commit(smem_u32(&sm.o_full));
-        mbar_arrive(&sm.o_full);  // carries what the loader wrote about the segment
-        count += 2 * n;
-        qc += two ? 2 : 1;
-        ++k;
-      }
-      if (!ok) atomicOr(&sm.err, 1);
     }
   } else {
-    // ------------------------------- softmax --------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    const int s = (warp - 4) >> 2, quad = warp & 3;
-    const int row = quad * 32 + lane;
-    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t t_s = tmem + lanes + s * kKeys, t_o = tmem + lanes + 2 * kKeys;
-    const float k2 = a.scale * kLog2e;
-    const int tok_of_row = row / G, head_of_row = row % G;
-    int32_t count = 0, sc = 0, k = 0;
-    bool ok = true;
-    while (true) {
-      const int sl = k % kSegRing;
-      if (!(ok = warp_wait(&sm.seg_full[sl], static_cast<uint32_t>((k / kSegRing) & 1)))) break;
-      const Segment g = sm.seg[sl];
-      if (g.tiles == 0) break;
-      const bool two = g.ntok1 > 0;
-      const int tile = two ? s : 0;
-      const int32_t ntok = tile ? g.ntok1 : g.ntok0;
-      const int32_t pos = g.pos0 + tile * a.tile_tokens + tok_of_row;
-      int32_t hi = g.kv, lo = 0;
-      if (a.causal) hi = min(hi, pos + 1);
-      if (a.window > 0) lo = max(0, pos + 1 - min(a.window, max(pos + 1, 1)));
-      const bool live = tok_of_row < ntok;
-      const bool warp_live = __any_sync(0xffffffffu, live);
-      if (!live) hi = lo;  // rows of no token: nothing to see
-      float M = -INFINITY, l = 0.f;
-      bool first = true;
-      for (int32_t j = two ? 0 : s; j < g.tiles; j += two ? 1 : 2) {
-        const int32_t key = g.key0 + j * kKeys;
-        if (!(ok = warp_wait(&sm.s_full[s], static_cast<uint32_t>(sc & 1)))) break;
-        ++sc;
-        tc_after();
-        if (warp_live) {
-          float x[kKeys];
-#pragma unroll
-          for (int c = 0; c < kKeys; c += 32) tmem_ld32(t_s + c, x + c);
-          tmem_wait_ld();
-          if (!__all_sync(0xffffffffu, key >= lo && key + kKeys <= hi)) {
-#pragma unroll
-            for (int c = 0; c < kKeys; ++c)
-              if (key + c < lo || key + c >= hi) x[c] = -INFINITY;
-          }
-          float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-          for (int c = 4; c < kKeys; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * k2;
-          const bool grow = top > M + kGrow || (M == -INFINITY && top > M);
-          const float f = grow ? (M == -INFINITY ? 0.f : ex2(M - top)) : 1.f;
-          if (grow) M = top;
-          l *= f;
-          if (!first && __any_sync(0xffffffffu, grow)) {
-#pragma unroll
-            for (int c = 0; c < D; c += 32) {
-              float o[32];
-              tmem_ld32(t_o + s * D + c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int u = 0; u < 32; ++u) o[u] *= f;
-              tmem_st32(t_o + s * D + c, o);
-            }
-          }
-          const float ref = (M == -INFINITY) ? 0.f : M;
-          const float2 kk = make_float2(k2, k2), nr = make_float2(-ref, -ref);
-          float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-#pragma unroll
-          for (int c = 0; c < kKeys; c += 32) {
-            uint32_t w[16];
-#pragma unroll
-            for (int u = 0; u < 16; ++u) {
-              const float2 d = __ffma2_rn(make_float2(x[c + 2 * u], x[c + 2 * u + 1]), kk, nr);
-              const float2 p = make_float2(ex2(d.x), ex2(d.y));
-              if (u & 1)
-                sum1 = __fadd2_rn(sum1, p);
-              else
-                sum0 = __fadd2_rn(sum0, p);
-              w[u] = pack_bf16(p.x, p.y);
-            }
-            tmem_st16(t_s + c / 2, w);
-          }
-          const float2 t = __fadd2_rn(sum0, sum1);
-          l += t.x + t.y;
-        }
-        if (key + kKeys > g.kv) {
-          // value rows beyond the request's keys: whatever is there must not meet a weight of zero
-          const int32_t vt = count + 2 * j + 1;
-          if (!(ok = warp_wait(&sm.full[vt % Sh::kRing], static_cast<uint32_t>((vt / Sh::kRing) & 1)))) break;
-          const int r0v = max(0, g.kv - key);
-          unsigned char *v = dyn + (ring - base) + (vt % Sh::kRing) * Sh::kTile;
-          for (int u = r0v * 8 + quad * 32 + lane; u < kKeys * 8; u += 128)
-#pragma unroll
-            for (int h = 0; h < Sh::kHalves; ++h)
-              *reinterpret_cast<uint4 *>(v + h * Sh::kHalf + u * 16) = make_uint4(0, 0, 0, 0);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        tmem_wait_st();
-        tc_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[s]);
-        first = false;
-      }
-      if (!ok) break;
-      // ---- the segment's results ----
-      if (!(ok = warp_wait(&sm.o_full, static_cast<uint32_t>(k & 1)))) break;
-      tc_after();
-      const bool bad = *reinterpret_cast<volatile int32_t *>(&sm.seg_bad[sl]) != 0;
-      // stages that alternated share the row: half the columns each
-      float w0 = 1.f, w1 = 0.f;
-      int c0 = 0, c1 = D;
-      const bool both = !two && g.tiles > 1;
-      if (!two) {
-        sm.ml[s][row] = make_float2(M, l);
-        named_sync(1, kSoftWarps * 32);
-        const float2 m0 = sm.ml[0][row], m1 = sm.ml[1][row];
-        M = both ? fmaxf(m0.x, m1.x) : m0.x;
-        w0 = (m0.x == -INFINITY) ? 0.f : ex2(m0.x - M);
-        w1 = (!both || m1.x == -INFINITY) ? 0.f : ex2(m1.x - M);
-        l = w0 * m0.y + (both ? w1 * m1.y : 0.f);
-        c0 = s * (D / 2);
-        c1 = c0 + D / 2;
-        named_sync(1, kSoftWarps * 32);
-      }
-      if (bad) l = kNaN;
-      const int32_t tok = g.tok0 + tile * a.tile_tokens + tok_of_row;
-      const int64_t orow = static_cast<int64_t>(tok) * a.Hq + g.hk * G + head_of_row;
-      const int prow = tile * kRows + row;
-      if (warp_live) {
-        const float inv = (g.part >= 0) ? 1.f : (l == 0.f ? 0.f : 1.f / l);
-        for (int c = c0; c < c1; c += 32) {
-          float o[32];
-          tmem_ld32(t_o + (two ? s * D : 0) + c, o);
-          if (both) {
-            float o1[32];
-            tmem_ld32(t_o + D + c, o1);
-            tmem_wait_ld();
-#pragma unroll
-            for (int u = 0; u < 32; ++u) o[u] = o[u] * w0 + o1[u] * w1;
-          } else {
-            tmem_wait_ld();
-          }
-          if (!live) continue;
-          if (g.part < 0) {
-            uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + orow * D + c);
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              dst[u] = make_uint4(pack_bf16(o[8 * u] * inv, o[8 * u + 1] * inv), pack_bf16(o[8 * u + 2] * inv, o[8 * u + 3] * inv),
-                                  pack_bf16(o[8 * u + 4] * inv, o[8 * u + 5] * inv), pack_bf16(o[8 * u + 6] * inv, o[8 * u + 7] * inv));
-          } else {
-            float4 *dst = reinterpret_cast<float4 *>(a.part_o + (static_cast<int64_t>(g.part) * a.part_rows + prow) * D + c);
-#pragma unroll
-            for (int u = 0; u < 8; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-          }
-        }
-        if (live && (two || s == 0)) {
-          if (g.part >= 0)
-            a.part_ml[static_cast<int64_t>(g.part) * a.part_rows + prow] = make_float2(M, l);
-          else if (a.lse)
-            a.lse[orow] = (l == 0.f) ? -INFINITY : (M + log2f(l)) * kLn2;
-        }
-      }
-      tc_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sm.o_free);
-        mbar_arrive(&sm.seg_empty[sl]);
-      }
-      count += 2 * g.tiles;
-      ++k;
-    }
-    if (!ok && lane == 0) atomicOr(&sm.err, 1);
+    if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    const int g = (warp - 4) >> 2;  // softmax warpgroup: stage, then half
+    const int s = g / Sh::kGroups, h = g % Sh::kGroups;
+    softmax_stage<D, kWide>(a, sm, s, h, dyn + (ring - base) + (kWide ? 0 : s * kRingBytes), tmem);
   }
   __syncthreads();
   if (sm.err) {
     // a wait gave up: what is in flight lands before the CTA goes
     if (tid == 0) {
       if (a.status) atomicOr(a.status, SVW_DEV_TIMEOUT);
-      for (int32_t c = max(0, sm.issued - Sh::kRing); c < sm.issued; ++c)
-        mbar_wait_bounded(&sm.full[c % Sh::kRing], static_cast<uint32_t>((c / Sh::kRing) & 1));
-      for (int32_t c = max(0, sm.q_issued - 2); c < sm.q_issued; ++c)
-        mbar_wait_bounded(&sm.q_full[c & 1], static_cast<uint32_t>((c / 2) & 1));
+      for (int w = 0; w < Sh::kWorkers; ++w) {
+        auto &ln = sm.lane[w];
+        for (int32_t c = max(0, ln.issued - Sh::kRing); c < ln.issued; ++c)
+          mbar_wait_bounded(&ln.full[c % Sh::kRing], par(c / Sh::kRing));
+        if (ln.q_issued > 0) mbar_wait_bounded(&sm.q_full[w], par(ln.q_issued - 1));
+      }
     }
-    if (tid == 32) {
-      mbar_init(&sm.seg_full[0], 1);
+    if ((warp == 1 || warp == 3) && (warp >> 1) < Sh::kWorkers && lane == 0) {
+      // an issuer's products: a commit on a barrier that nothing else uses any more
+      unsigned long long *bar = &sm.lane[warp >> 1].seg_full[0];
+      mbar_init(bar, 1);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-      tc_commit(smem_u32(&sm.seg_full[0]));
-      mbar_wait_bounded(&sm.seg_full[0], 0);
+      tc_commit(smem_u32(bar));
+      mbar_wait_bounded(bar, 0);
     }
     __syncthreads();
   }
@@ -737,10 +819,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// A unit that CTAs c .. last shared: each row's parts brought to one reference
-// and added, in the order of the line.  A warp per row.
+// A unit that workers c .. last shared: each row's parts brought to one
+// reference and added, in the order of the line.  A warp per row, 32 parts'
+// references and sums at a time, eight parts' outputs under way.
 template <int D>
-__global__ void __launch_bounds__(256) attention_join(AttendArgs a, int P) {
+__global__ void __launch_bounds__(256) attention_join(const __grid_constant__ AttendArgs a, int workers) {
   constexpr int E = D / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x;
@@ -749,29 +832,48 @@ __global__ void __launch_bounds__(256) attention_join(AttendArgs a, int P) {
   const int lane = threadIdx.x & 31, warps = static_cast<int>(gridDim.y) * 8;
   const int G = a.Hq / a.Hkv;
   const int rows0 = jt.ntok0 * G, rows = rows0 + jt.ntok1 * G;
+  const int n = jt.last - c + 1;
+  // a worker whose stretch is empty (fewer tiles than workers) has no part
+  auto some = [&](int q) {
+    return q == 0 || jt.total >= workers || jt.total * (c + q) / workers < jt.total * (c + q + 1) / workers;
+  };
   for (int r = static_cast<int>(blockIdx.y) * 8 + (threadIdx.x >> 5); r < rows; r += warps) {
     const int tile = r >= rows0 ? 1 : 0, in_tile = r - tile * rows0;
     const int prow = tile * kRows + in_tile;
-    // the part of CTA q: its last segment for the first, its first one for the others
-    auto part = [&](int q) { return static_cast<int64_t>(2 * q + (q == c ? 1 : 0)) * a.part_rows + prow; };
-    auto some = [&](int q) { return q == c || jt.total * q / P < jt.total * (q + 1) / P; };
+    // the part of worker c + q: its last segment for the first, its first one for the others
+    auto part = [&](int q) { return static_cast<int64_t>(2 * (c + q) + (q == 0 ? 1 : 0)) * a.part_rows + prow; };
     float M = -INFINITY;
-    for (int q = c + lane; q <= jt.last; q += 32)
+    for (int q = lane; q < n; q += 32)
       if (some(q)) M = fmaxf(M, a.part_ml[part(q)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float l = 0.f, acc[E];
 #pragma unroll
     for (int u = 0; u < E; ++u) acc[u] = 0.f;
-#pragma unroll 4
-    for (int q = c; q <= jt.last; ++q) {
-      if (!some(q)) continue;
-      const float2 ml = a.part_ml[part(q)];
+    for (int q0 = 0; q0 < n; q0 += 32) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (q0 + lane < n && some(q0 + lane)) ml = a.part_ml[part(q0 + lane)];
       const float w = (ml.x == -INFINITY) ? 0.f : ex2(ml.x - M);
-      l += (ml.x == -INFINITY && ml.y == 0.f) ? 0.f : (ml.x == -INFINITY ? ml.y : w * ml.y);
-      const float *o = a.part_o + part(q) * D + lane * E;
+      const float wl = (ml.x == -INFINITY) ? ml.y : w * ml.y;  // an empty part has 0, a bad one NaN
+      const int m = min(32, n - q0);
+      for (int b = 0; b < m; b += 8) {
+        float o[8][E];
 #pragma unroll
-      for (int u = 0; u < E; ++u) acc[u] = fmaf(w, o[u], acc[u]);
+        for (int u = 0; u < 8; ++u) {
+          const float *src = a.part_o + part(min(q0 + b + u, n - 1)) * D + lane * E;
+#pragma unroll
+          for (int v = 0; v < E; ++v) o[u][v] = __ldcg(src + v);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float wu = __shfl_sync(0xffffffffu, w, min(31, b + u)), lu = __shfl_sync(0xffffffffu, wl, min(31, b + u));
+          if (b + u < m) {
+            l += lu;
+#pragma unroll
+            for (int v = 0; v < E; ++v) acc[v] = (wu == 0.f) ? acc[v] : fmaf(wu, o[u][v], acc[v]);
+          }
+        }
+      }
     }
     const int tok = jt.tok0 + tile * a.tile_tokens + in_tile / G;
     const int64_t orow = static_cast<int64_t>(tok) * a.Hq + jt.hk * G + in_tile % G;
@@ -814,14 +916,13 @@ bool encode(CUtensorMap *map, const void *ptr, int rank, const int64_t *dims, co
 }
 
 int tile_tokens(int32_t Hq, int32_t Hkv) { return kRows / (Hq / Hkv); }
-// rows of a workspace part: two row tiles unless every unit fits one
-int part_rows(int64_t T, int32_t Hq, int32_t Hkv) { return T <= tile_tokens(Hq, Hkv) ? kRows : 2 * kRows; }
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-template <int D>
+template <int D, bool kWide>
 cudaError_t launch(AttendArgs a, cudaStream_t st) {
+  using Sh = Shape<D, kWide>;
   CUtensorMap mq, mk, mv;
-  const int G = a.Hq / a.Hkv, box = a.page_size < kKeys ? a.page_size : kKeys;
+  const int G = a.Hq / a.Hkv, box = a.page_size < Sh::kKeys ? a.page_size : Sh::kKeys;
   const int64_t qd[3] = {D, a.Hq, a.T}, qs[3] = {1, a.q_hs, a.q_ts};
   const int qb[3] = {64, G, a.tile_tokens};
   const int64_t cd[4] = {D, a.page_size, a.Hkv, a.n_pages};
@@ -829,7 +930,6 @@ cudaError_t launch(AttendArgs a, cudaStream_t st) {
   const int cb[4] = {64, box, 1, 1};
   if (!encode(&mq, a.q, 3, qd, qs, qb) || !encode(&mk, a.k_cache, 4, cd, ks, cb) || !encode(&mv, a.v_cache, 4, cd, vs, cb))
     return cudaErrorInvalidValue;
-  constexpr int smem = kControlBytes + (2 + Shape<D>::kRing) * Shape<D>::kTile;
   static std::mutex mu;
   static bool attr_done[64] = {};
   static int sms[64] = {};
@@ -838,15 +938,17 @@ cudaError_t launch(AttendArgs a, cudaStream_t st) {
   {
     std::lock_guard<std::mutex> lk(mu);
     if (!attr_done[dev]) {
-      cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      cudaError_t e =
+          cudaFuncSetAttribute(paged_attention_kernel<D, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
       if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
       if (e != cudaSuccess) return e;
       attr_done[dev] = true;
     }
   }
   const int P = sms[dev] < kMaxGrid ? sms[dev] : kMaxGrid;
+  a.part_rows = Sh::kTiles * kRows;
   void *tm = timer_before("paged_attention", st);
-  paged_attention_kernel<D><<<P, kThreads, smem, st>>>(mq, mk, mv, a);
+  paged_attention_kernel<D, kWide><<<P, Sh::kThreads, Sh::kSmem, st>>>(mq, mk, mv, a);
   timer_after(tm, st);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -854,35 +956,41 @@ cudaError_t launch(AttendArgs a, cudaStream_t st) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(P), 4, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(P * Sh::kWorkers), 4, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   tm = timer_before("attention_join", st);
-  e = cudaLaunchKernelEx(&cfg, attention_join<D>, a, P);
+  e = cudaLaunchKernelEx(&cfg, attention_join<D>, a, P * Sh::kWorkers);
   timer_after(tm, st);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
+// parts of the workspace: two per worker of 128 rows each row tile of a unit, narrow or wide alike
+constexpr size_t kPartRows = 2 * 2 * kMaxGrid * kRows;
+
 }  // namespace
 
 // joints | (reference, sum) of each part's rows | their outputs
-size_t attention_workspace(int64_t T, int32_t Hq, int32_t Hkv, int32_t D) {
-  const size_t rows = static_cast<size_t>(2 * kMaxGrid) * part_rows(T, Hq, Hkv);
-  return round256(sizeof(Joint) * kMaxGrid) + round256(rows * sizeof(float2)) + round256(rows * D * sizeof(float));
+size_t attention_workspace(int32_t D) {
+  return round256(sizeof(Joint) * 2 * kMaxGrid) + round256(kPartRows * sizeof(float2)) + kPartRows * D * sizeof(float);
 }
 
 cudaError_t launch_attention(const AttendArgs &args, cudaStream_t st) {
   AttendArgs a = args;
+  const int G = a.Hq / a.Hkv;
   a.tile_tokens = tile_tokens(a.Hq, a.Hkv);
-  a.part_rows = part_rows(a.T, a.Hq, a.Hkv);
-  const size_t rows = static_cast<size_t>(2 * kMaxGrid) * a.part_rows;
   char *ws = static_cast<char *>(a.ws);
   a.joints = reinterpret_cast<Joint *>(ws);
-  a.part_ml = reinterpret_cast<float2 *>(ws + round256(sizeof(Joint) * kMaxGrid));
-  a.part_o = reinterpret_cast<float *>(ws + round256(sizeof(Joint) * kMaxGrid) + round256(rows * sizeof(float2)));
-  return a.D == 128 ? launch<128>(a, st) : launch<64>(a, st);
+  a.part_ml = reinterpret_cast<float2 *>(ws + round256(sizeof(Joint) * 2 * kMaxGrid));
+  a.part_o = reinterpret_cast<float *>(ws + round256(sizeof(Joint) * 2 * kMaxGrid) + round256(kPartRows * sizeof(float2)));
+  // The rows of a request, on average: up to one tile's the bytes of its keys
+  // bound the work (128 rows are 128 flop per byte, the ridge lies at 280), and
+  // more would read the keys once per tile in the narrow form.
+  const bool wide = a.T * G > static_cast<int64_t>(kRows) * a.N;
+  if (a.D == 128) return wide ? launch<128, true>(a, st) : launch<128, false>(a, st);
+  return wide ? launch<64, true>(a, st) : launch<64, false>(a, st);
 }
 
 }  // namespace svw

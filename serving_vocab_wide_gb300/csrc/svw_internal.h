@@ -258,10 +258,10 @@ struct AppendArgs {
 cudaError_t launch_append(const AppendArgs &a, int dtype, cudaStream_t stream);
 
 // paged_attention (attention.cu)
-// the unit that a CTA's last segment begins and does not finish
+// the unit that a worker's last segment begins and does not finish
 struct alignas(16) AttendJoint {
-  int64_t total;  // length of the line of work (for the other CTAs' stretches)
-  int32_t last;   // the CTA that finishes the unit; -1: there is no such unit
+  int64_t total;  // length of the line of work (for the other workers' stretches)
+  int32_t last;   // the worker that finishes the unit; -1: there is no such unit
   int32_t tok0, ntok0, ntok1, hk, pad;
 };
 struct AttendArgs {
@@ -286,11 +286,11 @@ struct AttendArgs {
   // set by the launcher
   int32_t tile_tokens;  // tokens of a row tile
   int32_t part_rows;    // rows of a workspace part
-  AttendJoint *joints;  // [CTAs]
-  float2 *part_ml;      // [2 CTAs][part_rows] reference and sum
-  float *part_o;        // [2 CTAs][part_rows][D] unnormalised output
+  AttendJoint *joints;  // [workers]
+  float2 *part_ml;      // [2 workers][part_rows] reference and sum
+  float *part_o;        // [2 workers][part_rows][D] unnormalised output
 };
-size_t attention_workspace(int64_t T, int32_t Hq, int32_t Hkv, int32_t D);
+size_t attention_workspace(int32_t D);
 cudaError_t launch_attention(const AttendArgs &a, cudaStream_t stream);
 
 }  // namespace svw
