@@ -152,20 +152,45 @@ __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// D[tmem] (+)= A B^T, bf16 in, fp32 accumulate; A from shared or from tensor memory
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// D[tmem] (+)= A B^T over 64 elements of K, bf16 in, fp32 accumulate: four
+// products of 16 in one piece, so that their descriptors step by constants
+// (one product at a time, from one thread, an issue took 63 cycles, about what
+// a 128 x 128 x 16 product lasts; in fours from a converged warp at most 39).
+// A and B K-major in shared memory: 32 bytes a step.
+__device__ __forceinline__ void mma_ss_x4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tmov.b64 x, %1;\n\tmov.b64 y, %2;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t"
+      "add.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, 1;\n\t"
+      "add.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, 1;\n\t"
+      "add.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, 1;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// A in tensor memory (8 columns a step), B MN-major in shared memory (16 rows of 128 bytes a step)
+__device__ __forceinline__ void mma_ts_x4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p;\n\t.reg .b32 x;\n\t.reg .b64 y;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tmov.b32 x, %1;\n\tmov.b64 y, %2;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n\t"
+      "add.u32 x, x, 8;\n\tadd.s64 y, y, 128;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, 1;\n\t"
+      "add.u32 x, x, 8;\n\tadd.s64 y, y, 128;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, 1;\n\t"
+      "add.u32 x, x, 8;\n\tadd.s64 y, y, 128;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, 1;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
+}
+// one thread of a converged warp, always the same
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+  return r != 0;
 }
 // 32 consecutive columns of this thread's lane; the registers hold them after tmem_wait_ld
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *r) {
@@ -271,11 +296,10 @@ __device__ __forceinline__ int64_t request_cost(const AttendArgs &a, const Reque
   return c * a.Hkv;
 }
 
-// bounded wait of one lane for the whole warp; false: it gave up
+// bounded wait of a converged warp; false: it gave up
 __device__ __forceinline__ bool warp_wait(unsigned long long *bar, uint32_t parity) {
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait_bounded(bar, parity) ? 1 : 0;
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
 }
 // the parity of a barrier's n-th completion
 __device__ __forceinline__ uint32_t par(int32_t n) { return static_cast<uint32_t>(n & 1); }
@@ -409,87 +433,111 @@ __device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtens
 }
 
 // ------------------------------ the MMA issuer ------------------------------
-// (one thread)
+// A converged warp; one of its threads issues.
 template <int D, bool kWide, typename C>
 __device__ __forceinline__ void issue_worker(C &sm, int wk, uint32_t q_smem, uint32_t ring, uint32_t tmem) {
   using Sh = Shape<D, kWide>;
   constexpr uint32_t id_s = idesc(Sh::kKeys, false), id_o = idesc(D, true);
   auto &ln = sm.lane[wk];
-  int32_t count = 0, k = 0, sc[2] = {0, 0};
-  bool ok = true;
-  auto wait = [&](unsigned long long *bar, int32_t n) {  // the n-th completion of bar
-    if (ok && !mbar_wait_bounded(bar, par(n))) ok = false;
-    return ok;
+  // a place in the ring: slot and parity of its next completion
+  struct At {
+    int slot;
+    uint32_t parity;
+    __device__ void two_on() {  // the next tile of the same kind
+      slot += 2;
+      if (slot >= Sh::kRing) {
+        slot -= Sh::kRing;
+        parity ^= 1u;
+      }
+    }
   };
-  auto wait_ring = [&](int32_t c) {
-    const bool r = wait(&ln.full[c % Sh::kRing], c / Sh::kRing);
-    tc_after();
-    return r;
+  At kt = {0, 0}, vt = {1, 0};
+  int32_t k = 0, sc[2] = {0, 0};
+  bool ok = true;
+  auto wait_ring = [&](const At &t) {
+    ok = ok && warp_wait(&ln.full[t.slot], t.parity);
+    return ok;
   };
   // score buffer u: stage u (wide), buffer u of worker wk (narrow)
   auto s_col = [&](int u) { return tmem + (kWide ? u * 128 : wk * 128 + u * 64); };
   auto s_bar = [&](int u) { return kWide ? u : 2 * wk + u; };
-  auto scores = [&](int u, int32_t c) {
-    const uint32_t qa = q_smem + (kWide ? u * Sh::kQTile : 0), ka = ring + (c % Sh::kRing) * Sh::kTile;
+  auto scores = [&](int u, const At &t) {  // by the elected thread
+    const uint64_t qa = sw128(q_smem + (kWide ? u * Sh::kQTile : 0), 16), ka = sw128(ring + t.slot * Sh::kTile, 16);
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk)
-      mma_ss(s_col(u), sw128(qa + (kk / 4) * Sh::kQHalf + (kk % 4) * 32, 16),
-             sw128(ka + (kk / 4) * Sh::kHalf + (kk % 4) * 32, 16), id_s, kk > 0 ? 1u : 0u);
+    for (int h = 0; h < Sh::kHalves; ++h)
+      mma_ss_x4(s_col(u), qa + h * (Sh::kQHalf >> 4), ka + h * (Sh::kHalf >> 4), id_s, h);
     tc_commit(smem_u32(&sm.s_full[s_bar(u)]));
   };
-  auto output = [&](int u, int32_t c, bool acc) {
-    const uint32_t va = ring + (c % Sh::kRing) * Sh::kTile;
+  auto output = [&](int u, const At &t, bool acc) {
+    const uint64_t va = sw128(ring + t.slot * Sh::kTile, Sh::kHalf);
     // the weights of 64 keys lie in 32 columns over the first half of their scores
 #pragma unroll
-    for (int kk = 0; kk < Sh::kKeys / 16; ++kk)
-      mma_ts(tmem + 256 + (kWide ? u : wk) * D, s_col(u) + (kk / 4) * kCols + (kk % 4) * 8,
-             sw128(va + kk * 2048, Sh::kHalf), id_o, (acc || kk > 0) ? 1u : 0u);
+    for (int h = 0; h < Sh::kKeys / 64; ++h)
+      mma_ts_x4(tmem + 256 + (kWide ? u : wk) * D, s_col(u) + h * kCols, va + h * 512, id_o, (acc || h > 0) ? 1u : 0u);
   };
-  auto release = [&](int32_t c) { tc_commit(smem_u32(&ln.empty[c % Sh::kRing])); };
+  auto release = [&](const At &t) { tc_commit(smem_u32(&ln.empty[t.slot])); };
   while (ok) {
     const int sl = k % kSegRing;
-    if (!wait(&ln.seg_full[sl], k / kSegRing)) break;
+    if (!(ok = warp_wait(&ln.seg_full[sl], par(k / kSegRing)))) break;
     const int32_t n = ln.seg[sl].tiles;
+    __syncwarp();
     if (n == 0) break;
-    mbar_arrive(&ln.seg_empty[sl]);
-    if (!wait(&sm.q_full[wk], k)) break;
-    // key tile j is ring tile count + 2 j, its values one behind
-    if (!wait_ring(count)) break;
-    scores(0, count);
-    if (kWide) scores(1, count);
-    release(count);
+    if (elect_one()) mbar_arrive(&ln.seg_empty[sl]);
+    if (!(ok = warp_wait(&sm.q_full[wk], par(k))) || !wait_ring(kt)) break;
+    tc_after();
+    if (elect_one()) {
+      scores(0, kt);
+      if (kWide) scores(1, kt);
+      release(kt);
+    }
+    kt.two_on();
     if (!kWide && n > 1) {
-      if (!wait_ring(count + 2)) break;
-      scores(1, count + 2);
-      release(count + 2);
+      if (!wait_ring(kt)) break;
+      tc_after();
+      if (elect_one()) {
+        scores(1, kt);
+        release(kt);
+      }
+      kt.two_on();
     }
     constexpr int kLead = kWide ? 1 : 2;  // a score buffer's next key tile
     for (int32_t j = 0; j < n && ok; ++j) {
-      const int32_t vt = count + 2 * j + 1, kt = count + 2 * (j + kLead);
-      for (int u = kWide ? 0 : (j & 1); u < (kWide ? 2 : (j & 1) + 1) && ok; ++u) {
-        if (!wait(&sm.p_full[s_bar(u)], sc[u])) break;
+      const bool more = j + kLead < n;
+      if (!wait_ring(vt)) break;
+#pragma unroll
+      for (int i = 0; i < (kWide ? 2 : 1); ++i) {
+        const int u = kWide ? i : (j & 1);
+        if (!(ok = warp_wait(&sm.p_full[s_bar(u)], par(sc[u])))) break;
         ++sc[u];
-        if (j == 0 && k > 0 && u == 0 && !wait(&ln.o_free, k - 1)) break;
-        if (!wait_ring(vt)) break;
-        output(u, vt, j > 0);
-        if (!kWide) tc_commit(smem_u32(&ln.o_step));
-        if (!kWide || u == 1) release(vt);
-        if (j + kLead < n) {
-          if (!wait_ring(kt)) break;
-          scores(u, kt);
-          if (!kWide || u == 1) release(kt);
+        if (i == 0 && j == 0 && k > 0 && !(ok = warp_wait(&ln.o_free, par(k - 1)))) break;
+        tc_after();
+        if (elect_one()) {
+          output(u, vt, j > 0);
+          if (!kWide) tc_commit(smem_u32(&ln.o_step));
+          if (!kWide || i == 1) release(vt);
         }
-        // every score of the segment is under way: the query buffer may be refilled after them
-        if (j == max(0, n - 1 - kLead) && (!kWide || u == 1)) tc_commit(smem_u32(&sm.q_empty[wk]));
+        if (more && !wait_ring(kt)) break;
+        tc_after();
+        if (elect_one()) {
+          if (more) {
+            scores(u, kt);
+            if (!kWide || i == 1) release(kt);
+          }
+          // every score of the segment is under way: the query buffer may be refilled after them
+          if (j == max(0, n - 1 - kLead) && (!kWide || i == 1)) tc_commit(smem_u32(&sm.q_empty[wk]));
+        }
       }
+      vt.two_on();
+      if (more) kt.two_on();
     }
     if (!ok) break;
-    tc_commit(smem_u32(&ln.o_full));
-    mbar_arrive(&ln.o_full);  // carries what the loader wrote about the segment
-    count += 2 * n;
+    if (elect_one()) {
+      tc_commit(smem_u32(&ln.o_full));
+      mbar_arrive(&ln.o_full);  // carries what the loader wrote about the segment
+    }
     ++k;
   }
-  if (!ok) atomicOr(&sm.err, 1);
+  if (!ok && elect_one()) atomicOr(&sm.err, 1);
 }
 
 // ------------------------------- the softmax --------------------------------
@@ -525,7 +573,7 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
     if (a.window > 0) lo = max(0, pos + 1 - min(a.window, max(pos + 1, 1)));
     const bool live = tok_of_row < (tile ? g.ntok1 : g.ntok0);
     const bool warp_live = __any_sync(0xffffffffu, live);
-    if (!live) hi = lo;  // rows of no token see nothing
+    if (!live) hi = INT32_MAX, lo = 0;  // rows of no token: never masked, never looked at
     float M = -INFINITY, l = 0.f;
     for (int32_t j = 0; j < g.tiles; ++j) {
       const int u = kWide ? 0 : (j & 1);  // score buffer
@@ -541,9 +589,11 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
         tmem_ld32(t_su + 32, x + 32);
         tmem_wait_ld();
         if (!__all_sync(0xffffffffu, c0 >= lo && c0 + kCols <= hi)) {
+          const int32_t from = c0 - lo;  // key c0 + c is seen where 0 <= c + from < hi - lo
+          const uint32_t seen = static_cast<uint32_t>(max(0, hi - lo));
 #pragma unroll
           for (int c = 0; c < kCols; ++c)
-            if (c0 + c < lo || c0 + c >= hi) x[c] = -INFINITY;
+            if (static_cast<uint32_t>(c + from) >= seen) x[c] = -INFINITY;
         }
         float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -554,7 +604,7 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
           meet();
           top = fmaxf(top, sm.row[s][1 - h][row]);
         }
-        const bool grow = top > M + kGrow || (M == -INFINITY && top > M);
+        const bool grow = live && (top > M + kGrow || (M == -INFINITY && top > M));
         const float f = grow ? (M == -INFINITY ? 0.f : ex2(M - top)) : 1.f;
         if (grow) M = top;
         l *= f;
@@ -781,7 +831,7 @@ __global__ void __launch_bounds__(Shape<D, kWide>::kThreads, 1)
         const int64_t id = static_cast<int64_t>(blockIdx.x) * Sh::kWorkers + wk;
         load_worker<D, kWide>(tmQ, tmK, tmV, a, sm, wk, static_cast<int>(id), W, W * id / workers,
                               W * (id + 1) / workers, workers, q_smem + wk * Sh::kQTile, ring + wk * kRingBytes);
-      } else if (lane == 0) {
+      } else {
         issue_worker<D, kWide>(sm, wk, q_smem + wk * Sh::kQTile, ring + wk * kRingBytes, tmem);
       }
     }
@@ -803,13 +853,16 @@ __global__ void __launch_bounds__(Shape<D, kWide>::kThreads, 1)
         if (ln.q_issued > 0) mbar_wait_bounded(&sm.q_full[w], par(ln.q_issued - 1));
       }
     }
-    if ((warp == 1 || warp == 3) && (warp >> 1) < Sh::kWorkers && lane == 0) {
+    if ((warp == 1 || warp == 3) && (warp >> 1) < Sh::kWorkers) {
       // an issuer's products: a commit on a barrier that nothing else uses any more
       unsigned long long *bar = &sm.lane[warp >> 1].seg_full[0];
-      mbar_init(bar, 1);
-      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-      tc_commit(smem_u32(bar));
-      mbar_wait_bounded(bar, 0);
+      if (elect_one()) {
+        mbar_init(bar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        tc_commit(smem_u32(bar));
+        mbar_wait_bounded(bar, 0);
+      }
+      __syncwarp();
     }
     __syncthreads();
   }
