@@ -65,18 +65,19 @@ namespace svw {
 namespace {
 
 constexpr int kRows = 128;     // rows of a score tile (the MMA's M)
-constexpr int kCols = 64;      // keys of a softmax thread
 constexpr int kSegRing = 4;
 constexpr int kMaxGrid = 152;  // CTAs: one per SM
 constexpr float kGrow = 8.f;   // the reference lags the maximum by at most this (base 2)
 constexpr float kNaN = __builtin_nanf("");
 
+constexpr int kWideGroups = 1;
 template <int D, bool kWide>
 struct Shape {
   static constexpr int kWorkers = kWide ? 1 : 2;           // of a CTA
   static constexpr int kKeys = kWide ? 128 : 64;           // keys of a tile
   static constexpr int kTiles = kWide ? 2 : 1;             // row tiles of a unit, at most
-  static constexpr int kGroups = kWide ? 2 : 1;            // softmax warpgroups of a stage
+  static constexpr int kGroups = (kWide && kWideGroups == 2) ? 2 : 1;                    // softmax warpgroups of a stage
+  static constexpr int kCols = kKeys / kGroups;            // keys of a softmax thread
   static constexpr int kSoftWarps = 4 * kGroups * (kWide ? 2 : 1);  // softmax warps of a worker
   static constexpr int kThreads = 128 + 256 * kGroups;     // loaders and issuers; softmax
   static constexpr int kUnitCost = kWide ? 1 : 2;          // a unit's fixed cost on the line, in key tiles
@@ -116,7 +117,7 @@ struct Lane {  // of a worker
   int32_t first_req;
   int64_t first_at;
 };
-template <int kRing, int kWorkers>
+template <int kRing, int kWorkers, bool kPairs>
 struct Control {
   Lane<kRing> lane[kWorkers];
   unsigned long long q_full[2], q_empty[2];
@@ -124,7 +125,7 @@ struct Control {
   uint32_t tmem;
   int32_t err;
   int64_t scan[20];
-  float row[kWorkers == 1 ? 2 : 1][2][kWorkers == 1 ? kRows : 1];  // what the two threads of a row tell each other
+  float row[kPairs ? 2 : 1][2][kPairs ? kRows : 1];  // what the two threads of a row tell each other
 };
 
 using Joint = AttendJoint;
@@ -470,10 +471,10 @@ __device__ __forceinline__ void issue_worker(C &sm, int wk, uint32_t q_smem, uin
   };
   auto output = [&](int u, const At &t, bool acc) {
     const uint64_t va = sw128(ring + t.slot * Sh::kTile, Sh::kHalf);
-    // the weights of 64 keys lie in 32 columns over the first half of their scores
+    // a thread's weights lie over the first half of its scores
 #pragma unroll
     for (int h = 0; h < Sh::kKeys / 64; ++h)
-      mma_ts_x4(tmem + 256 + (kWide ? u : wk) * D, s_col(u) + h * kCols, va + h * 512, id_o, (acc || h > 0) ? 1u : 0u);
+      mma_ts_x4(tmem + 256 + (kWide ? u : wk) * D, s_col(u) + h * (Sh::kGroups == 2 ? 64 : 32), va + h * 512, id_o, (acc || h > 0) ? 1u : 0u);
   };
   auto release = [&](const At &t) { tc_commit(smem_u32(&ln.empty[t.slot])); };
   while (ok) {
@@ -546,17 +547,19 @@ template <int D, bool kWide, typename C>
 __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s, int h, unsigned char *ring_ptr,
                                               uint32_t tmem) {
   using Sh = Shape<D, kWide>;
+  constexpr int kCols = Sh::kCols;
+  constexpr bool kPair = Sh::kGroups == 2;  // two threads to a row
   auto &ln = sm.lane[kWide ? 0 : s];
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
   const int row = quad * 32 + lane;
   const int G = a.Hq / a.Hkv;
   const int tok_of_row = row / G, head_of_row = row - tok_of_row * G;
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-  const uint32_t t_s = tmem + lanes + s * 128 + (kWide ? h * kCols : 0);
+  const uint32_t t_s = tmem + lanes + s * 128 + h * kCols;
   const uint32_t t_o = tmem + lanes + 256 + s * D;
   const float k2 = a.scale * kLog2e;
-  constexpr int kMyCols = kWide ? D / 2 : D;  // columns of the output that this thread looks after
-  const int oc0 = kWide ? h * kMyCols : 0;
+  constexpr int kMyCols = D / Sh::kGroups;  // columns of the output that this thread looks after
+  const int oc0 = h * kMyCols;
   // the two threads of a row
   auto meet = [&] { named_sync(1 + s * 4 + quad, 64); };
   int32_t count = 0, k = 0, steps = 0, sc[2] = {0, 0};  // ring tiles, segments, outputs, score tiles by buffer
@@ -581,12 +584,12 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
       if (!(ok = warp_wait(&sm.s_full[kWide ? s : 2 * s + u], par(sc[u])))) break;
       ++sc[u];
       tc_after();
-      const uint32_t t_su = t_s + u * kCols;
+      const uint32_t t_su = t_s + u * 64;
       if (warp_live) {
-        const int32_t c0 = key + (kWide ? h * kCols : 0);  // this thread's first key
+        const int32_t c0 = key + h * kCols;  // this thread's first key
         float x[kCols];
-        tmem_ld32(t_su, x);
-        tmem_ld32(t_su + 32, x + 32);
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) tmem_ld32(t_su + c, x + c);
         tmem_wait_ld();
         if (!__all_sync(0xffffffffu, c0 >= lo && c0 + kCols <= hi)) {
           const int32_t from = c0 - lo;  // key c0 + c is seen where 0 <= c + from < hi - lo
@@ -599,7 +602,7 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
 #pragma unroll
         for (int c = 4; c < kCols; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
         float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * k2;
-        if (kWide) {
+        if (kPair) {
           sm.row[s][h][row] = top;
           meet();
           top = fmaxf(top, sm.row[s][1 - h][row]);
@@ -663,7 +666,7 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
     if (!(ok = warp_wait(&ln.o_full, par(k)))) break;
     tc_after();
     if (warp_live) {
-      if (kWide) {
+      if (kPair) {
         sm.row[s][h][row] = l;  // the maxima have been read: the outputs waited for it
         meet();
         const float l0 = sm.row[s][0][row], l1 = sm.row[s][1][row];
@@ -718,7 +721,7 @@ __global__ void __launch_bounds__(Shape<D, kWide>::kThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttendArgs a) {
   using Sh = Shape<D, kWide>;
-  using C = Control<Sh::kRing, Sh::kWorkers>;
+  using C = Control<Sh::kRing, Sh::kWorkers, Sh::kGroups == 2>;
   static_assert(sizeof(C) <= Sh::kControl, "control block");
   constexpr int kWarps = Sh::kThreads / 32;
   extern __shared__ __align__(1024) unsigned char dyn[];
@@ -824,7 +827,13 @@ __global__ void __launch_bounds__(Shape<D, kWide>::kThreads, 1)
   constexpr int kRingBytes = Sh::kRing * Sh::kTile;
 
   if (warp < 4) {
-    if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (kWide) {
+      // the launch has 96 (168) registers for each of 640 (384) threads: 128 * 64 + 512 * 104 (128 * 72 + 256 * 216)
+      if (Sh::kGroups == 2)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+      else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    }
     const int wk = warp >> 1;
     if (wk < Sh::kWorkers) {
       if ((warp & 1) == 0) {
@@ -836,7 +845,12 @@ __global__ void __launch_bounds__(Shape<D, kWide>::kThreads, 1)
       }
     }
   } else {
-    if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    if (kWide) {
+      if (Sh::kGroups == 2)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+      else
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    }
     const int g = (warp - 4) >> 2;  // softmax warpgroup: stage, then half
     const int s = g / Sh::kGroups, h = g % Sh::kGroups;
     softmax_stage<D, kWide>(a, sm, s, h, dyn + (ring - base) + (kWide ? 0 : s * kRingBytes), tmem);
