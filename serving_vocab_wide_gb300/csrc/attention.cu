@@ -36,9 +36,9 @@
 //           the ring held 160 KB of which two slots were under way, 2.0 us a
 //           tile against 1.47 us of its bytes' time.
 //   wide    (more: prompts; bound by the products) the CTA is one worker, a unit
-//           is two row tiles, one a stage, reading the same key tiles of 128;
-//           two threads share a row, 64 keys each, and exchange their maxima
-//           through shared memory.
+//           is two row tiles, one a stage, reading the same key tiles of 128.
+//           (Two threads to a row, 64 keys each, exchanging their maxima: 557 us
+//           against 469, more warps contending for the exponentials.)
 // The reference: exp2(x - M) is exact algebra for any M, so M follows the
 // row's maximum only when that has outgrown it by more than 8 (a factor 256:
 // far from overflow, and the same relative rounding of P); only then are l
@@ -66,20 +66,18 @@ namespace {
 
 constexpr int kRows = 128;     // rows of a score tile (the MMA's M)
 constexpr int kSegRing = 4;
+constexpr int kThreads = 384;  // loaders and issuers; two softmax warpgroups, one a stage
 constexpr int kMaxGrid = 152;  // CTAs: one per SM
 constexpr float kGrow = 8.f;   // the reference lags the maximum by at most this (base 2)
 constexpr float kNaN = __builtin_nanf("");
 
-constexpr int kWideGroups = 1;
 template <int D, bool kWide>
 struct Shape {
   static constexpr int kWorkers = kWide ? 1 : 2;           // of a CTA
   static constexpr int kKeys = kWide ? 128 : 64;           // keys of a tile
   static constexpr int kTiles = kWide ? 2 : 1;             // row tiles of a unit, at most
-  static constexpr int kGroups = (kWide && kWideGroups == 2) ? 2 : 1;                    // softmax warpgroups of a stage
-  static constexpr int kCols = kKeys / kGroups;            // keys of a softmax thread
-  static constexpr int kSoftWarps = 4 * kGroups * (kWide ? 2 : 1);  // softmax warps of a worker
-  static constexpr int kThreads = 128 + 256 * kGroups;     // loaders and issuers; softmax
+  static constexpr int kBufs = kWide ? 1 : 2;              // score buffers of a stage
+  static constexpr int kSoftWarps = kWide ? 8 : 4;         // softmax warps of a worker
   static constexpr int kUnitCost = kWide ? 1 : 2;          // a unit's fixed cost on the line, in key tiles
   static constexpr int kHalves = D / 64;                   // 128-byte columns of a tile
   static constexpr int kQTile = kRows * D * 2;             // bytes of a query tile
@@ -110,22 +108,21 @@ template <int kRing>
 struct Lane {  // of a worker
   unsigned long long full[kRing], empty[kRing];
   unsigned long long seg_full[kSegRing], seg_empty[kSegRing];
-  unsigned long long o_full, o_free, o_step;
   Segment seg[kSegRing];
   int32_t seg_bad[kSegRing];
   int32_t issued, q_issued;  // ring tiles, query tiles
   int32_t first_req;
   int64_t first_at;
 };
-template <int kRing, int kWorkers, bool kPairs>
+template <int kRing, int kWorkers>
 struct Control {
   Lane<kRing> lane[kWorkers];
   unsigned long long q_full[2], q_empty[2];
-  unsigned long long s_full[4], p_full[4];  // by score buffer: stage, or 2 * worker + buffer
+  unsigned long long s_full[4], p_full[4];  // 2 * stage + score buffer
+  unsigned long long o_full[2], o_free[2], o_step[2];  // by stage: a segment's outputs; read; each tile's (narrow)
   uint32_t tmem;
   int32_t err;
   int64_t scan[20];
-  float row[kPairs ? 2 : 1][2][kPairs ? kRows : 1];  // what the two threads of a row tell each other
 };
 
 using Joint = AttendJoint;
@@ -434,7 +431,9 @@ __device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtens
 }
 
 // ------------------------------ the MMA issuer ------------------------------
-// A converged warp; one of its threads issues.
+// A converged warp per worker; one of its threads issues.  (An issuer for each
+// stage of the wide form, their products interleaving as they come, took 582 us
+// against 469 on two prompts of 2048 new tokens over 8192.)
 template <int D, bool kWide, typename C>
 __device__ __forceinline__ void issue_worker(C &sm, int wk, uint32_t q_smem, uint32_t ring, uint32_t tmem) {
   using Sh = Shape<D, kWide>;
@@ -455,26 +454,21 @@ __device__ __forceinline__ void issue_worker(C &sm, int wk, uint32_t q_smem, uin
   At kt = {0, 0}, vt = {1, 0};
   int32_t k = 0, sc[2] = {0, 0};
   bool ok = true;
-  auto wait_ring = [&](const At &t) {
-    ok = ok && warp_wait(&ln.full[t.slot], t.parity);
-    return ok;
-  };
-  // score buffer u: stage u (wide), buffer u of worker wk (narrow)
-  auto s_col = [&](int u) { return tmem + (kWide ? u * 128 : wk * 128 + u * 64); };
-  auto s_bar = [&](int u) { return kWide ? u : 2 * wk + u; };
-  auto scores = [&](int u, const At &t) {  // by the elected thread
-    const uint64_t qa = sw128(q_smem + (kWide ? u * Sh::kQTile : 0), 16), ka = sw128(ring + t.slot * Sh::kTile, 16);
+  auto wait_ring = [&](const At &t) { return ok = ok && warp_wait(&ln.full[t.slot], t.parity); };
+  // by the elected thread: into score buffer u of stage st, from it into the stage's output
+  auto scores = [&](int st, int u, const At &t) {
+    const uint64_t qa = sw128(q_smem + (kWide ? st * Sh::kQTile : 0), 16), ka = sw128(ring + t.slot * Sh::kTile, 16);
 #pragma unroll
     for (int h = 0; h < Sh::kHalves; ++h)
-      mma_ss_x4(s_col(u), qa + h * (Sh::kQHalf >> 4), ka + h * (Sh::kHalf >> 4), id_s, h);
-    tc_commit(smem_u32(&sm.s_full[s_bar(u)]));
+      mma_ss_x4(tmem + st * 128 + u * 64, qa + h * (Sh::kQHalf >> 4), ka + h * (Sh::kHalf >> 4), id_s, h);
+    tc_commit(smem_u32(&sm.s_full[2 * st + u]));
   };
-  auto output = [&](int u, const At &t, bool acc) {
+  auto output = [&](int st, int u, const At &t, bool acc) {
     const uint64_t va = sw128(ring + t.slot * Sh::kTile, Sh::kHalf);
-    // a thread's weights lie over the first half of its scores
 #pragma unroll
-    for (int h = 0; h < Sh::kKeys / 64; ++h)
-      mma_ts_x4(tmem + 256 + (kWide ? u : wk) * D, s_col(u) + h * (Sh::kGroups == 2 ? 64 : 32), va + h * 512, id_o, (acc || h > 0) ? 1u : 0u);
+    for (int h = 0; h < Sh::kKeys / 64; ++h)  // a row's weights of 64 keys take 32 columns
+      mma_ts_x4(tmem + 256 + st * D, tmem + st * 128 + u * 64 + h * 32, va + h * 512, id_o, (acc || h > 0) ? 1u : 0u);
+    if (!kWide) tc_commit(smem_u32(&sm.o_step[st]));
   };
   auto release = [&](const At &t) { tc_commit(smem_u32(&ln.empty[t.slot])); };
   while (ok) {
@@ -484,48 +478,53 @@ __device__ __forceinline__ void issue_worker(C &sm, int wk, uint32_t q_smem, uin
     __syncwarp();
     if (n == 0) break;
     if (elect_one()) mbar_arrive(&ln.seg_empty[sl]);
-    if (!(ok = warp_wait(&sm.q_full[wk], par(k))) || !wait_ring(kt)) break;
-    tc_after();
-    if (elect_one()) {
-      scores(0, kt);
-      if (kWide) scores(1, kt);
-      release(kt);
-    }
-    kt.two_on();
-    if (!kWide && n > 1) {
-      if (!wait_ring(kt)) break;
-      tc_after();
-      if (elect_one()) {
-        scores(1, kt);
-        release(kt);
+    if (!(ok = warp_wait(&sm.q_full[wk], par(k)))) break;
+    // the first scores: both stages of the wide form, both buffers of the narrow one
+#pragma unroll
+    for (int u = 0; u < (kWide ? 1 : 2); ++u) {
+      if (u < n) {
+        if (!wait_ring(kt)) break;
+        tc_after();
+        if (elect_one()) {
+          scores(kWide ? 0 : wk, u, kt);
+          if (kWide) scores(1, 0, kt);
+          release(kt);
+        }
+        kt.two_on();
       }
-      kt.two_on();
     }
     constexpr int kLead = kWide ? 1 : 2;  // a score buffer's next key tile
     for (int32_t j = 0; j < n && ok; ++j) {
       const bool more = j + kLead < n;
       if (!wait_ring(vt)) break;
+      if (kWide && more && !wait_ring(kt)) break;  // there long before; narrow: its values' weights come first
 #pragma unroll
       for (int i = 0; i < (kWide ? 2 : 1); ++i) {
-        const int u = kWide ? i : (j & 1);
-        if (!(ok = warp_wait(&sm.p_full[s_bar(u)], par(sc[u])))) break;
-        ++sc[u];
-        if (i == 0 && j == 0 && k > 0 && !(ok = warp_wait(&ln.o_free, par(k - 1)))) break;
+        const int st = kWide ? i : wk, u = kWide ? 0 : (j & 1);
+        if (!(ok = warp_wait(&sm.p_full[2 * st + u], par(sc[kWide ? i : u])))) break;
+        ++sc[kWide ? i : u];
+        if (j == 0 && k > 0 && !(ok = warp_wait(&sm.o_free[st], par(k - 1)))) break;
         tc_after();
         if (elect_one()) {
-          output(u, vt, j > 0);
-          if (!kWide) tc_commit(smem_u32(&ln.o_step));
+          output(st, u, vt, j > 0);
           if (!kWide || i == 1) release(vt);
-        }
-        if (more && !wait_ring(kt)) break;
-        tc_after();
-        if (elect_one()) {
-          if (more) {
-            scores(u, kt);
-            if (!kWide || i == 1) release(kt);
+          if (kWide && more) {
+            scores(st, 0, kt);
+            if (i == 1) release(kt);
           }
-          // every score of the segment is under way: the query buffer may be refilled after them
-          if (j == max(0, n - 1 - kLead) && (!kWide || i == 1)) tc_commit(smem_u32(&sm.q_empty[wk]));
+          // every score of the segment is under way: the queries may be replaced after them
+          if (kWide && i == 1 && j == max(0, n - 2)) tc_commit(smem_u32(&sm.q_empty[0]));
+        }
+        if (!kWide) {
+          if (more && !wait_ring(kt)) break;
+          tc_after();
+          if (elect_one()) {
+            if (more) {
+              scores(st, u, kt);
+              release(kt);
+            }
+            if (j == max(0, n - 3)) tc_commit(smem_u32(&sm.q_empty[wk]));
+          }
         }
       }
       vt.two_on();
@@ -533,8 +532,11 @@ __device__ __forceinline__ void issue_worker(C &sm, int wk, uint32_t q_smem, uin
     }
     if (!ok) break;
     if (elect_one()) {
-      tc_commit(smem_u32(&ln.o_full));
-      mbar_arrive(&ln.o_full);  // carries what the loader wrote about the segment
+#pragma unroll
+      for (int i = 0; i < (kWide ? 2 : 1); ++i) {
+        tc_commit(smem_u32(&sm.o_full[kWide ? i : wk]));
+        mbar_arrive(&sm.o_full[kWide ? i : wk]);  // carries what the loader wrote about the segment
+      }
     }
     ++k;
   }
@@ -542,26 +544,20 @@ __device__ __forceinline__ void issue_worker(C &sm, int wk, uint32_t q_smem, uin
 }
 
 // ------------------------------- the softmax --------------------------------
-// Stage s; half h of the keys (wide).  A thread has one row and 64 keys.
+// Of stage s: a thread has one row and all keys of a tile.
 template <int D, bool kWide, typename C>
-__device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s, int h, unsigned char *ring_ptr,
+__device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s, unsigned char *ring_ptr,
                                               uint32_t tmem) {
   using Sh = Shape<D, kWide>;
-  constexpr int kCols = Sh::kCols;
-  constexpr bool kPair = Sh::kGroups == 2;  // two threads to a row
   auto &ln = sm.lane[kWide ? 0 : s];
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
   const int row = quad * 32 + lane;
   const int G = a.Hq / a.Hkv;
   const int tok_of_row = row / G, head_of_row = row - tok_of_row * G;
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-  const uint32_t t_s = tmem + lanes + s * 128 + h * kCols;
+  const uint32_t t_s = tmem + lanes + s * 128;
   const uint32_t t_o = tmem + lanes + 256 + s * D;
   const float k2 = a.scale * kLog2e;
-  constexpr int kMyCols = D / Sh::kGroups;  // columns of the output that this thread looks after
-  const int oc0 = h * kMyCols;
-  // the two threads of a row
-  auto meet = [&] { named_sync(1 + s * 4 + quad, 64); };
   int32_t count = 0, k = 0, steps = 0, sc[2] = {0, 0};  // ring tiles, segments, outputs, score tiles by buffer
   bool ok = true;
   while (true) {
@@ -579,57 +575,51 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
     if (!live) hi = INT32_MAX, lo = 0;  // rows of no token: never masked, never looked at
     float M = -INFINITY, l = 0.f;
     for (int32_t j = 0; j < g.tiles; ++j) {
-      const int u = kWide ? 0 : (j & 1);  // score buffer
+      const int u = Sh::kBufs == 1 ? 0 : (j & 1);  // score buffer
       const int32_t key = g.key0 + j * Sh::kKeys;
-      if (!(ok = warp_wait(&sm.s_full[kWide ? s : 2 * s + u], par(sc[u])))) break;
+      if (!(ok = warp_wait(&sm.s_full[2 * s + u], par(sc[u])))) break;
       ++sc[u];
       tc_after();
       const uint32_t t_su = t_s + u * 64;
       if (warp_live) {
-        const int32_t c0 = key + h * kCols;  // this thread's first key
-        float x[kCols];
+        float x[Sh::kKeys];
 #pragma unroll
-        for (int c = 0; c < kCols; c += 32) tmem_ld32(t_su + c, x + c);
+        for (int c = 0; c < Sh::kKeys; c += 32) tmem_ld32(t_su + c, x + c);
         tmem_wait_ld();
-        if (!__all_sync(0xffffffffu, c0 >= lo && c0 + kCols <= hi)) {
-          const int32_t from = c0 - lo;  // key c0 + c is seen where 0 <= c + from < hi - lo
+        if (!__all_sync(0xffffffffu, key >= lo && key + Sh::kKeys <= hi)) {
+          const int32_t from = key - lo;  // key + c is seen where 0 <= c + from < hi - lo
           const uint32_t seen = static_cast<uint32_t>(max(0, hi - lo));
 #pragma unroll
-          for (int c = 0; c < kCols; ++c)
+          for (int c = 0; c < Sh::kKeys; ++c)
             if (static_cast<uint32_t>(c + from) >= seen) x[c] = -INFINITY;
         }
         float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int c = 4; c < kCols; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
-        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * k2;
-        if (kPair) {
-          sm.row[s][h][row] = top;
-          meet();
-          top = fmaxf(top, sm.row[s][1 - h][row]);
-        }
+        for (int c = 4; c < Sh::kKeys; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * k2;
         const bool grow = live && (top > M + kGrow || (M == -INFINITY && top > M));
         const float f = grow ? (M == -INFINITY ? 0.f : ex2(M - top)) : 1.f;
         if (grow) M = top;
         l *= f;
         if (j > 0 && __any_sync(0xffffffffu, grow)) {
           // the outputs so far are complete (wide: the scores' arrival said so)
-          if (!kWide && !(ok = warp_wait(&ln.o_step, par(steps + j - 1)))) break;
+          if (!kWide && !(ok = warp_wait(&sm.o_step[s], par(steps + j - 1)))) break;
           if (!kWide) tc_after();
 #pragma unroll
-          for (int c = 0; c < kMyCols; c += 16) {
+          for (int c = 0; c < D; c += 16) {
             float o[16];
-            tmem_ld16(t_o + oc0 + c, o);
+            tmem_ld16(t_o + c, o);
             tmem_wait_ld();
 #pragma unroll
             for (int v = 0; v < 16; ++v) o[v] *= f;
-            tmem_st16(t_o + oc0 + c, o);
+            tmem_st16(t_o + c, o);
           }
         }
         const float ref = (M == -INFINITY) ? 0.f : M;
         const float2 kk = make_float2(k2, k2), nr = make_float2(-ref, -ref);
         float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
-        for (int c = 0; c < kCols; c += 16) {
+        for (int c = 0; c < Sh::kKeys; c += 16) {
           uint32_t w[8];
 #pragma unroll
           for (int v = 0; v < 8; ++v) {
@@ -659,27 +649,20 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
       tmem_wait_st();
       tc_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full[kWide ? s : 2 * s + u]);
+      if (lane == 0) mbar_arrive(&sm.p_full[2 * s + u]);
     }
     if (!ok) break;
     // ---- the segment's results ----
-    if (!(ok = warp_wait(&ln.o_full, par(k)))) break;
+    if (!(ok = warp_wait(&sm.o_full[s], par(k)))) break;
     tc_after();
     if (warp_live) {
-      if (kPair) {
-        sm.row[s][h][row] = l;  // the maxima have been read: the outputs waited for it
-        meet();
-        const float l0 = sm.row[s][0][row], l1 = sm.row[s][1][row];
-        l = l0 + l1;
-        meet();  // before the next segment's maxima
-      }
       if (*reinterpret_cast<volatile int32_t *>(&ln.seg_bad[sl]) != 0) l = kNaN;
       const int32_t tok = g.tok0 + tile * a.tile_tokens + tok_of_row;
       const int64_t orow = static_cast<int64_t>(tok) * a.Hq + g.hk * G + head_of_row;
       const int64_t prow = static_cast<int64_t>(max(g.part, 0)) * a.part_rows + tile * kRows + row;
       const float inv = (g.part >= 0) ? 1.f : (l == 0.f ? 0.f : 1.f / l);
 #pragma unroll 1
-      for (int c = oc0; c < oc0 + kMyCols; c += 32) {
+      for (int c = 0; c < D; c += 32) {
         float o[32];
         tmem_ld32(t_o + c, o);
         tmem_wait_ld();
@@ -696,7 +679,7 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
           for (int v = 0; v < 8; ++v) dst[v] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
         }
       }
-      if (live && h == 0) {
+      if (live) {
         if (g.part >= 0)
           a.part_ml[prow] = make_float2(M, l);
         else if (a.lse)
@@ -706,7 +689,7 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
     tc_before();
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(&ln.o_free);
+      mbar_arrive(&sm.o_free[s]);
       mbar_arrive(&ln.seg_empty[sl]);
     }
     count += 2 * g.tiles;
@@ -717,13 +700,13 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
 }
 
 template <int D, bool kWide>
-__global__ void __launch_bounds__(Shape<D, kWide>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttendArgs a) {
   using Sh = Shape<D, kWide>;
-  using C = Control<Sh::kRing, Sh::kWorkers, Sh::kGroups == 2>;
+  using C = Control<Sh::kRing, Sh::kWorkers>;
   static_assert(sizeof(C) <= Sh::kControl, "control block");
-  constexpr int kWarps = Sh::kThreads / 32;
+  constexpr int kWarps = kThreads / 32;
   extern __shared__ __align__(1024) unsigned char dyn[];
   C &sm = *reinterpret_cast<C *>(dyn);
   const uint32_t base = smem_u32(dyn);
@@ -746,9 +729,6 @@ __global__ void __launch_bounds__(Shape<D, kWide>::kThreads, 1)
         mbar_init(&ln.seg_full[s], 1);
         mbar_init(&ln.seg_empty[s], Sh::kSoftWarps + 1);
       }
-      mbar_init(&ln.o_full, 2);
-      mbar_init(&ln.o_free, Sh::kSoftWarps);
-      mbar_init(&ln.o_step, 1);
       ln.issued = 0;
       ln.q_issued = 0;
       ln.first_req = a.N;
@@ -757,10 +737,13 @@ __global__ void __launch_bounds__(Shape<D, kWide>::kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.q_full[s], 1);
       mbar_init(&sm.q_empty[s], 1);
+      mbar_init(&sm.o_full[s], 2);
+      mbar_init(&sm.o_free[s], 4);
+      mbar_init(&sm.o_step[s], 1);
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&sm.s_full[s], 1);
-      mbar_init(&sm.p_full[s], 4 * Sh::kGroups);
+      mbar_init(&sm.p_full[s], 4);
     }
     sm.err = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -776,7 +759,7 @@ __global__ void __launch_bounds__(Shape<D, kWide>::kThreads, 1)
   }
 
   // ---- the line, and the workers' stretches of it ----
-  const int32_t per = (a.N + Sh::kThreads - 1) / Sh::kThreads;
+  const int32_t per = (a.N + kThreads - 1) / kThreads;
   const int32_t r0 = min(a.N, tid * per), r1 = min(a.N, r0 + per);
   int64_t mine = 0;
   bool wrong = false;
@@ -826,34 +809,24 @@ __global__ void __launch_bounds__(Shape<D, kWide>::kThreads, 1)
   const uint32_t q_smem = base + Sh::kControl, ring = q_smem + 2 * Sh::kQTile;
   constexpr int kRingBytes = Sh::kRing * Sh::kTile;
 
+  // a loader and an issuer per worker; softmax warps from the fifth on
   if (warp < 4) {
-    if (kWide) {
-      // the launch has 96 (168) registers for each of 640 (384) threads: 128 * 64 + 512 * 104 (128 * 72 + 256 * 216)
-      if (Sh::kGroups == 2)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-      else
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    }
+    // the launch has 168 registers for each of 384 threads: 128 * 72 + 256 * 216
+    if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int wk = warp >> 1;
     if (wk < Sh::kWorkers) {
-      if ((warp & 1) == 0) {
+      if (warp & 1) {
+        issue_worker<D, kWide>(sm, wk, q_smem + wk * Sh::kQTile, ring + wk * kRingBytes, tmem);
+      } else {
         const int64_t id = static_cast<int64_t>(blockIdx.x) * Sh::kWorkers + wk;
         load_worker<D, kWide>(tmQ, tmK, tmV, a, sm, wk, static_cast<int>(id), W, W * id / workers,
                               W * (id + 1) / workers, workers, q_smem + wk * Sh::kQTile, ring + wk * kRingBytes);
-      } else {
-        issue_worker<D, kWide>(sm, wk, q_smem + wk * Sh::kQTile, ring + wk * kRingBytes, tmem);
       }
     }
   } else {
-    if (kWide) {
-      if (Sh::kGroups == 2)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-      else
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    }
-    const int g = (warp - 4) >> 2;  // softmax warpgroup: stage, then half
-    const int s = g / Sh::kGroups, h = g % Sh::kGroups;
-    softmax_stage<D, kWide>(a, sm, s, h, dyn + (ring - base) + (kWide ? 0 : s * kRingBytes), tmem);
+    if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int st = (warp - 4) >> 2;
+    softmax_stage<D, kWide>(a, sm, st, dyn + (ring - base) + (kWide ? 0 : st * kRingBytes), tmem);
   }
   __syncthreads();
   if (sm.err) {
@@ -869,7 +842,7 @@ __global__ void __launch_bounds__(Shape<D, kWide>::kThreads, 1)
     }
     if ((warp == 1 || warp == 3) && (warp >> 1) < Sh::kWorkers) {
       // an issuer's products: a commit on a barrier that nothing else uses any more
-      unsigned long long *bar = &sm.lane[warp >> 1].seg_full[0];
+      unsigned long long *bar = &sm.o_step[warp >> 1];
       if (elect_one()) {
         mbar_init(bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1015,7 +988,7 @@ cudaError_t launch(AttendArgs a, cudaStream_t st) {
   const int P = sms[dev] < kMaxGrid ? sms[dev] : kMaxGrid;
   a.part_rows = Sh::kTiles * kRows;
   void *tm = timer_before("paged_attention", st);
-  paged_attention_kernel<D, kWide><<<P, Sh::kThreads, Sh::kSmem, st>>>(mq, mk, mv, a);
+  paged_attention_kernel<D, kWide><<<P, kThreads, Sh::kSmem, st>>>(mq, mk, mv, a);
   timer_after(tm, st);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
