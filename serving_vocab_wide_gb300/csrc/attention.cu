@@ -860,52 +860,72 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // A unit that workers c .. last shared: each row's parts brought to one
-// reference and added, in the order of the line.  A warp per row, 32 parts'
-// references and sums at a time, eight parts' outputs under way.
+// reference and added, in the order of the line.  A warp per row at a time; the
+// first eight parts' outputs are under way beside the references and sums (one
+// after the other, eight rows a warp, the joins of two prompts took 50 us).
+constexpr int kJoinRows = 2;  // rows of a warp, at most
 template <int D>
-__global__ void __launch_bounds__(256) attention_join(const __grid_constant__ AttendArgs a, int workers) {
-  constexpr int E = D / 32;
+__global__ void __launch_bounds__(256, 4) attention_join(const __grid_constant__ AttendArgs a, int workers) {
+  constexpr int E = D / 32, kAhead = 8;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x;
   const Joint jt = a.joints[c];
-  if (jt.last < 0) return;
-  const int lane = threadIdx.x & 31, warps = static_cast<int>(gridDim.y) * 8;
   const int G = a.Hq / a.Hkv;
   const int rows0 = jt.ntok0 * G, rows = rows0 + jt.ntok1 * G;
+  const int lane = threadIdx.x & 31, warps = static_cast<int>(gridDim.y) * 8;
+  int r = static_cast<int>(blockIdx.y) * 8 + (threadIdx.x >> 5);
+  if (jt.last < 0) return;
   const int n = jt.last - c + 1;
   // a worker whose stretch is empty (fewer tiles than workers) has no part
   auto some = [&](int q) {
     return q == 0 || jt.total >= workers || jt.total * (c + q) / workers < jt.total * (c + q + 1) / workers;
   };
-  for (int r = static_cast<int>(blockIdx.y) * 8 + (threadIdx.x >> 5); r < rows; r += warps) {
+  for (; r < rows; r += warps) {
     const int tile = r >= rows0 ? 1 : 0, in_tile = r - tile * rows0;
     const int prow = tile * kRows + in_tile;
     // the part of worker c + q: its last segment for the first, its first one for the others
-    auto part = [&](int q) { return static_cast<int64_t>(2 * (c + q) + (q == 0 ? 1 : 0)) * a.part_rows + prow; };
-    float M = -INFINITY;
-    for (int q = lane; q < n; q += 32)
-      if (some(q)) M = fmaxf(M, a.part_ml[part(q)].x);
+    const uint32_t first = static_cast<uint32_t>(2 * c * a.part_rows + prow);  // rows of parts: below 2^18
+    auto part = [&](int q) { return first + static_cast<uint32_t>((q == 0 ? 1 : 2 * q) * a.part_rows); };
+    auto load = [&](int q, float *o) {
+      const float *src = a.part_o + (part(q) * D + lane * E);
+      if (E == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+        o[0] = v.x, o[1] = v.y, o[E - 2] = v.z, o[E - 1] = v.w;
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+        o[0] = v.x, o[1] = v.y;
+      }
+    };
+    float o[kAhead][E];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int u = 0; u < kAhead; ++u)
+      if (u < n) load(u, o[u]);
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < n && some(lane)) ml = __ldcg(a.part_ml + part(lane));
+    float M = ml.x;
+    for (int q = lane + 32; q < n; q += 32)
+      if (some(q)) M = fmaxf(M, __ldcg(&a.part_ml[part(q)].x));
+#pragma unroll
+    for (int u = 16; u > 0; u >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, u));
     float l = 0.f, acc[E];
 #pragma unroll
     for (int u = 0; u < E; ++u) acc[u] = 0.f;
     for (int q0 = 0; q0 < n; q0 += 32) {
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (q0 + lane < n && some(q0 + lane)) ml = a.part_ml[part(q0 + lane)];
+      if (q0 > 0) {
+        ml = make_float2(-INFINITY, 0.f);
+        if (q0 + lane < n && some(q0 + lane)) ml = __ldcg(a.part_ml + part(q0 + lane));
+      }
       const float w = (ml.x == -INFINITY) ? 0.f : ex2(ml.x - M);
       const float wl = (ml.x == -INFINITY) ? ml.y : w * ml.y;  // an empty part has 0, a bad one NaN
       const int m = min(32, n - q0);
-      for (int b = 0; b < m; b += 8) {
-        float o[8][E];
+      for (int b = 0; b < m; b += kAhead) {
+        if (q0 + b > 0) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float *src = a.part_o + part(min(q0 + b + u, n - 1)) * D + lane * E;
-#pragma unroll
-          for (int v = 0; v < E; ++v) o[u][v] = __ldcg(src + v);
+          for (int u = 0; u < kAhead; ++u)
+            if (b + u < m) load(q0 + b + u, o[u]);
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < kAhead; ++u) {
           const float wu = __shfl_sync(0xffffffffu, w, min(31, b + u)), lu = __shfl_sync(0xffffffffu, wl, min(31, b + u));
           if (b + u < m) {
             l += lu;
@@ -996,7 +1016,7 @@ cudaError_t launch(AttendArgs a, cudaStream_t st) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(P * Sh::kWorkers), 4, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(P * Sh::kWorkers), Sh::kTiles * kRows / 8 / kJoinRows, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = st;
   cfg.attrs = attr;
