@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 import threading
 
 from .build import LIB_PATH, build  # noqa: F401
@@ -459,14 +460,24 @@ def _need_numel(names, ts, n):
             raise SvwError(f"{name} must have {n} elements")
 
 
+def _off(t, dtype, index):
+    """Whether a tensor is not contiguous, of this type and on this GPU (None is fine)."""
+    return t is not None and (t.dtype is not dtype or t.get_device() != index or not t.is_contiguous())
+
+
 def _addr(t):
     return 0 if t is None else t.data_ptr()
 
 
 def _stream_of(stream, index):
     """The handle of `stream`, or of the current stream of GPU `index`."""
+    return _torch()._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+@functools.lru_cache(maxsize=None)
+def _torch():
     import torch
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    return torch
 
 
 def _lent(stream, *ts):
@@ -494,76 +505,100 @@ def logits_adjust(logits, cu_draft, draft_tokens=None, *, history=None, cu_histo
     (in place).  `total_draft_rows` (= cu_draft[-1]) may be passed to avoid a
     device read.
     """
-    import torch
+    torch = _torch()
+    i32, f32 = torch.int32, torch.float32
     code = _dtype_code(logits)
-    if not logits.is_cuda or logits.dim() != 2 or logits.stride(1) != 1:
-        raise SvwError("logits must be a CUDA matrix with contiguous rows")
     gpu = logits.get_device()
+    if gpu < 0 or logits.dim() != 2 or logits.stride(1) != 1:
+        raise SvwError("logits must be a CUDA matrix with contiguous rows")
     rows, V = logits.shape
     N = cu_draft.numel() - 1
     R = int(cu_draft[-1].item()) if total_draft_rows is None else int(total_draft_rows)
     if rows != R + (N if has_bonus else 0):
         raise SvwError(f"logits have {rows} rows for {R} draft rows of {N} requests")
+    if (_off(cu_draft, i32, gpu) or _off(draft_tokens, i32, gpu) or _off(repetition, f32, gpu)
+            or _off(frequency, f32, gpu) or _off(presence, f32, gpu) or _off(status, i32, gpu)):
+        _need_like(gpu, i32, ("cu_draft", "draft_tokens", "status"), (cu_draft, draft_tokens, status))
+        _need_like(gpu, f32, ("repetition", "frequency", "presence"), (repetition, frequency, presence))
+    _need_numel(("repetition", "frequency", "presence"), (repetition, frequency, presence), N)
+    if draft_tokens is not None and draft_tokens.numel() != R:
+        raise SvwError(f"draft_tokens must have {R} elements")
     if (history is None) != (cu_history is None) or (prompt_len is not None and history is None):
         raise SvwError("history comes with cu_history, prompt_len with a history")
+    n_history = n_bias = mask_rows = 0
+    if history is not None:
+        if _off(history, i32, gpu) or _off(cu_history, i32, gpu) or _off(prompt_len, i32, gpu):
+            _need_like(gpu, i32, ("history", "cu_history", "prompt_len"), (history, cu_history, prompt_len))
+        _need_numel(("cu_history",), (cu_history,), N + 1)
+        _need_numel(("prompt_len",), (prompt_len,), N)
+        n_history = history.numel()
     if (bias_tokens is None) != (cu_bias is None) or (bias_values is None) != (cu_bias is None):
         raise SvwError("bias_tokens, bias_values and cu_bias come together")
-    if mask is None and mask_row is not None:
+    if cu_bias is not None:
+        _need_like(gpu, i32, ("bias_tokens", "cu_bias"), (bias_tokens, cu_bias))
+        _need_like(gpu, f32, ("bias_values",), (bias_values,))
+        _need_numel(("cu_bias",), (cu_bias,), N + 1)
+        n_bias = bias_tokens.numel()
+        if n_bias != bias_values.numel():
+            raise SvwError("bias_tokens and bias_values must have one length")
+    if mask is not None:
+        _need_like(gpu, i32, ("mask", "mask_row"), (mask, mask_row))
+        _need_numel(("mask_row",), (mask_row,), rows)
+        if mask.dim() != 2 or mask.shape[1] != (V + 31) // 32:
+            raise SvwError(f"mask must be [mask rows, {(V + 31) // 32}]")
+        mask_rows = mask.shape[0]
+    elif mask_row is not None:
         raise SvwError("mask_row comes with a mask")
-    _need_like(gpu, torch.int32, ("cu_draft", "draft_tokens", "history", "cu_history", "prompt_len", "bias_tokens",
-                                  "cu_bias", "mask", "mask_row", "status"),
-               (cu_draft, draft_tokens, history, cu_history, prompt_len, bias_tokens, cu_bias, mask, mask_row, status))
-    _need_like(gpu, torch.float32, ("repetition", "frequency", "presence", "bias_values"),
-               (repetition, frequency, presence, bias_values))
-    _need_numel(("prompt_len", "repetition", "frequency", "presence"), (prompt_len, repetition, frequency, presence), N)
-    _need_numel(("cu_history", "cu_bias"), (cu_history, cu_bias), N + 1)
-    _need_numel(("draft_tokens",), (draft_tokens,), R)
-    _need_numel(("mask_row",), (mask_row,), rows)
-    if bias_tokens is not None and bias_tokens.numel() != bias_values.numel():
-        raise SvwError("bias_tokens and bias_values must have one length")
-    if mask is not None and (mask.dim() != 2 or mask.shape[1] != (V + 31) // 32):
-        raise SvwError(f"mask must be [mask rows, {(V + 31) // 32}]")
     if out is None:
         out = torch.empty((rows, V), dtype=logits.dtype, device=logits.device)
         _lent(stream, out)
-    elif out.dtype != logits.dtype or out.get_device() != gpu or out.shape != logits.shape or out.stride(1) != 1:
+    elif out is not logits and (out.dtype is not logits.dtype or out.get_device() != gpu or out.shape != logits.shape
+                                or out.stride(1) != 1):
         raise SvwError("out must be like logits")
     # a single row has no pitch of its own
     pitch = logits.stride(0) if rows > 1 else V
     out_pitch = out.stride(0) if rows > 1 else V
     rc = lib().logits_adjust(logits.data_ptr(), pitch, code, V, N, cu_draft.data_ptr(), R, 1 if has_bonus else 0,
-                             _addr(draft_tokens), _addr(history), _addr(cu_history),
-                             0 if history is None else history.numel(), _addr(prompt_len), _addr(repetition),
-                             _addr(frequency), _addr(presence), _addr(bias_tokens), _addr(bias_values), _addr(cu_bias),
-                             0 if bias_tokens is None else bias_tokens.numel(), _addr(mask),
-                             0 if mask is None else mask.shape[0], _addr(mask_row), out.data_ptr(), out_pitch,
-                             _addr(status), _stream_of(stream, gpu))
-    _check(rc)
+                             _addr(draft_tokens), _addr(history), _addr(cu_history), n_history, _addr(prompt_len),
+                             _addr(repetition), _addr(frequency), _addr(presence), _addr(bias_tokens),
+                             _addr(bias_values), _addr(cu_bias), n_bias, _addr(mask), mask_rows, _addr(mask_row),
+                             out.data_ptr(), out_pitch, _addr(status), _stream_of(stream, gpu))
+    if rc:
+        _check(rc)
     return out
+
+
+# svw_paged_kv, field by field
+_pack_paged = struct.Struct("@2P6qPq5i").pack
 
 
 def _paged(k_cache, v_cache, block_table, N):
     """The svw_paged_kv of two [n_pages, heads, page_size, head_dim] tensors
-    (any strides but the last) and their block table."""
-    import torch
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+    (any strides but the last) and their block table, their GPU and shape."""
+    shape, gpu = k_cache.shape, k_cache.get_device()
+    if len(shape) != 4 or v_cache.shape != shape or k_cache.dtype is not v_cache.dtype:
         raise SvwError("k_cache and v_cache must be alike: [n_pages, heads, page_size, head_dim]")
-    ks, vs, gpu = k_cache.stride(), v_cache.stride(), k_cache.get_device()
-    if gpu < 0 or v_cache.get_device() != gpu or ks[3] != 1 or vs[3] != 1:
+    k0, k1, k2, k3 = k_cache.stride()
+    v0, v1, v2, v3 = v_cache.stride()
+    if gpu < 0 or v_cache.get_device() != gpu or k3 != 1 or v3 != 1:
         raise SvwError("the caches must be CUDA tensors with contiguous head vectors")
-    if (block_table.dtype != torch.int32 or block_table.get_device() != gpu or block_table.dim() != 2
-            or block_table.shape[0] != N or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
-        raise SvwError(f"block_table must be an int32 [{N}, max_pages] CUDA tensor with contiguous rows")
-    pages, heads, size, dim = k_cache.shape
-    mp = block_table.shape[1]
-    return _PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), ks[:3], vs[:3], block_table.data_ptr(),
-                    block_table.stride(0) if N > 1 else mp, mp, pages, size, heads, dim), gpu
+    if block_table.dtype is not _torch().int32 or block_table.get_device() != gpu or block_table.dim() != 2:
+        raise SvwError(f"block_table must be an int32 [{N}, max_pages] CUDA tensor")
+    rows, mp = block_table.shape
+    t0, t1 = block_table.stride()
+    if rows != N or (mp > 1 and t1 != 1):
+        raise SvwError(f"block_table must be [{N}, max_pages] with contiguous rows")
+    pages, heads, size, dim = shape
+    return _pack_paged(k_cache.data_ptr(), v_cache.data_ptr(), k0, k1, k2, v0, v1, v2, block_table.data_ptr(),
+                       t0 if N > 1 else mp, mp, pages, size, heads, dim), gpu, shape
 
 
-def _heads(name, t, dim, like):
-    if (t.dim() != 3 or t.shape[2] != dim or t.stride(2) != 1 or t.dtype != like.dtype
-            or t.get_device() != like.get_device()):
-        raise SvwError(f"{name} must be [new tokens, heads, {dim}], of the cache's type and device, with contiguous heads")
+def _heads(name, t, dim, dtype, gpu):
+    """The strides of tokens and heads of a [new tokens, heads, head_dim] tensor."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != dim or stride[2] != 1 or t.dtype is not dtype or t.get_device() != gpu:
+        raise SvwError(f"{name} must be [new tokens, heads, {dim}], of the cache's type and GPU, with contiguous heads")
+    return shape, stride
 
 
 def kv_append(k, v, k_cache, v_cache, block_table, cu_new, kv_len, *, cos_sin=None, interleaved: bool = False,
@@ -580,41 +615,45 @@ def kv_append(k, v, k_cache, v_cache, block_table, cu_new, kv_len, *, cos_sin=No
     token t is written at place kv_len[i] - n_i + t and rotated by that
     position, or by positions (int32 [total_new]).
     """
-    import torch
+    torch = _torch()
+    i32 = torch.int32
     N = cu_new.numel() - 1
-    cache, gpu = _paged(k_cache, v_cache, block_table, N)
-    T, dim = k.shape[0], k_cache.shape[3]
-    _heads("k", k, dim, k_cache)
-    _heads("v", v, dim, k_cache)
-    if k.shape[1] != k_cache.shape[1] or v.shape != k.shape:
+    cache, gpu, shape = _paged(k_cache, v_cache, block_table, N)
+    dim, dtype = shape[3], k_cache.dtype
+    kh, ks = _heads("k", k, dim, dtype, gpu)
+    vh, vs = _heads("v", v, dim, dtype, gpu)
+    T = kh[0]
+    if kh[1] != shape[1] or vh != kh:
         raise SvwError("k and v must have the cache's heads and one length")
-    _need_like(gpu, torch.int32, ("cu_new", "kv_len", "positions", "status"), (cu_new, kv_len, positions, status))
-    _need_numel(("kv_len",), (kv_len,), N)
+    if _off(cu_new, i32, gpu) or _off(kv_len, i32, gpu) or _off(positions, i32, gpu) or _off(status, i32, gpu):
+        _need_like(gpu, i32, ("cu_new", "kv_len", "positions", "status"), (cu_new, kv_len, positions, status))
+    if kv_len.numel() != N:
+        raise SvwError(f"kv_len must have {N} elements")
     _need_numel(("positions",), (positions,), T)
-    _need_like(gpu, torch.float32, ("cos_sin",), (cos_sin,))
-    if cos_sin is not None and cos_sin.dim() != 2:
-        raise SvwError("cos_sin must be [max_pos, rot_dim]")
-    qs = (0, 0, 0)
+    max_pos = rot = 0
+    if cos_sin is not None:
+        if _off(cos_sin, torch.float32, gpu) or cos_sin.dim() != 2:
+            raise SvwError(f"cos_sin must be a contiguous float32 [max_pos, rot_dim] tensor on cuda:{gpu}")
+        max_pos, rot = cos_sin.shape
+    hq, qs = 0, (0, 0)
     if q is not None:
-        _heads("q", q, dim, k_cache)
-        if q.shape[0] != T:
+        qh, qs = _heads("q", q, dim, dtype, gpu)
+        hq = qh[1]
+        if qh[0] != T:
             raise SvwError("q must have as many tokens as k")
-        qs = q.stride()
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = torch.empty(qh, dtype=dtype, device=q.device)
             _lent(stream, q_out)
-        elif (q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.get_device() != gpu
-              or not q_out.is_contiguous()):
+        elif _off(q_out, dtype, gpu) or q_out.shape != qh:
             raise SvwError("q_out must be like q, contiguous")
     elif q_out is not None:
         raise SvwError("q_out comes with q")
-    ks, vs = k.stride(), v.stride()
     rc = lib().kv_append(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _addr(q), qs[0], qs[1], _addr(q_out),
-                         _dtype_code(k_cache), 0 if q is None else q.shape[1], N, cu_new.data_ptr(), T,
-                         kv_len.data_ptr(), _addr(positions), _addr(cos_sin),
-                         0 if cos_sin is None else cos_sin.shape[0], 0 if cos_sin is None else cos_sin.shape[1],
-                         1 if interleaved else 0, ctypes.byref(cache), _addr(status), _stream_of(stream, gpu))
-    _check(rc)
+                         _dtype_code(k_cache), hq, N, cu_new.data_ptr(), T, kv_len.data_ptr(), _addr(positions),
+                         _addr(cos_sin), max_pos, rot, 1 if interleaved else 0, cache, _addr(status),
+                         _stream_of(stream, gpu))
+    if rc:
+        _check(rc)
     return q_out
 
 
@@ -636,34 +675,38 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, *, scale: 
     block; window > 0: only the last `window` keys up to its own.  scale
     defaults to head_dim ** -0.5.
     """
-    import torch
+    torch = _torch()
+    i32 = torch.int32
     N = cu_new.numel() - 1
-    cache, gpu = _paged(k_cache, v_cache, block_table, N)
-    dim = k_cache.shape[3]
-    _heads("q", q, dim, k_cache)
-    T, hq, _ = q.shape
-    _need_like(gpu, torch.int32, ("cu_new", "kv_len", "status"), (cu_new, kv_len, status))
-    _need_numel(("kv_len",), (kv_len,), N)
+    cache, gpu, shape = _paged(k_cache, v_cache, block_table, N)
+    dim, dtype = shape[3], k_cache.dtype
+    qh, qs = _heads("q", q, dim, dtype, gpu)
+    T, hq, _ = qh
+    if _off(cu_new, i32, gpu) or _off(kv_len, i32, gpu) or _off(status, i32, gpu):
+        _need_like(gpu, i32, ("cu_new", "kv_len", "status"), (cu_new, kv_len, status))
+    if kv_len.numel() != N:
+        raise SvwError(f"kv_len must have {N} elements")
     if out is None:
-        out = torch.empty((T, hq, dim), dtype=q.dtype, device=q.device)
+        out = torch.empty(qh, dtype=dtype, device=q.device)
         _lent(stream, out)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.get_device() != gpu or not out.is_contiguous():
+    elif _off(out, dtype, gpu) or out.shape != qh:
         raise SvwError("out must be like q, contiguous")
-    if lse is None and want_lse:
-        lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
-        _lent(stream, lse)
-    _need_like(gpu, torch.float32, ("lse",), (lse,))
-    _need_numel(("lse",), (lse,), T * hq)
+    if lse is None:
+        if want_lse:
+            lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
+            _lent(stream, lse)
+    elif _off(lse, torch.float32, gpu) or lse.numel() != T * hq:
+        raise SvwError(f"lse must be a contiguous float32 [{T}, {hq}] tensor on cuda:{gpu}")
     if workspace is None:
-        need = paged_attention_workspace_size(T, hq, k_cache.shape[1], dim)
+        need = paged_attention_workspace_size(T, hq, shape[1], dim)
         workspace = torch.empty(max(1, need), dtype=torch.uint8, device=q.device)
         _lent(stream, workspace)
-    _need_like(gpu, torch.uint8, ("workspace",), (workspace,))
-    qs = q.stride()
+    elif _off(workspace, torch.uint8, gpu):
+        raise SvwError(f"workspace must be a contiguous uint8 tensor on cuda:{gpu}")
     rc = lib().paged_attention(q.data_ptr(), qs[0], qs[1], _dtype_code(q), hq, N, cu_new.data_ptr(), T,
-                               kv_len.data_ptr(), ctypes.byref(cache),
-                               float(dim ** -0.5 if scale is None else scale), 1 if causal else 0, int(window),
-                               out.data_ptr(), _addr(lse), _addr(status), workspace.data_ptr(), workspace.numel(),
-                               _stream_of(stream, gpu))
-    _check(rc)
+                               kv_len.data_ptr(), cache, float(dim ** -0.5 if scale is None else scale),
+                               1 if causal else 0, int(window), out.data_ptr(), _addr(lse), _addr(status),
+                               workspace.data_ptr(), workspace.numel(), _stream_of(stream, gpu))
+    if rc:
+        _check(rc)
     return out, lse
