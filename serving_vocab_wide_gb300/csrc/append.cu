@@ -7,9 +7,11 @@
 // A copy with an address per token: bound by bytes for many tokens, by its
 // chain of dependent loads (offsets and lengths -> block table, cosines ->
 // stores) for a few.  Threads of a row of the block belong to one token; each
-// takes one or more pairs of 16-byte vectors (both halves of its rotated
-// pairs, so that queries may be rotated in place), whose loads are under way
-// before the token's request has been found.
+// takes slots of two 16-byte vectors (both halves of its rotated pairs, so that
+// queries may be rotated in place), whose loads are under way before the
+// token's request has been found.  Two tokens a row, to search once for both,
+// were slower (18 us against 16 where a slot a thread was), and a torch copy of
+// 27 MB takes 9.9 us where rotating and scattering them takes 13.0.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -22,8 +24,8 @@ namespace svw {
 
 namespace {
 
-constexpr int kAppThreads = 256;
-constexpr int kAppMaxRow = 512;  // threads of a token at most
+constexpr int kAppThreads = 256;  // of a block of many tokens' rows
+constexpr int kAppRow = 512;      // of a row when tokens are few
 
 __device__ __forceinline__ float ld_f(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float ld_f(const float *p) { return *p; }
@@ -102,28 +104,34 @@ __device__ __forceinline__ T *head_out(const AppendArgs &a, const Place &p, int6
   return reinterpret_cast<T *>(a.q_out) + (t * a.Hq + (h - 2 * a.Hkv)) * a.D;
 }
 
-// a 16-byte vector as floats and back
+// entries 4 q .. 4 q + 3 of a 16-byte vector as floats, and back
 template <typename T>
 struct Vec;
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
-  __device__ static void get(const uint4 &w, float *f) { Elem<1>::unpack(w, f); }
   __device__ static uint32_t two(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
   }
-  __device__ static uint4 put(const float *f) {
-    return make_uint4(two(f[0], f[1]), two(f[2], f[3]), two(f[4], f[5]), two(f[6], f[7]));
+  __device__ static float4 get(const uint4 &w, int q) {
+    const float2 a = bf16x2_f2(q ? w.z : w.x), b = bf16x2_f2(q ? w.w : w.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+  __device__ static void put(uint4 &w, int q, const float4 &f) {
+    (q ? w.z : w.x) = two(f.x, f.y);
+    (q ? w.w : w.y) = two(f.z, f.w);
   }
 };
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
-  __device__ static void get(const uint4 &w, float *f) { Elem<0>::unpack(w, f); }
-  __device__ static uint4 put(const float *f) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  __device__ static float4 get(const uint4 &w, int) {
+    return make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+  }
+  __device__ static void put(uint4 &w, int, const float4 &f) {
+    w = make_uint4(__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z), __float_as_uint(f.w));
   }
 };
 
@@ -133,10 +141,54 @@ __device__ __forceinline__ void turn(float &x, float &y, float c, float s) {
   y = __fadd_rn(__fmul_rn(r, c), __fmul_rn(p, s));
 }
 
-// Rows of the block: tokens.  Heads and rotated parts in multiples of two
-// vectors, everything 16-byte aligned.
+// the rotation of a slot's two vectors
 template <typename T>
-__global__ void kv_append_vec(AppendArgs a) {
+__device__ __forceinline__ void rotate_slot(const Place &p, bool halves, int x, int half, uint4 &u, uint4 &w) {
+  constexpr int N = Vec<T>::N;
+  // four pairs at a time: of the two halves, or of neighbours within each vector
+  const float4 nan = make_float4(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff), __int_as_float(0x7fffffff),
+                                 __int_as_float(0x7fffffff));
+  const float *cs = p.cs + (halves ? x : x / 2);
+#pragma unroll
+  for (int q = 0; q < N / 4; ++q) {
+    float4 c = nan, s = nan;
+    if (p.pos_ok) {
+      c = __ldg(reinterpret_cast<const float4 *>(cs + 4 * q));
+      s = __ldg(reinterpret_cast<const float4 *>(cs + half + 4 * q));
+    }
+    if (halves) {
+      float4 f = Vec<T>::get(u, q), g = Vec<T>::get(w, q);
+      turn(f.x, g.x, c.x, s.x);
+      turn(f.y, g.y, c.y, s.y);
+      turn(f.z, g.z, c.z, s.z);
+      turn(f.w, g.w, c.w, s.w);
+      Vec<T>::put(u, q, f);
+      Vec<T>::put(w, q, g);
+    } else if (N == 8) {  // four pairs are one vector
+      uint4 &m = q ? w : u;
+      float4 f = Vec<T>::get(m, 0), g = Vec<T>::get(m, 1);
+      turn(f.x, f.y, c.x, s.x);
+      turn(f.z, f.w, c.y, s.y);
+      turn(g.x, g.y, c.z, s.z);
+      turn(g.z, g.w, c.w, s.w);
+      Vec<T>::put(m, 0, f);
+      Vec<T>::put(m, 1, g);
+    } else {  // two pairs in each
+      float4 f = Vec<T>::get(u, 0), g = Vec<T>::get(w, 0);
+      turn(f.x, f.y, c.x, s.x);
+      turn(f.z, f.w, c.y, s.y);
+      turn(g.x, g.y, c.z, s.z);
+      turn(g.z, g.w, c.w, s.w);
+      Vec<T>::put(u, 0, f);
+      Vec<T>::put(w, 0, g);
+    }
+  }
+}
+
+// Rows of the block: tokens; kItems slots of a thread under way.  Heads and
+// rotated parts in multiples of two vectors, everything 16-byte aligned.
+template <typename T, int kItems>
+__global__ void __launch_bounds__(kItems == 1 ? kAppRow : kAppThreads, kItems == 1 ? 3 : 4) kv_append_vec(const __grid_constant__ AppendArgs a) {
   constexpr int N = Vec<T>::N;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   if (t >= a.T) return;
@@ -144,73 +196,55 @@ __global__ void kv_append_vec(AppendArgs a) {
   const int half = a.rot / 2;
   Place p;
   bool found = false;
-  for (int m = threadIdx.x; m - static_cast<int>(threadIdx.x & 31) < items; m += blockDim.x) {
-    const bool mine = m < items;
-    const int h = mine ? m / slots : 0, sl = mine ? m % slots : 0;
-    const bool rotates = h < a.Hkv || h >= 2 * a.Hkv;
-    // the slot's two vectors: both halves of rotated pairs, or neighbours
-    const bool halves = !a.interleaved && rotates && sl * N < half;
-    const int x = halves ? sl * N : 2 * sl * N;
-    const int y = halves ? half + sl * N : x + N;
-    const T *src;
-    head_rows<T>(a, t, h, src);
-    uint4 u, w;
-    if (mine) {
-      u = *reinterpret_cast<const uint4 *>(src + x);
-      w = *reinterpret_cast<const uint4 *>(src + y);
+  for (int m0 = threadIdx.x; m0 - static_cast<int>(threadIdx.x & 31) < items; m0 += kItems * blockDim.x) {
+    uint4 u[kItems], w[kItems];
+    int at[kItems];  // head, and the first vector's element; -1: no slot
+    // a slot's two vectors: both halves of rotated pairs, or neighbours
+    auto split = [&](int code, int &h, bool &rotates, bool &halves, int &x, int &y) {
+      const int sl = code & 0xffff;
+      h = code >> 16;
+      rotates = h < a.Hkv || h >= 2 * a.Hkv;
+      halves = !a.interleaved && rotates && sl * N < half;
+      x = halves ? sl * N : 2 * sl * N;
+      y = halves ? half + sl * N : x + N;
+    };
+#pragma unroll
+    for (int q = 0; q < kItems; ++q) {
+      const int m = m0 + q * blockDim.x;
+      at[q] = -1;
+      if (m < items) {
+        int h = m / slots, x, y;
+        bool rotates, halves;
+        at[q] = (h << 16) | (m - h * slots);
+        split(at[q], h, rotates, halves, x, y);
+        const T *src;
+        head_rows<T>(a, t, h, src);
+        u[q] = *reinterpret_cast<const uint4 *>(src + x);
+        w[q] = *reinterpret_cast<const uint4 *>(src + y);
+      }
     }
     if (!found) {
       p = find_place(a, t);
       found = true;
     }
-    if (!mine) continue;
-    if (h < 2 * a.Hkv && !p.write) continue;
-    if (rotates && x < a.rot) {
-      if (!p.pos_ok) {
-        float f[N];
 #pragma unroll
-        for (int e = 0; e < N; ++e) f[e] = __int_as_float(0x7fffffff);
-        u = w = Vec<T>::put(f);
-      } else {
-        float f[N], g[N];
-        Vec<T>::get(u, f);
-        Vec<T>::get(w, g);
-        if (halves) {
-          float c[N], s[N];
-#pragma unroll
-          for (int e = 0; e < N; e += 4) {
-            *reinterpret_cast<float4 *>(c + e) = __ldg(reinterpret_cast<const float4 *>(p.cs + x + e));
-            *reinterpret_cast<float4 *>(s + e) = __ldg(reinterpret_cast<const float4 *>(p.cs + half + x + e));
-          }
-#pragma unroll
-          for (int e = 0; e < N; ++e) turn(f[e], g[e], c[e], s[e]);
-        } else {
-          // neighbours are pairs: N / 2 of each vector, N in a row of the table
-          float c[N], s[N];
-#pragma unroll
-          for (int e = 0; e < N; e += 4) {
-            *reinterpret_cast<float4 *>(c + e) = __ldg(reinterpret_cast<const float4 *>(p.cs + x / 2 + e));
-            *reinterpret_cast<float4 *>(s + e) = __ldg(reinterpret_cast<const float4 *>(p.cs + half + x / 2 + e));
-          }
-#pragma unroll
-          for (int e = 0; e < N / 2; ++e) {
-            turn(f[2 * e], f[2 * e + 1], c[e], s[e]);
-            turn(g[2 * e], g[2 * e + 1], c[N / 2 + e], s[N / 2 + e]);
-          }
-        }
-        u = Vec<T>::put(f);
-        w = Vec<T>::put(g);
-      }
+    for (int q = 0; q < kItems; ++q) {
+      if (at[q] < 0) continue;
+      int h, x, y;
+      bool rotates, halves;
+      split(at[q], h, rotates, halves, x, y);
+      if (h < 2 * a.Hkv && !p.write) continue;
+      if (rotates && x < a.rot) rotate_slot<T>(p, halves, x, half, u[q], w[q]);
+      T *dst = head_out<T>(a, p, t, h);
+      *reinterpret_cast<uint4 *>(dst + x) = u[q];
+      *reinterpret_cast<uint4 *>(dst + y) = w[q];
     }
-    T *dst = head_out<T>(a, p, t, h);
-    *reinterpret_cast<uint4 *>(dst + x) = u;
-    *reinterpret_cast<uint4 *>(dst + y) = w;
   }
 }
 
 // any sizes, strides and alignments: one CTA per new token, entry by entry
 template <typename T>
-__global__ void __launch_bounds__(kAppThreads) kv_append_any(AppendArgs a) {
+__global__ void __launch_bounds__(kAppThreads) kv_append_any(const __grid_constant__ AppendArgs a) {
   const int64_t t = blockIdx.x;
   const Place p = find_place(a, t);
   const int D = a.D, half = a.rot / 2;
@@ -253,13 +287,23 @@ void launch(const AppendArgs &a, cudaStream_t st) {
     kv_append_any<T><<<static_cast<unsigned>(a.T), kAppThreads, 0, st>>>(a);
     return;
   }
-  // one slot per thread where a row of kAppMaxRow threads allows it; small
-  // tokens share a block
+  // Many tokens: about six slots a thread, in two rounds of three (the second
+  // round's loads run beside the first one's stores; measured on 2220 tokens of
+  // 48 heads of 128 and 14 k tokens of 48 heads of 64: 13.0 and 34.7 us; three
+  // slots in one round 14.1 and 37.3, a slot a thread 16.0 and 41.3).  Few: a
+  // slot a thread, the shortest way through.
   const int items = (a.Hq + 2 * a.Hkv) * (a.D / (2 * N));
-  const int x = items >= kAppMaxRow ? kAppMaxRow : (items + 31) / 32 * 32;
+  const bool few = a.T < 2 * 152;
+  const int share = few ? items : (items + 5) / 6;
+  const int most = few ? kAppRow : kAppThreads;
+  const int x = share >= most ? most : (share + 31) / 32 * 32;
   int y = kAppThreads / x < 1 ? 1 : kAppThreads / x;
   while (y > 1 && (a.T + y - 1) / y < 2 * 152) y /= 2;  // rather more blocks than fuller ones
-  kv_append_vec<T><<<static_cast<unsigned>((a.T + y - 1) / y), dim3(x, y), 0, st>>>(a);
+  const dim3 grid(static_cast<unsigned>((a.T + y - 1) / y)), block(x, y);
+  if (few)
+    kv_append_vec<T, 1><<<grid, block, 0, st>>>(a);
+  else
+    kv_append_vec<T, 3><<<grid, block, 0, st>>>(a);
 }
 
 }  // namespace
