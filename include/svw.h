@@ -409,8 +409,16 @@ svw_status length_head_label(const int32_t *accept_len, const int32_t *cu_draft,
  *                  spec_verify reports as a bad request), a mask row is
  *                  outside [-1, mask_rows) (that row becomes NaN), or its
  *                  CSR range is invalid (its rows are not written).
- * One kernel launch, no workspace.
+ *   workspace      device, 256-byte aligned, >= svw_logits_adjust_workspace_size
+ *                  bytes (0: none is needed); contents need not be
+ *                  initialised; not preserved; or NULL.  With it the lists of
+ *                  a large batch are counted once per request instead of once
+ *                  per 4096 entries of its vocabulary; the results are the
+ *                  same.
  */
+size_t svw_logits_adjust_workspace_size(int32_t n_requests, int32_t V, int64_t total_draft_rows, int64_t total_history,
+                                        int64_t total_bias);
+
 svw_status logits_adjust(const void *logits, int64_t logits_stride, svw_dtype dtype, int32_t V, int32_t N,
                          const int32_t *cu_draft, int64_t total_draft_rows, int32_t has_bonus_row,
                          const int32_t *draft_tokens, const int32_t *history, const int32_t *cu_history,
@@ -418,7 +426,7 @@ svw_status logits_adjust(const void *logits, int64_t logits_stride, svw_dtype dt
                          const float *frequency, const float *presence, const int32_t *bias_tokens,
                          const float *bias_values, const int32_t *cu_bias, int64_t total_bias,
                          const uint32_t *mask, int64_t mask_rows, const int32_t *mask_row, void *out,
-                         int64_t out_stride, int32_t *status, void *stream);
+                         int64_t out_stride, int32_t *status, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * A paged key / value cache: n_pages pages of page_size tokens for each of
@@ -562,8 +570,8 @@ svw_status spec_verify_noalloc(const void *target_logits, const void *draft_logi
  * kernel made from this thread ("early_plan", "verify_stats",
  * "verify_finalize", "verify_early_cluster", "filter_rows", "filtered_finalize",
  * "opd_fast_kernel", "opd_fix_parts", "opd_fix_grad", "opd_exact_kernel",
- * "fused_finalize", "length_head_mma", "length_head_final", "logits_adjust",
- * "kv_append", "paged_attention") records
+ * "fused_finalize", "length_head_mma", "length_head_final", "adjust_lists",
+ * "logits_adjust", "kv_append", "paged_attention", "attention_join") records
  * begin_event just before it and end_event just after it on the launch stream (cudaEvent_t handles passed as void*, owned
  * by the caller).  kernel = NULL disarms.  The library records nothing
  * unless armed.  Lets a benchmark time one kernel of a multi-kernel call with

@@ -94,8 +94,10 @@ def lib():
             L.length_head.restype = ctypes.c_int
             L.length_head_label.argtypes = [P, P, P, I32, P, P, P]
             L.length_head_label.restype = ctypes.c_int
+            L.svw_logits_adjust_workspace_size.argtypes = [I32, I32, I64, I64, I64]
+            L.svw_logits_adjust_workspace_size.restype = SZ
             L.logits_adjust.argtypes = [P, I64, ctypes.c_int, I32, I32, P, I64, I32, P, P, P, I64, P, P, P, P,
-                                        P, P, P, I64, P, I64, P, P, I64, P, P]
+                                        P, P, P, I64, P, I64, P, P, I64, P, P, SZ, P]
             L.logits_adjust.restype = ctypes.c_int
             L.kv_append.argtypes = [P, I64, I64, P, I64, I64, P, I64, I64, P, ctypes.c_int, I32, I32, P, I64, P,
                                     P, P, I64, I32, I32, P, P, P]
@@ -488,10 +490,16 @@ def _lent(stream, *ts):
             t.record_stream(stream)
 
 
+@functools.lru_cache(maxsize=64)
+def logits_adjust_workspace_size(n_requests: int, V: int, total_draft_rows: int, total_history: int,
+                                 total_bias: int) -> int:
+    return int(lib().svw_logits_adjust_workspace_size(n_requests, V, total_draft_rows, total_history, total_bias))
+
+
 def logits_adjust(logits, cu_draft, draft_tokens=None, *, history=None, cu_history=None, prompt_len=None,
                   repetition=None, frequency=None, presence=None, bias_tokens=None, bias_values=None, cu_bias=None,
                   mask=None, mask_row=None, has_bonus: bool = True, total_draft_rows: int | None = None, out=None,
-                  status=None, stream=None):
+                  status=None, workspace=None, stream=None):
     """Penalties for repeated tokens, biases and grammar masks on the logits of
     every drafted position (a position has seen the request's history and the
     drafted tokens before it).  Returns the adjusted logits.
@@ -503,7 +511,7 @@ def logits_adjust(logits, cu_draft, draft_tokens=None, *, history=None, cu_histo
     [mask rows, ceil(V / 32)] of 32 tokens' bits each, the row of each logit row
     in mask_row (-1: unmasked; without mask_row, its own).  out may be logits
     (in place).  `total_draft_rows` (= cu_draft[-1]) may be passed to avoid a
-    device read.
+    device read; workspace: uint8, >= logits_adjust_workspace_size(...) bytes.
     """
     torch = _torch()
     i32, f32 = torch.int32, torch.float32
@@ -555,6 +563,12 @@ def logits_adjust(logits, cu_draft, draft_tokens=None, *, history=None, cu_histo
     elif out is not logits and (out.dtype is not logits.dtype or out.get_device() != gpu or out.shape != logits.shape
                                 or out.stride(1) != 1):
         raise SvwError("out must be like logits")
+    if workspace is None:
+        if need := logits_adjust_workspace_size(N, V, R, n_history, n_bias):
+            workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
+            _lent(stream, workspace)
+    elif _off(workspace, torch.uint8, gpu):
+        raise SvwError(f"workspace must be a contiguous uint8 tensor on cuda:{gpu}")
     # a single row has no pitch of its own
     pitch = logits.stride(0) if rows > 1 else V
     out_pitch = out.stride(0) if rows > 1 else V
@@ -562,7 +576,8 @@ def logits_adjust(logits, cu_draft, draft_tokens=None, *, history=None, cu_histo
                              _addr(draft_tokens), _addr(history), _addr(cu_history), n_history, _addr(prompt_len),
                              _addr(repetition), _addr(frequency), _addr(presence), _addr(bias_tokens),
                              _addr(bias_values), _addr(cu_bias), n_bias, _addr(mask), mask_rows, _addr(mask_row),
-                             out.data_ptr(), out_pitch, _addr(status), _stream_of(stream, gpu))
+                             out.data_ptr(), out_pitch, _addr(status), _addr(workspace),
+                             0 if workspace is None else workspace.numel(), _stream_of(stream, gpu))
     if rc:
         _check(rc)
     return out

@@ -534,6 +534,14 @@ svw_status length_head_label(const int32_t *accept_len, const int32_t *cu_draft,
   return rc == 0 ? SVW_OK : SVW_ERR_CUDA;
 }
 
+size_t svw_logits_adjust_workspace_size(int32_t n_requests, int32_t V, int64_t total_draft_rows, int64_t total_history,
+                                        int64_t total_bias) {
+  if (n_requests <= 0 || V <= 0 || V > kMaxV || total_draft_rows < 0 || total_history < 0 || total_bias < 0 ||
+      total_draft_rows > INT32_MAX || total_history > INT32_MAX || total_bias > INT32_MAX)
+    return 0;
+  return svw::adjust_workspace(n_requests, V, total_draft_rows, total_history, total_bias);
+}
+
 svw_status logits_adjust(const void *logits, int64_t logits_stride, svw_dtype dtype, int32_t V, int32_t N,
                          const int32_t *cu_draft, int64_t total_draft_rows, int32_t has_bonus_row,
                          const int32_t *draft_tokens, const int32_t *history, const int32_t *cu_history,
@@ -541,7 +549,7 @@ svw_status logits_adjust(const void *logits, int64_t logits_stride, svw_dtype dt
                          const float *frequency, const float *presence, const int32_t *bias_tokens,
                          const float *bias_values, const int32_t *cu_bias, int64_t total_bias,
                          const uint32_t *mask, int64_t mask_rows, const int32_t *mask_row, void *out,
-                         int64_t out_stride, int32_t *status, void *stream) {
+                         int64_t out_stride, int32_t *status, void *workspace, size_t workspace_bytes, void *stream) {
   if (dtype != SVW_F32 && dtype != SVW_BF16) return SVW_ERR_UNSUPPORTED;
   if (V <= 0 || N <= 0 || total_draft_rows < 0 || total_history < 0 || total_bias < 0 || mask_rows < 0)
     return SVW_ERR_INVALID_ARG;
@@ -559,8 +567,12 @@ svw_status logits_adjust(const void *logits, int64_t logits_stride, svw_dtype dt
   if (!aligned(logits, es) || !aligned(out, es) || !aligned(cu_draft, 4) || !aligned(draft_tokens, 4) ||
       !aligned(history, 4) || !aligned(cu_history, 4) || !aligned(prompt_len, 4) || !aligned(repetition, 4) ||
       !aligned(frequency, 4) || !aligned(presence, 4) || !aligned(bias_tokens, 4) || !aligned(bias_values, 4) ||
-      !aligned(cu_bias, 4) || !aligned(mask, 4) || !aligned(mask_row, 4) || !aligned(status, 4))
+      !aligned(cu_bias, 4) || !aligned(mask, 4) || !aligned(mask_row, 4) || !aligned(status, 4) ||
+      !aligned(workspace, 256))
     return SVW_ERR_MISALIGNED;
+  if (workspace &&
+      workspace_bytes < svw_logits_adjust_workspace_size(N, V, total_draft_rows, total_history, total_bias))
+    return SVW_ERR_WORKSPACE;
   if (rows == 0) return SVW_OK;  // no drafts and no bonus rows
   if (rows > INT64_MAX / 8 / std::max(logits_stride, out_stride)) return SVW_ERR_INVALID_ARG;
   // in place, or apart
@@ -595,6 +607,7 @@ svw_status logits_adjust(const void *logits, int64_t logits_stride, svw_dtype dt
   a.mask_words = (static_cast<int64_t>(V) + 31) / 32;
   a.mask_row = mask_row;
   a.status = status;
+  a.ws = workspace;
   return svw::launch_adjust(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SVW_OK : SVW_ERR_CUDA;
 }
 

@@ -231,8 +231,14 @@ struct AdjustArgs {
   int64_t mask_rows, mask_words;
   const int32_t *mask_row;
   int32_t *status;
-  int32_t chunk_len, chunks, groups;  // set by the launcher
+  void *ws;  // NULL: the chunks' CTAs count for themselves
+  // set by the launcher
+  int32_t chunk_len, chunks, groups;  // entries of a CTA's chunk; CTAs of a request's vocabulary, of its rows
+  int32_t list_chunks, even;          // chunks of the lists; 1: CTAs of a request's vocabulary share its list evenly
+  int32_t *list_offs;  // [N][list_chunks + 2] a request's chunks in its list, its end, whether it is bad
+  int4 *list;          // token, count word, bias place
 };
+size_t adjust_workspace(int64_t N, int64_t V, int64_t R, int64_t total_history, int64_t total_bias);
 cudaError_t launch_adjust(const AdjustArgs &a, int dtype, cudaStream_t stream);
 
 // kv_append (append.cu)

@@ -82,11 +82,12 @@ def _reference(c):
                       c["bonus"])
 
 
-def _compare(got, c):
+def _compare(got, c, reference=None, rows=slice(None)):
     import torch
-    y, size = _reference(c)
+    y, size = _reference(c) if reference is None else reference
+    y, size = y[rows], size[rows]
     bf16 = c["t"].dtype == torch.bfloat16
-    g = got.double().cpu().numpy()
+    g = got.double().cpu().numpy()[rows]
     top = 3.3961775e38 if bf16 else 3.4028235e38  # beyond: rounds to infinity
     with np.errstate(invalid="ignore"):
         y = np.where(np.abs(y) > top, np.sign(y) * np.inf, y)
@@ -100,7 +101,9 @@ def _compare(got, c):
 
 SHAPES = [([0], 40, "bf16"), ([1], 1, "fp32"), ([3, 0, 16, 1], 1000, "bf16"), ([3, 0, 16, 1], 1001, "bf16"),
           ([2, 5], 5003, "fp32"), ([32, 32], 8192, "fp32"), ([4] * 9, 32001, "bf16"), ([16, 2, 8], 151936, "bf16"),
-          ([1] * 40, 4104, "bf16"), ([7], 70000, "fp32")]
+          ([1] * 40, 4104, "bf16"), ([7], 70000, "fp32"),
+          # enough requests that their lists are counted first
+          ([3, 0] * 23, 32001, "bf16"), ([2] * 64, 20488, "fp32"), ([1] * 310, 300, "bf16")]
 
 
 @pytest.mark.parametrize("lens,V,dtype", SHAPES)
@@ -337,3 +340,53 @@ def test_adjust_refusals():
     big = torch.zeros(x.numel() + 64, dtype=x.dtype, device="cuda")
     with pytest.raises(E):
         svw.logits_adjust(big[:x.numel()].view(x.shape), *a, out=big[64:].view(x.shape), **kw)
+
+
+@pytest.mark.parametrize("V,hist,lens", [(151936, 20000, [4]), (9000, 30000, [2, 3]), (4097, 5000, [1]),
+                                         (151936, 7000, [1, 0, 2])])
+def test_adjust_long_histories(V, hist, lens):
+    """Histories of more distinct tokens than are counted at once."""
+    import serving_vocab_wide_gb300 as svw
+    assert svw.logits_adjust_workspace_size(len(lens), V, sum(lens), hist * len(lens), 0) > 0
+    c = _case(71, lens, V, "bf16", hist=(hist, hist), nbias=300)
+    rng = np.random.default_rng(72)
+    c["history"] = rng.integers(0, V, len(c["history"])).astype(np.int32)
+    a, kw = _args(c)
+    import torch
+    x = c["t"].cuda()
+    out = svw.logits_adjust(x, *a, **kw)
+    _compare(out, c)
+    svw.logits_adjust(x, *a, out=x, **kw)
+    assert torch.equal(out.view(torch.int16), x.view(torch.int16))
+
+
+def test_adjust_bad_requests_of_a_large_batch():
+    """The same refusals where the lists are counted first: a bad request's rows
+    are NaN, a list that begins before an earlier one's end is bad, the others
+    are right; a workspace of the caller's, whatever it holds."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    V, N = 5000, 200
+    for which in ("history token", "draft token", "repetition", "bias value", "overlap"):
+        c = _case(81, [1, 2] * (N // 2), V, "bf16", hist=(5, 30))
+        good = _reference(c)
+        bad = 1
+        if which == "overlap":
+            c["cu_h"][100] = c["cu_h"][98]  # request 99 runs backwards, request 100 begins inside an earlier one
+            bad = None
+        else:
+            _bad(c, which, V)
+        a, kw = _args(c)
+        need = svw.logits_adjust_workspace_size(N, V, int(c["cu"][-1]), len(c["history"]), 5 * N)
+        assert need > 0
+        ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = svw.logits_adjust(c["t"].cuda(), *a, status=status, workspace=ws, **kw)
+        assert int(status) == svw.SVW_DEV_BAD_INPUT
+        mine = np.zeros(c["rows"], bool)  # the bad requests' rows
+        for i in (99, 100) if bad is None else (bad,):
+            mine[c["cu"][i] + i:c["cu"][i + 1] + i + 1] = True
+        assert bool(out[torch.from_numpy(mine).cuda()].isnan().all()), which
+        _compare(out, c, good, ~mine)
+    with pytest.raises(svw.SvwError):
+        svw.logits_adjust(c["t"].cuda(), *a, workspace=ws[:need - 1], **kw)

@@ -18,7 +18,7 @@ def svw():
 
 def _adjust(svw, **o):
     a = dict(logits=P, ls=100, dt=1, V=100, N=2, cu=P, R=3, bonus=1, tok=P, hist=P, cuh=P, nh=5, pl=P, rep=P, freq=P,
-             pres=P, bt=P, bv=P, cub=P, nb=2, mask=P, mr=4, mrow=P, out=P + 0x10000, os=100, st=P, stream=None)
+             pres=P, bt=P, bv=P, cub=P, nb=2, mask=P, mr=4, mrow=P, out=P + 0x10000, os=100, st=P, ws=None, wb=0, stream=None)
     a.update(o)
     return svw.lib().logits_adjust(*a.values())
 
@@ -29,6 +29,7 @@ def _adjust(svw, **o):
     ({"tok": None}, INVALID), ({"hist": None}, INVALID), ({"bv": None}, INVALID), ({"ls": 99}, INVALID),
     ({"os": 99}, INVALID), ({"mrow": None}, INVALID), ({"logits": P + 1}, MISALIGNED), ({"cu": P + 2}, MISALIGNED),
     ({"mask": P + 2}, MISALIGNED), ({"out": P + 64}, INVALID), ({"out": P, "os": 104}, INVALID),
+    ({"ws": P + 16}, MISALIGNED), ({"N": 500, "V": 8192, "ls": 8192, "os": 8192, "mr": 503, "ws": P, "wb": 256}, WORKSPACE),
     ({"R": 0, "tok": None, "bonus": 0, "mask": None}, OK)])
 def test_adjust_validates(svw, o, want):
     assert _adjust(svw, **o) == want
@@ -102,3 +103,12 @@ def test_attention_workspace_size(svw):
     f = svw.paged_attention_workspace_size
     assert f(10, 8, 2, 128) > 0 and f(10, 8, 2, 128) % 256 == 0
     assert f(10, 7, 2, 128) == 0 and f(10, 8, 2, 96) == 0 and f(-1, 8, 2, 128) == 0 and f(10, 130, 2, 128) == 0
+
+
+def test_adjust_workspace_size(svw):
+    f = svw.logits_adjust_workspace_size
+    assert f(1, 32000, 0, 64, 0) == 0          # a small batch counts for itself
+    assert f(1, 32000, 0, 1 << 17, 0) > (16 << 17)  # a long history does not
+    n = f(256, 151936, 2000, 500000, 8192)
+    assert n >= 16 * (2000 + 500000 + 8192) and n % 256 == 0
+    assert f(0, 100, 0, 0, 0) == 0 and f(1, 1 << 21, 0, 0, 0) == 0 and f(1, 100, -1, 0, 0) == 0
