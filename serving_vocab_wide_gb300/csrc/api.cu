@@ -696,7 +696,7 @@ size_t svw_paged_attention_workspace_size(int64_t total_new, int32_t n_q_heads, 
   if (total_new < 0 || n_kv_heads <= 0 || n_q_heads <= 0 || n_q_heads % n_kv_heads != 0 ||
       n_q_heads / n_kv_heads > 64 || (head_dim != 64 && head_dim != 128))
     return 0;
-  return svw::attention_workspace(head_dim);
+  return svw::attention_workspace(total_new, n_q_heads / n_kv_heads, head_dim);
 }
 
 svw_status paged_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, svw_dtype dtype,

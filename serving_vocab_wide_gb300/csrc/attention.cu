@@ -54,6 +54,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <mutex>
 
@@ -861,12 +862,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // A unit that workers c .. last shared: each row's parts brought to one
 // reference and added, in the order of the line.  A warp per row at a time; the
-// first eight parts' outputs are under way beside the references and sums (one
+// first kAhead parts' outputs are under way beside the references and sums (one
 // after the other, eight rows a warp, the joins of two prompts took 50 us).
-constexpr int kJoinRows = 2;  // rows of a warp, at most
-template <int D>
-__global__ void __launch_bounds__(256, 4) attention_join(const __grid_constant__ AttendArgs a, int workers) {
-  constexpr int E = D / 32, kAhead = 8;
+// Wide units have many rows and two or three parts, narrow ones few rows and,
+// where one request fills the GPU, dozens.
+template <int D, bool kWide>
+__global__ void __launch_bounds__(256, kWide ? 4 : 3) attention_join(const __grid_constant__ AttendArgs a, int workers) {
+  constexpr int E = D / 32, kAhead = kWide ? 4 : 8;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x;
   const Joint jt = a.joints[c];
@@ -878,7 +880,9 @@ __global__ void __launch_bounds__(256, 4) attention_join(const __grid_constant__
   const int n = jt.last - c + 1;
   // a worker whose stretch is empty (fewer tiles than workers) has no part
   auto some = [&](int q) {
-    return q == 0 || jt.total >= workers || jt.total * (c + q) / workers < jt.total * (c + q + 1) / workers;
+    if (q == 0 || jt.total >= workers) return true;
+    const int t = static_cast<int>(jt.total);  // below 2^9, as the workers are
+    return t * (c + q) / workers < t * (c + q + 1) / workers;
   };
   for (; r < rows; r += warps) {
     const int tile = r >= rows0 ? 1 : 0, in_tile = r - tile * rows0;
@@ -978,6 +982,12 @@ bool encode(CUtensorMap *map, const void *ptr, int rank, const int64_t *dims, co
 int tile_tokens(int32_t Hq, int32_t Hkv) { return kRows / (Hq / Hkv); }
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
+// rows of the workspace's parts, two per worker: a row tile (no more rows than
+// there are tokens) of the narrow form's 2 * kMaxGrid workers, or the two of the
+// wide form's kMaxGrid
+int narrow_rows(int64_t T, int G) { return static_cast<int>(T * G < kRows ? (T * G + 7) / 8 * 8 : kRows); }
+size_t all_part_rows(int64_t T, int G) { return static_cast<size_t>(2 * 2 * kMaxGrid) * narrow_rows(T, G); }
+
 template <int D, bool kWide>
 cudaError_t launch(AttendArgs a, cudaStream_t st) {
   using Sh = Shape<D, kWide>;
@@ -1006,7 +1016,7 @@ cudaError_t launch(AttendArgs a, cudaStream_t st) {
     }
   }
   const int P = sms[dev] < kMaxGrid ? sms[dev] : kMaxGrid;
-  a.part_rows = Sh::kTiles * kRows;
+  a.part_rows = kWide ? 2 * kRows : narrow_rows(a.T, G);
   void *tm = timer_before("paged_attention", st);
   paged_attention_kernel<D, kWide><<<P, kThreads, Sh::kSmem, st>>>(mq, mk, mv, a);
   timer_after(tm, st);
@@ -1016,25 +1026,25 @@ cudaError_t launch(AttendArgs a, cudaStream_t st) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(P * Sh::kWorkers), Sh::kTiles * kRows / 8 / kJoinRows, 1);
+  // blocks for a unit's rows, on average (in a larger one a warp has several); two rows a warp when wide
+  const int64_t rows = std::min<int64_t>(a.part_rows, a.T * G / a.N + 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(P * Sh::kWorkers), static_cast<unsigned>(kWide ? (rows + 15) / 16 : (rows + 7) / 8), 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   tm = timer_before("attention_join", st);
-  e = cudaLaunchKernelEx(&cfg, attention_join<D>, a, P * Sh::kWorkers);
+  e = cudaLaunchKernelEx(&cfg, attention_join<D, kWide>, a, P * Sh::kWorkers);
   timer_after(tm, st);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-// parts of the workspace: two per worker of 128 rows each row tile of a unit, narrow or wide alike
-constexpr size_t kPartRows = 2 * 2 * kMaxGrid * kRows;
-
 }  // namespace
 
 // joints | (reference, sum) of each part's rows | their outputs
-size_t attention_workspace(int32_t D) {
-  return round256(sizeof(Joint) * 2 * kMaxGrid) + round256(kPartRows * sizeof(float2)) + kPartRows * D * sizeof(float);
+size_t attention_workspace(int64_t T, int32_t G, int32_t D) {
+  const size_t rows = all_part_rows(T, G);
+  return round256(sizeof(Joint) * 2 * kMaxGrid) + round256(rows * sizeof(float2)) + rows * D * sizeof(float);
 }
 
 cudaError_t launch_attention(const AttendArgs &args, cudaStream_t st) {
@@ -1044,7 +1054,7 @@ cudaError_t launch_attention(const AttendArgs &args, cudaStream_t st) {
   char *ws = static_cast<char *>(a.ws);
   a.joints = reinterpret_cast<Joint *>(ws);
   a.part_ml = reinterpret_cast<float2 *>(ws + round256(sizeof(Joint) * 2 * kMaxGrid));
-  a.part_o = reinterpret_cast<float *>(ws + round256(sizeof(Joint) * 2 * kMaxGrid) + round256(kPartRows * sizeof(float2)));
+  a.part_o = reinterpret_cast<float *>(ws + round256(sizeof(Joint) * 2 * kMaxGrid) + round256(all_part_rows(a.T, G) * sizeof(float2)));
   // The rows of a request, on average: up to one tile's the bytes of its keys
   // bound the work (128 rows are 128 flop per byte, the ridge lies at 280), and
   // more would read the keys once per tile in the narrow form.

@@ -296,7 +296,7 @@ struct AttendArgs {
   float2 *part_ml;      // [2 workers][part_rows] reference and sum
   float *part_o;        // [2 workers][part_rows][D] unnormalised output
 };
-size_t attention_workspace(int32_t D);
+size_t attention_workspace(int64_t T, int32_t G, int32_t D);  // G: query heads of a key head
 cudaError_t launch_attention(const AttendArgs &a, cudaStream_t stream);
 
 }  // namespace svw
