@@ -64,8 +64,8 @@ cudaError_t register_wait_limit(cudaError_t (*set)(long long)) {
 int32_t test_fault() { return g_fault.load(std::memory_order_relaxed); }
 }  // namespace svw
 
-// a new tag for every OPD call (never 0): flags set by an earlier call never
-// match it
+// a new tag for every OPD and attention call (never 0): flags set by an earlier
+// call never match it
 static int32_t next_epoch() {
   static std::atomic<uint32_t> g_epoch{0x3c5a0000u};
   uint32_t ep = ++g_epoch;
@@ -765,6 +765,7 @@ svw_status paged_attention(const void *q, int64_t q_token_stride, int64_t q_head
   a.lse = lse;
   a.status = status;
   a.ws = workspace;
+  a.tag = next_epoch();
   return svw::launch_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SVW_OK : SVW_ERR_CUDA;
 }
 

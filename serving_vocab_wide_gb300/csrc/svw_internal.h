@@ -266,9 +266,8 @@ cudaError_t launch_append(const AppendArgs &a, int dtype, cudaStream_t stream);
 // paged_attention (attention.cu)
 // the unit that a worker's last segment begins and does not finish
 struct alignas(16) AttendJoint {
-  int64_t total;  // length of the line of work (for the other workers' stretches)
-  int32_t last;   // the worker that finishes the unit; -1: there is no such unit
-  int32_t tok0, ntok0, ntok1, hk, pad;
+  int32_t last;  // the worker that finishes the unit; -1: there is no such unit
+  int32_t tok0, ntok0, ntok1, hk, pad[3];
 };
 struct AttendArgs {
   const void *q;
@@ -289,10 +288,12 @@ struct AttendArgs {
   float *lse;
   int32_t *status;
   void *ws;
+  int32_t tag;  // this call's, never 0
   // set by the launcher
   int32_t tile_tokens;  // tokens of a row tile
   int32_t part_rows;    // rows of a workspace part
   AttendJoint *joints;  // [workers]
+  int32_t *marks;       // [2 workers] parts that are written, by the call's tag
   float2 *part_ml;      // [2 workers][part_rows] reference and sum
   float *part_o;        // [2 workers][part_rows][D] unnormalised output
 };

@@ -378,9 +378,38 @@ def test_attend_streams_and_graph():
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         svw.paged_attention(*args, out=out, lse=lse, workspace=ws)
-    g.replay()
+    for _ in range(3):  # one captured call, replayed: the same workspace as it was left
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("new,kv,hq,hkv", [([1], [9000], 8, 2), ([1] * 5, [700, 1, 9000, 64, 3000], 8, 8), ([2], [30000], 4, 1)])
+def test_attend_replays_with_other_keys(new, kv, hq, hkv):
+    """A captured call of few rows, replayed after its cache has changed, gives
+    what a fresh call gives: nothing of an earlier replay is joined in."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    rng = np.random.default_rng(24)
+    kc, vc, table = _cache(rng, new, kv, hkv, 128, 64, torch.bfloat16)
+    T = sum(new)
+    q = torch.from_numpy(rng.normal(size=(T, hq, 128))).to(torch.bfloat16).cuda()
+    args = (q, kc, vc, _i32(table), _i32(_cu(new)), _i32(kv))
+    out, lse = torch.zeros_like(q), torch.zeros(T, hq, device="cuda")
+    ws = torch.empty(svw.paged_attention_workspace_size(T, hq, hkv, 128), dtype=torch.uint8, device="cuda")
+    svw.paged_attention(*args, out=out, lse=lse, workspace=ws)
     torch.cuda.synchronize()
-    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        svw.paged_attention(*args, out=out, lse=lse, workspace=ws)
+    for n in range(20):
+        vc.mul_(-1)
+        q.mul_(0.9)
+        g.replay()
+        want = svw.paged_attention(*args)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), n
 
 
 def test_append_then_attend_follow_on_one_stream():
