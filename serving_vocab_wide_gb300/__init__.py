@@ -456,12 +456,6 @@ def _need_like(index, dtype, names, ts):
             raise SvwError(f"{name} must be a contiguous {dtype} tensor on cuda:{index}")
 
 
-def _need_numel(names, ts, n):
-    for name, t in zip(names, ts):
-        if t is not None and t.numel() != n:
-            raise SvwError(f"{name} must have {n} elements")
-
-
 def _off(t, dtype, index):
     """Whether a tensor is not contiguous, of this type and on this GPU (None is fine)."""
     return t is not None and (t.dtype is not dtype or t.get_device() != index or not t.is_contiguous())
@@ -528,30 +522,32 @@ def logits_adjust(logits, cu_draft, draft_tokens=None, *, history=None, cu_histo
             or _off(frequency, f32, gpu) or _off(presence, f32, gpu) or _off(status, i32, gpu)):
         _need_like(gpu, i32, ("cu_draft", "draft_tokens", "status"), (cu_draft, draft_tokens, status))
         _need_like(gpu, f32, ("repetition", "frequency", "presence"), (repetition, frequency, presence))
-    _need_numel(("repetition", "frequency", "presence"), (repetition, frequency, presence), N)
+    if ((repetition is not None and repetition.numel() != N) or (frequency is not None and frequency.numel() != N)
+            or (presence is not None and presence.numel() != N)):
+        raise SvwError(f"repetition, frequency and presence must have {N} elements")
     if draft_tokens is not None and draft_tokens.numel() != R:
         raise SvwError(f"draft_tokens must have {R} elements")
-    if (history is None) != (cu_history is None) or (prompt_len is not None and history is None):
+    if (history is None) is not (cu_history is None) or (prompt_len is not None and history is None):
         raise SvwError("history comes with cu_history, prompt_len with a history")
     n_history = n_bias = mask_rows = 0
     if history is not None:
         if _off(history, i32, gpu) or _off(cu_history, i32, gpu) or _off(prompt_len, i32, gpu):
             _need_like(gpu, i32, ("history", "cu_history", "prompt_len"), (history, cu_history, prompt_len))
-        _need_numel(("cu_history",), (cu_history,), N + 1)
-        _need_numel(("prompt_len",), (prompt_len,), N)
+        if cu_history.numel() != N + 1 or (prompt_len is not None and prompt_len.numel() != N):
+            raise SvwError(f"cu_history must have {N + 1} elements, prompt_len {N}")
         n_history = history.numel()
     if (bias_tokens is None) != (cu_bias is None) or (bias_values is None) != (cu_bias is None):
         raise SvwError("bias_tokens, bias_values and cu_bias come together")
     if cu_bias is not None:
         _need_like(gpu, i32, ("bias_tokens", "cu_bias"), (bias_tokens, cu_bias))
         _need_like(gpu, f32, ("bias_values",), (bias_values,))
-        _need_numel(("cu_bias",), (cu_bias,), N + 1)
         n_bias = bias_tokens.numel()
-        if n_bias != bias_values.numel():
-            raise SvwError("bias_tokens and bias_values must have one length")
+        if cu_bias.numel() != N + 1 or n_bias != bias_values.numel():
+            raise SvwError(f"cu_bias must have {N + 1} elements, bias_tokens and bias_values one length")
     if mask is not None:
         _need_like(gpu, i32, ("mask", "mask_row"), (mask, mask_row))
-        _need_numel(("mask_row",), (mask_row,), rows)
+        if mask_row is not None and mask_row.numel() != rows:
+            raise SvwError(f"mask_row must have {rows} elements")
         if mask.dim() != 2 or mask.shape[1] != (V + 31) // 32:
             raise SvwError(f"mask must be [mask rows, {(V + 31) // 32}]")
         mask_rows = mask.shape[0]
@@ -644,7 +640,8 @@ def kv_append(k, v, k_cache, v_cache, block_table, cu_new, kv_len, *, cos_sin=No
         _need_like(gpu, i32, ("cu_new", "kv_len", "positions", "status"), (cu_new, kv_len, positions, status))
     if kv_len.numel() != N:
         raise SvwError(f"kv_len must have {N} elements")
-    _need_numel(("positions",), (positions,), T)
+    if positions is not None and positions.numel() != T:
+        raise SvwError(f"positions must have {T} elements")
     max_pos = rot = 0
     if cos_sin is not None:
         if _off(cos_sin, torch.float32, gpu) or cos_sin.dim() != 2:

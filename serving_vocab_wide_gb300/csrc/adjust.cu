@@ -462,7 +462,7 @@ __host__ __device__ constexpr int list_bytes(int V, bool bias) {
 // counts and the bits below its own) is its place in the list and, less the
 // window's start, in the array of counts.  (A hash table of the same tokens
 // took 52 us for 8182 of them, 4.5 thousand distinct, in its probes.)
-__global__ void __launch_bounds__(kListThreads) adjust_lists(const __grid_constant__ AdjustArgs a) {
+__global__ void __launch_bounds__(kListThreads, 2) adjust_lists(const __grid_constant__ AdjustArgs a) {
   extern __shared__ int32_t dyn[];
   const int words = list_words(a.V);
   uint32_t *bits = reinterpret_cast<uint32_t *>(dyn);
@@ -476,20 +476,24 @@ __global__ void __launch_bounds__(kListThreads) adjust_lists(const __grid_consta
   if (tid == 0 && (!rows_fine(a, s) || (i == 0 && s.d0 != 0) || (i == a.N - 1 && s.d1 != a.R))) report(a);
   int32_t *offs = a.list_offs + static_cast<int64_t>(i) * (a.list_chunks + 2);
   if (!rows_fine(a, s)) return;  // its rows are not written
-  bool bad = !factors_of(a, i).fine() || !lists_fine(a, s);
-  // lists that begin before an earlier request's would share their room in the workspace
-  for (int32_t j = tid; j < i; j += kListThreads)
-    bad |= __ldg(a.cu + j) > s.d0 || (a.cu_history && __ldg(a.cu_history + j) > s.h0) ||
-           (a.cu_bias && __ldg(a.cu_bias + j) > s.b0);
-  bad = __syncthreads_or(bad);
+  const Factors f = factors_of(a, i);
+  bool bad = !lists_fine(a, s);
   if (bad) s.h1 = s.h0, s.b1 = s.b0, s.d1 = s.d0;
+  bad |= !f.fine();
   int4 *list = a.list + (static_cast<int64_t>(s.h0) + s.b0 + s.d0);  // room for one entry per token listed
   const int32_t *hist = a.history + s.h0;
   const int32_t hn = s.h1 - s.h0, L = s.d1 - s.d0;
   const uint32_t V = static_cast<uint32_t>(a.V);
-  // every token of the history with its place, kAhead of a thread under way
+  // every token of the history with its place, kAhead of a thread under way; the
+  // first kAhead stay in registers
+  int32_t held[kAhead];
+#pragma unroll
+  for (int q = 0; q < kAhead; ++q) held[q] = (tid + q * kListThreads < hn) ? __ldg(hist + tid + q * kListThreads) : -1;
   auto each = [&](auto &&f) {
-    for (int32_t p0 = tid; p0 < hn; p0 += kAhead * kListThreads) {
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
+      if (tid + q * kListThreads < hn) f(held[q], tid + q * kListThreads);
+    for (int32_t p0 = tid + kAhead * kListThreads; p0 < hn; p0 += kAhead * kListThreads) {
       int32_t v[kAhead];
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) v[q] = (p0 + q * kListThreads < hn) ? __ldg(hist + p0 + q * kListThreads) : -1;
@@ -498,6 +502,11 @@ __global__ void __launch_bounds__(kListThreads) adjust_lists(const __grid_consta
         if (p0 + q * kListThreads < hn) f(v[q], p0 + q * kListThreads);
     }
   };
+  // lists that begin before an earlier request's would share their room in the workspace
+  for (int32_t j = tid; j < i; j += kListThreads)
+    bad |= __ldg(a.cu + j) > s.d0 || (a.cu_history && __ldg(a.cu_history + j) > s.h0) ||
+           (a.cu_bias && __ldg(a.cu_bias + j) > s.b0);
+  const bool apart = __syncthreads_or(bad) == 0;  // the list may be written
   int32_t base = 0;  // entries of the ranges before
   for (int32_t lo = 0; lo < a.V; lo += words * 32) {
     const int32_t n_tok = min(a.V - lo, words * 32);
@@ -574,7 +583,7 @@ __global__ void __launch_bounds__(kListThreads) adjust_lists(const __grid_consta
       for (int w = tid; w < words; w += kListThreads) {
         int32_t r = below[w] - r0;
         for (uint32_t m = bits[w]; m != 0; m &= m - 1, ++r)
-          if (r >= 0 && r < n) list[base + r0 + r] = make_int4(lo + w * 32 + __ffs(m) - 1, cnt[r], a.cu_bias ? bid[r] : 0, 0);
+          if (apart && r >= 0 && r < n) list[base + r0 + r] = make_int4(lo + w * 32 + __ffs(m) - 1, cnt[r], a.cu_bias ? bid[r] : 0, 0);
       }
       __syncthreads();
     }
