@@ -603,8 +603,9 @@ struct Listed {
   int n;
   bool bad;
 };
+__device__ __forceinline__ void wait_for_lists() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ Listed listed_of(const AdjustArgs &a, const Slices &s, int32_t i, int32_t c) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_lists();
   const int32_t *offs = a.list_offs + static_cast<int64_t>(i) * (a.list_chunks + 2);
   int32_t first, last;
   if (a.even) {
@@ -661,7 +662,7 @@ __global__ void __launch_bounds__(kAdjThreads, 7) adjust_staged(const __grid_con
   const int32_t c = static_cast<int32_t>(item % static_cast<unsigned>(a.chunks));
   const Slices s = slices_of(a, i);
   const Factors f = factors_of(a, i);
-  if (!rows_fine(a, s)) return;
+  if (!rows_fine(a, s)) return wait_for_lists();  // no CTA is done before the lists are
   const Rows<DT> r = rows_of<DT>(a, s, i, c, group, mask_of);
   if (tid < s.d1 - s.d0) drafts[tid] = __ldg(a.tokens + s.d0 + tid);
   // entry u of row q lies in the stage as far from a 16-byte boundary as in memory
@@ -782,7 +783,7 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_rows(const __grid_const
   const int32_t c = static_cast<int32_t>(item % static_cast<unsigned>(a.chunks));
   const Slices s = slices_of(a, i);
   const Factors f = factors_of(a, i);
-  if (!rows_fine(a, s)) return;
+  if (!rows_fine(a, s)) return wait_for_lists();  // no CTA is done before the lists are
   const Rows<DT> r = rows_of<DT>(a, s, i, a.even ? 0 : c, group, mask_of);
   if (tid < s.d1 - s.d0) drafts[tid] = __ldg(a.tokens + s.d0 + tid);
   __syncthreads();

@@ -635,7 +635,12 @@ __device__ __forceinline__ void join_rows(const AttendArgs &a, const Joint &jt, 
 // fence between the two lets the last of them see all marks, and it joins (two
 // may both see them all: they write the same results).  No worker waits for
 // another.  The joiner takes the marks off again, so that a graph that replays
-// a call with its tag finds none.
+// a call with its tag finds none.  A mark is 64 bits of the tag and the part's
+// number: what else has been in the workspace does not look like one.
+__device__ __forceinline__ unsigned long long mark_of(const AttendArgs &a, int part) {
+  return static_cast<unsigned long long>(static_cast<uint32_t>(a.tag)) * 0x9e3779b97f4a7c15ull ^
+         static_cast<unsigned long long>(part + 1);
+}
 template <int D>
 __device__ __forceinline__ void mark_and_join(const AttendArgs &a, const Segment &g, int s, int row, int32_t *complete) {
   const Joint jt = {g.last, g.tok0, g.ntok0, g.ntok1, g.hk, {}};
@@ -645,12 +650,14 @@ __device__ __forceinline__ void mark_and_join(const AttendArgs &a, const Segment
   meet();
   if (row == 0) {
     *complete = 1;
-    *reinterpret_cast<volatile int32_t *>(a.marks + g.part) = a.tag;
+    *reinterpret_cast<volatile unsigned long long *>(a.marks + g.part) = mark_of(a, g.part);
     __threadfence();
   }
   meet();
-  for (int q = row; q < n; q += kRows)
-    if (*reinterpret_cast<volatile int32_t *>(a.marks + part_of(g.first, q)) != a.tag) *complete = 0;
+  for (int q = row; q < n; q += kRows) {
+    const int part = part_of(g.first, q);
+    if (*reinterpret_cast<volatile unsigned long long *>(a.marks + part) != mark_of(a, part)) *complete = 0;
+  }
   meet();
   if (*reinterpret_cast<volatile int32_t *>(complete) == 0) return;
   __threadfence();
@@ -1084,7 +1091,7 @@ cudaError_t launch(AttendArgs a, cudaStream_t st) {
 
 // joints | the parts' marks | (reference, sum) of each part's rows | their outputs
 constexpr size_t kJointBytes = (sizeof(Joint) * 2 * kMaxGrid + 255) / 256 * 256;
-constexpr size_t kMarkBytes = (sizeof(int32_t) * 2 * 2 * kMaxGrid + 255) / 256 * 256;
+constexpr size_t kMarkBytes = (sizeof(unsigned long long) * 2 * 2 * kMaxGrid + 255) / 256 * 256;
 size_t attention_workspace(int64_t T, int32_t G, int32_t D) {
   const size_t rows = all_part_rows(T, G);
   return kJointBytes + kMarkBytes + round256(rows * sizeof(float2)) + rows * D * sizeof(float);
@@ -1096,7 +1103,7 @@ cudaError_t launch_attention(const AttendArgs &args, cudaStream_t st) {
   a.tile_tokens = tile_tokens(a.Hq, a.Hkv);
   char *ws = static_cast<char *>(a.ws);
   a.joints = reinterpret_cast<Joint *>(ws);
-  a.marks = reinterpret_cast<int32_t *>(ws + kJointBytes);
+  a.marks = reinterpret_cast<unsigned long long *>(ws + kJointBytes);
   a.part_ml = reinterpret_cast<float2 *>(ws + kJointBytes + kMarkBytes);
   a.part_o = reinterpret_cast<float *>(ws + kJointBytes + kMarkBytes + round256(all_part_rows(a.T, G) * sizeof(float2)));
   // The rows of a request, on average: up to one tile's the bytes of its keys

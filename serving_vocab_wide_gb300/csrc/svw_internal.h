@@ -293,7 +293,7 @@ struct AttendArgs {
   int32_t tile_tokens;  // tokens of a row tile
   int32_t part_rows;    // rows of a workspace part
   AttendJoint *joints;  // [workers]
-  int32_t *marks;       // [2 workers] parts that are written, by the call's tag
+  unsigned long long *marks;  // [2 workers] parts that are written, by the call's tag
   float2 *part_ml;      // [2 workers][part_rows] reference and sum
   float *part_o;        // [2 workers][part_rows][D] unnormalised output
 };
