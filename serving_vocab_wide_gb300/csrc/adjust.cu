@@ -820,11 +820,21 @@ void *rows_kernel(int row_vecs) {  // full chunks
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-constexpr int64_t kFew = 152;          // chunks of a small batch: not one per SM
-constexpr int64_t kShortList = 4096;   // tokens of a request's lists, on average, that its chunks count themselves
+constexpr int64_t kFew = 152;         // CTAs: one per SM
+constexpr int64_t kShortList = 4096;  // tokens of a request's lists, on average, that its chunks count themselves
+constexpr int64_t kSmall = 15;        // rows' chunks per SM of a small batch, if lists are short
 
-bool by_lists(int64_t N, int64_t V, int64_t listed) {
-  return N * ((V + kChunk - 1) / kChunk) >= kFew || listed / N > kShortList;
+// Whether the lists are worth a launch of their own: a chunk that counts for
+// itself reads all its request's tokens, and its rows pass through registers.
+// Rows' chunks per SM times (1 + tokens / 2048) is where the two are even on the
+// GPU (us, chunks against lists; bf16, drawn tokens, masks):
+//   16 requests of 4 rows of 134840, 14 per SM: 127 tokens 11.4 / 14.9, 1023 14.2 / 16.7, 3999 19.4 / 18.8;
+//   40 of 1 of 52776, 3.4: 3999 tokens 12.2 / 14.7, 8191 17.8 / 18.3;
+//   200 of 4 of 5169, 11: 127 tokens 12.7 / 15.2, 1023 19.7 / 18.8;  of 52776, 68: 127 tokens 51 / 40;
+// the host is 10 us sooner done with one launch.
+bool by_lists(int64_t N, int64_t V, int64_t rows, int64_t listed) {
+  const int64_t chunks = (V + kChunk - 1) / kChunk, each = listed / N;
+  return each > kShortList || rows * chunks * (2048 + each) > kSmall * kFew * 2048;
 }
 
 // CTAs of a request's rows, so that there are about `want` in all
@@ -855,7 +865,7 @@ cudaError_t allow_shared() {
 // offsets of each request's chunks, its end and whether it is bad | entries
 size_t adjust_workspace(int64_t N, int64_t V, int64_t R, int64_t total_history, int64_t total_bias) {
   const int64_t listed = R + total_history + total_bias;
-  if (!by_lists(N, V, listed)) return 0;
+  if (!by_lists(N, V, R + N, listed)) return 0;
   return round256(static_cast<size_t>(N) * ((V + kChunk - 1) / kChunk + 2) * 4) + round256(static_cast<size_t>(listed) * sizeof(int4));
 }
 
@@ -864,7 +874,7 @@ cudaError_t launch_adjust(const AdjustArgs &args, int dtype, cudaStream_t st) {
   const int es = dtype == SVW_BF16 ? 2 : 4;
   const uintptr_t apart = reinterpret_cast<uintptr_t>(a.logits) - reinterpret_cast<uintptr_t>(a.out);
   const bool vec = (apart & 15u) == 0 && ((a.in_stride - a.out_stride) * es) % 16 == 0;
-  const bool lists = a.ws && by_lists(a.N, a.V, a.R + a.total_history + a.total_bias);
+  const bool lists = a.ws && by_lists(a.N, a.V, a.R + a.N, a.R + a.total_history + a.total_bias);
   a.chunk_len = kChunk;
   a.list_chunks = static_cast<int32_t>((a.V + kChunk - 1) / kChunk);
   // in place without a mask there is nothing to stream: the CTAs share out the lists evenly

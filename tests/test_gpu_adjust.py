@@ -102,8 +102,9 @@ def _compare(got, c, reference=None, rows=slice(None)):
 SHAPES = [([0], 40, "bf16"), ([1], 1, "fp32"), ([3, 0, 16, 1], 1000, "bf16"), ([3, 0, 16, 1], 1001, "bf16"),
           ([2, 5], 5003, "fp32"), ([32, 32], 8192, "fp32"), ([4] * 9, 32001, "bf16"), ([16, 2, 8], 151936, "bf16"),
           ([1] * 40, 4104, "bf16"), ([7], 70000, "fp32"),
-          # enough requests that their lists are counted first
-          ([3, 0] * 23, 32001, "bf16"), ([2] * 64, 20488, "fp32"), ([1] * 310, 300, "bf16")]
+          # more requests; then enough that their lists are counted first
+          ([3, 0] * 23, 32001, "bf16"), ([2] * 64, 20488, "fp32"), ([1] * 310, 300, "bf16"),
+          ([3, 0] * 64, 32001, "bf16"), ([2] * 150, 20488, "fp32"), ([1] * 1200, 300, "bf16")]
 
 
 @pytest.mark.parametrize("lens,V,dtype", SHAPES)
@@ -366,7 +367,7 @@ def test_adjust_bad_requests_of_a_large_batch():
     are right; a workspace of the caller's, whatever it holds."""
     import serving_vocab_wide_gb300 as svw
     import torch
-    V, N = 5000, 200
+    V, N = 5000, 600
     for which in ("history token", "draft token", "repetition", "bias value", "overlap"):
         c = _case(81, [1, 2] * (N // 2), V, "bf16", hist=(5, 30))
         good = _reference(c)

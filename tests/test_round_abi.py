@@ -29,7 +29,7 @@ def _adjust(svw, **o):
     ({"tok": None}, INVALID), ({"hist": None}, INVALID), ({"bv": None}, INVALID), ({"ls": 99}, INVALID),
     ({"os": 99}, INVALID), ({"mrow": None}, INVALID), ({"logits": P + 1}, MISALIGNED), ({"cu": P + 2}, MISALIGNED),
     ({"mask": P + 2}, MISALIGNED), ({"out": P + 64}, INVALID), ({"out": P, "os": 104}, INVALID),
-    ({"ws": P + 16}, MISALIGNED), ({"N": 500, "V": 8192, "ls": 8192, "os": 8192, "mr": 503, "ws": P, "wb": 256}, WORKSPACE),
+    ({"ws": P + 16}, MISALIGNED), ({"N": 500, "V": 65536, "ls": 65536, "os": 65536, "mr": 503, "ws": P, "wb": 256}, WORKSPACE),
     ({"R": 0, "tok": None, "bonus": 0, "mask": None}, OK)])
 def test_adjust_validates(svw, o, want):
     assert _adjust(svw, **o) == want
