@@ -113,7 +113,7 @@ struct Lane {  // of a worker
   unsigned long long seg_full[kSegRing], seg_empty[kSegRing];
   Segment seg[kSegRing];
   int32_t seg_bad[kSegRing];
-  int32_t issued, q_issued;  // ring tiles, query tiles
+  int32_t issued[2], q_issued;  // key tiles, value tiles; query tiles
   int32_t first_req;
   int64_t first_at;
 };
@@ -256,6 +256,24 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// Four lanes' 16-byte pieces transposed: lane 4 i + c has piece c of lanes
+// 4 i + r, r = 0 .. 3, so that they store 64 bytes of a row in one piece.
+__device__ __forceinline__ void turn_pieces(uint32_t (&p)[4][4]) {
+#pragma unroll
+  for (int bit = 1; bit < 4; bit <<= 1) {
+    const bool up = (threadIdx.x & bit) != 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & bit) continue;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? p[k][w] : p[k + bit][w], bit);
+        (up ? p[k][w] : p[k + bit][w]) = got;
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // the line of work
 // ---------------------------------------------------------------------------
@@ -307,7 +325,10 @@ __device__ __forceinline__ bool warp_wait(unsigned long long *bar, uint32_t pari
 __device__ __forceinline__ uint32_t par(int32_t n) { return static_cast<uint32_t>(n & 1); }
 
 // -------------------------------- the loader --------------------------------
-template <int D, bool kWide, typename C>
+// A worker's keys, values or both (kinds [kFrom, kTo)).  The copies of a tile's
+// pages go out one by one, 0.1 us each, so the wide form has a warp for each
+// kind; the keys' loader also announces the segments and loads the queries.
+template <int D, bool kWide, int kFrom, int kTo, typename C>
 __device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtensorMap &tmK, const CUtensorMap &tmV,
                                             const AttendArgs &a, C &sm, int wk, int worker, int64_t W, int64_t b,
                                             int64_t e, int64_t workers, uint32_t q_smem, uint32_t ring) {
@@ -319,7 +340,8 @@ __device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtens
   const int shift = 31 - __clz(a.page_size);
   const int32_t step = Sh::kTiles * a.tile_tokens;
   int64_t at = ln.first_at;
-  int32_t count = 0, qc = 0, k = 0;  // ring tiles, query tiles, segments so far
+  int32_t count = 0, qc = 0, k = 0;  // tiles of a kind, query tiles, segments so far
+  int32_t sent[2] = {0, 0};
   bool ok = true;
   Joint joint = {-1, 0, 0, 0, 0, {}};
   for (int32_t i = ln.first_req; i < a.N && at < e && ok; ++i) {
@@ -345,11 +367,11 @@ __device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtens
         int32_t ids = (p_base + lane < p_end) ? __ldg(table + p_base + lane) : 0;
         int32_t next_ids = (p_base + 32 + lane < p_end) ? __ldg(table + p_base + 32 + lane) : 0;
         const int sl = k % kSegRing;
-        ok = k < kSegRing || warp_wait(&ln.seg_empty[sl], par(k / kSegRing - 1));
+        ok = kFrom > 0 || k < kSegRing || warp_wait(&ln.seg_empty[sl], par(k / kSegRing - 1));
         if (!ok) break;
         const bool whole = (j0 == 0 && j1 == k1 - k0);
         const int32_t ntok0 = min(nt, a.tile_tokens), ntok1 = nt - ntok0;
-        if (lane == 0) {
+        if (kFrom == 0 && lane == 0) {
           Segment &s = ln.seg[sl];
           s.tiles = j1 - j0;
           s.tok0 = r.c0 + t0;
@@ -375,8 +397,8 @@ __device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtens
         }
         ++k;
         // the queries: the two tiles of a wide unit, one buffer each; the worker's one otherwise
-        ok = qc == 0 || warp_wait(&sm.q_empty[wk], par(qc - 1));
-        if (ok && lane == 0) {
+        ok = kFrom > 0 || qc == 0 || warp_wait(&sm.q_empty[wk], par(qc - 1));
+        if (kFrom == 0 && ok && lane == 0) {
           const int tiles = kWide ? 2 : 1;
           mbar_arrive_expect_tx(&sm.q_full[wk], static_cast<uint32_t>(tiles * G * a.tile_tokens * D * 2));
           for (int s = 0; s < tiles; ++s)
@@ -387,7 +409,7 @@ __device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtens
         ++qc;
         // the keys and values, a lane per page
         bool bad = false;
-        for (int32_t j = j0; j < j1 && ok; ++j) {
+        for (int32_t j = j0; j < j1 && ok; ++j, ++count) {
           const int32_t key = (k0 + j) * Sh::kKeys;
           const int32_t have = max(0, min(Sh::kKeys, r.kv - key));
           const int need = (have + box - 1) / box;  // pages that hold keys of the request
@@ -402,15 +424,16 @@ __device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtens
             page = a.n_pages;  // outside the tensor: reads as zeros
           }
           const int row = key & (a.page_size - 1);  // 0 unless a page holds several tiles
-          for (int v = 0; v < 2 && ok; ++v, ++count) {
-            const int s = count % Sh::kRing;
-            ok = count < Sh::kRing || warp_wait(&ln.empty[s], par(count / Sh::kRing - 1));
+          for (int v = kFrom; v < kTo && ok; ++v) {
+            const int n = 2 * count + v, s = n % Sh::kRing;
+            ok = n < Sh::kRing || warp_wait(&ln.empty[s], par(n / Sh::kRing - 1));
             if (!ok) break;
-            if (v == 1 && j == j1 - 1 && __any_sync(0xffffffffu, bad) && lane == 0) {
-              ln.seg_bad[sl] = 1;  // the last arrival of the segment carries this to its epilogue
+            if (v == 0 && j == j1 - 1 && __any_sync(0xffffffffu, bad) && lane == 0) {
+              ln.seg_bad[sl] = 1;  // the last keys' arrival carries this to the segment's epilogue
               if (a.status) atomicOr(a.status, SVW_DEV_BAD_INPUT);
             }
             if (lane == 0) mbar_arrive_expect_tx(&ln.full[s], static_cast<uint32_t>(need * box * D * 2));
+            ++sent[v];
             __syncwarp();
             if (lane < need) {
               const uint32_t dst = ring + s * Sh::kTile + lane * box * 128;
@@ -423,17 +446,18 @@ __device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtens
     }
   }
   // the end marker
-  if (ok) ok = k < kSegRing || warp_wait(&ln.seg_empty[k % kSegRing], par(k / kSegRing - 1));
+  if (kFrom == 0 && ok) ok = k < kSegRing || warp_wait(&ln.seg_empty[k % kSegRing], par(k / kSegRing - 1));
   if (lane == 0) {
-    if (ok) {
-      ln.seg[k % kSegRing].tiles = 0;
-      mbar_arrive(&ln.seg_full[k % kSegRing]);
-    } else {
-      atomicOr(&sm.err, 1);
+    if (!ok) atomicOr(&sm.err, 1);
+    for (int v = kFrom; v < kTo; ++v) ln.issued[v] = sent[v];
+    if (kFrom == 0) {
+      if (ok) {
+        ln.seg[k % kSegRing].tiles = 0;
+        mbar_arrive(&ln.seg_full[k % kSegRing]);
+      }
+      ln.q_issued = qc;
+      a.joints[worker] = joint;
     }
-    ln.issued = count;
-    ln.q_issued = qc;
-    a.joints[worker] = joint;
   }
 }
 
@@ -779,25 +803,39 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
     if (warp_live) {
       if (*reinterpret_cast<volatile int32_t *>(&ln.seg_bad[sl]) != 0) l = kNaN;
       const int32_t tok = g.tok0 + tile * a.tile_tokens + tok_of_row;
-      const int64_t orow = static_cast<int64_t>(tok) * a.Hq + g.hk * G + head_of_row;
+      const int32_t orow = live ? tok * a.Hq + g.hk * G + head_of_row : -1;  // below 2^31, checked by the host
       const int64_t prow = static_cast<int64_t>(max(g.part, 0)) * a.part_rows + tile * kRows + row;
       const float inv = (g.part >= 0) ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+      int32_t to[4];  // the rows of this lane's four, and its piece of each
+#pragma unroll
+      for (int q = 0; q < 4; ++q) to[q] = __shfl_sync(0xffffffffu, orow, (lane & ~3) + q);
+      const int piece = lane & 3;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32];
         tmem_ld32(t_o + c, o);
         tmem_wait_ld();
-        if (!live) continue;
+        uint32_t p[4][4];
         if (g.part < 0) {
-          uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + orow * D + c);
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            dst[v] = make_uint4(pack_bf16(o[8 * v] * inv, o[8 * v + 1] * inv), pack_bf16(o[8 * v + 2] * inv, o[8 * v + 3] * inv),
-                                pack_bf16(o[8 * v + 4] * inv, o[8 * v + 5] * inv), pack_bf16(o[8 * v + 6] * inv, o[8 * v + 7] * inv));
+          for (int v = 0; v < 16; ++v) p[v >> 2][v & 3] = pack_bf16(o[2 * v] * inv, o[2 * v + 1] * inv);
+          turn_pieces(p);
+          __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(a.out) + c + piece * 8;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (to[q] >= 0)
+              *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(to[q]) * D) = make_uint4(p[q][0], p[q][1], p[q][2], p[q][3]);
         } else {
-          float4 *dst = reinterpret_cast<float4 *>(a.part_o + prow * D + c);
+          float *dst = a.part_o + (prow - piece) * D + c + piece * 4;
 #pragma unroll
-          for (int v = 0; v < 8; ++v) dst[v] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int v = 0; v < 16; ++v) p[v >> 2][v & 3] = __float_as_uint(o[h * 16 + v]);
+            turn_pieces(p);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (to[q] >= 0) *reinterpret_cast<uint4 *>(dst + q * D + h * 16) = make_uint4(p[q][0], p[q][1], p[q][2], p[q][3]);
+          }
         }
       }
       if (live) {
@@ -851,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&ln.seg_full[s], 1);
         mbar_init(&ln.seg_empty[s], Sh::kSoftWarps + 1);
       }
-      ln.issued = 0;
+      ln.issued[0] = ln.issued[1] = 0;
       ln.q_issued = 0;
       ln.first_req = a.N;
       ln.first_at = 0;
@@ -934,20 +972,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t q_smem = base + Sh::kControl, ring = q_smem + 2 * Sh::kQTile;
   constexpr int kRingBytes = Sh::kRing * Sh::kTile;
 
-  // a loader and an issuer per worker; softmax warps from the fifth on
+  // loaders and an issuer per worker; softmax warps from the fifth on
   if (warp < 4) {
     // the launch has 168 registers for each of 384 threads: 128 * 72 + 256 * 216
     if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    const int wk = warp >> 1;
-    if (wk < Sh::kWorkers) {
-      if (warp & 1) {
-        issue_worker<D, kWide>(sm, wk, q_smem + wk * Sh::kQTile, ring + wk * kRingBytes, tmem);
-      } else {
-        const int64_t id = static_cast<int64_t>(blockIdx.x) * Sh::kWorkers + wk;
-        load_worker<D, kWide>(tmQ, tmK, tmV, a, sm, wk, static_cast<int>(id), W, line(id),
-                              line(id + 1), workers, q_smem + wk * Sh::kQTile, ring + wk * kRingBytes);
-      }
-    }
+    const int wk = kWide ? 0 : warp >> 1;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * Sh::kWorkers + wk;
+    const uint32_t my_q = q_smem + wk * Sh::kQTile, my_ring = ring + wk * kRingBytes;
+    if (warp == 1 || (!kWide && warp == 3))
+      issue_worker<D, kWide>(sm, wk, my_q, my_ring, tmem);
+    else if (!kWide)
+      load_worker<D, kWide, 0, 2>(tmQ, tmK, tmV, a, sm, wk, static_cast<int>(id), W, line(id), line(id + 1), workers, my_q, my_ring);
+    else if (warp == 0)
+      load_worker<D, kWide, 0, 1>(tmQ, tmK, tmV, a, sm, wk, static_cast<int>(id), W, line(id), line(id + 1), workers, my_q, my_ring);
+    else if (warp == 2)
+      load_worker<D, kWide, 1, 2>(tmQ, tmK, tmV, a, sm, wk, static_cast<int>(id), W, line(id), line(id + 1), workers, my_q, my_ring);
   } else {
     if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int st = (warp - 4) >> 2;
@@ -960,8 +999,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (a.status) atomicOr(a.status, SVW_DEV_TIMEOUT);
       for (int w = 0; w < Sh::kWorkers; ++w) {
         auto &ln = sm.lane[w];
-        for (int32_t c = max(0, ln.issued - Sh::kRing); c < ln.issued; ++c)
+        // each slot's last tile: 2 n + v is the n-th of kind v
+        uint32_t seen = 0;
+        for (int32_t c = 2 * max(ln.issued[0], ln.issued[1]) - 1, q = 0; c >= 0 && q < 3 * Sh::kRing; --c, ++q) {
+          if (c / 2 >= ln.issued[c & 1] || (seen >> (c % Sh::kRing) & 1u)) continue;
+          seen |= 1u << (c % Sh::kRing);
           mbar_wait_bounded(&ln.full[c % Sh::kRing], par(c / Sh::kRing));
+        }
         if (ln.q_issued > 0) mbar_wait_bounded(&sm.q_full[w], par(ln.q_issued - 1));
       }
     }
