@@ -78,6 +78,7 @@ struct Shape {
   static constexpr int kKeys = kWide ? 128 : 64;           // keys of a tile
   static constexpr int kTiles = kWide ? 2 : 1;             // row tiles of a unit, at most
   static constexpr int kBufs = kWide ? 1 : 2;              // score buffers of a stage
+  static constexpr bool kApart = kWide && D == 64;         // weights in columns of their own, not over their scores
   static constexpr int kSoftWarps = kWide ? 8 : 4;         // softmax warps of a worker
   static constexpr int kUnitCost = kWide ? 1 : 2;          // a unit's fixed cost on the line, in key tiles
   static constexpr int kHalves = D / 64;                   // 128-byte columns of a tile
@@ -88,6 +89,8 @@ struct Shape {
   static constexpr int kRing = (D == 128) ? 5 : 11;        // key and value tiles in flight of a worker
   static constexpr int kControl = (D == 128) ? 3072 : 4096;
   static constexpr int kSmem = kControl + 2 * kQTile + kWorkers * kRing * kTile;
+  // columns of tensor memory: scores of stage st, buffer u at st * 128 + u * 64; outputs at 256 + st * D; weights:
+  __host__ __device__ static constexpr int weights(int st, int u) { return kApart ? 384 + st * 64 : st * 128 + u * 64; }
 };
 static_assert(Shape<128, true>::kSmem <= 232448 && Shape<128, false>::kSmem <= 232448, "shared memory");
 static_assert(Shape<64, true>::kSmem <= 232448 && Shape<64, false>::kSmem <= 232448, "shared memory");
@@ -122,7 +125,8 @@ struct Control {
   Lane<kRing> lane[kWorkers];
   unsigned long long q_full[2], q_empty[2];
   unsigned long long s_full[4], p_full[4];  // 2 * stage + score buffer
-  unsigned long long o_full[2], o_free[2], o_step[2];  // by stage: a segment's outputs; read; each tile's (narrow)
+  unsigned long long s_read[2];             // by stage (apart): the scores are in registers
+  unsigned long long o_full[2], o_free[2], o_step[2];  // by stage: a segment's outputs; read; each tile's (narrow, apart)
   uint32_t tmem;
   int32_t err;
   int32_t complete[2];  // by stage: every part of the unit is there
@@ -498,8 +502,8 @@ __device__ __forceinline__ void issue_worker(C &sm, int wk, uint32_t q_smem, uin
     const uint64_t va = sw128(ring + t.slot * Sh::kTile, Sh::kHalf);
 #pragma unroll
     for (int h = 0; h < Sh::kKeys / 64; ++h)  // a row's weights of 64 keys take 32 columns
-      mma_ts_x4(tmem + 256 + st * D, tmem + st * 128 + u * 64 + h * 32, va + h * 512, id_o, (acc || h > 0) ? 1u : 0u);
-    if (!kWide) tc_commit(smem_u32(&sm.o_step[st]));
+      mma_ts_x4(tmem + 256 + st * D, tmem + Sh::weights(st, u) + h * 32, va + h * 512, id_o, (acc || h > 0) ? 1u : 0u);
+    if (!kWide || Sh::kApart) tc_commit(smem_u32(&sm.o_step[st]));
   };
   auto release = [&](const At &t) { tc_commit(smem_u32(&ln.empty[t.slot])); };
   while (ok) {
@@ -527,6 +531,35 @@ __device__ __forceinline__ void issue_worker(C &sm, int wk, uint32_t q_smem, uin
     constexpr int kLead = kWide ? 1 : 2;  // a score buffer's next key tile
     for (int32_t j = 0; j < n && ok; ++j) {
       const bool more = j + kLead < n;
+      if (Sh::kApart) {
+        // the next scores as soon as these are read, beside the softmax of these
+        if (more && !wait_ring(kt)) break;
+#pragma unroll
+        for (int i = 0; i < 2 && ok; ++i) {
+          if (more && !(ok = warp_wait(&sm.s_read[i], par(sc[i])))) break;
+          tc_after();
+          if (elect_one()) {
+            if (more) scores(i, 0, kt);
+            if (more && i == 1) release(kt);
+            if (i == 1 && j == max(0, n - 2)) tc_commit(smem_u32(&sm.q_empty[0]));
+          }
+        }
+        if (!ok || !wait_ring(vt)) break;
+#pragma unroll
+        for (int i = 0; i < 2 && ok; ++i) {
+          if (!(ok = warp_wait(&sm.p_full[2 * i], par(sc[i])))) break;
+          ++sc[i];
+          if (j == 0 && k > 0 && !(ok = warp_wait(&sm.o_free[i], par(k - 1)))) break;
+          tc_after();
+          if (elect_one()) {
+            output(i, 0, vt, j > 0);
+            if (i == 1) release(vt);
+          }
+        }
+        vt.two_on();
+        if (more) kt.two_on();
+        continue;
+      }
       if (!wait_ring(vt)) break;
       if (kWide && more && !wait_ring(kt)) break;  // there long before; narrow: its values' weights come first
 #pragma unroll
@@ -700,7 +733,7 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
   const int G = a.Hq / a.Hkv;
   const int tok_of_row = row / G, head_of_row = row - tok_of_row * G;
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-  const uint32_t t_s = tmem + lanes + s * 128;
+  const uint32_t t_s = tmem + lanes + s * 128, t_p = tmem + lanes + Sh::weights(s, 0);
   const uint32_t t_o = tmem + lanes + 256 + s * D;
   const float k2 = a.scale * kLog2e;
   int32_t count = 0, k = 0, steps = 0, sc[2] = {0, 0};  // ring tiles, segments, outputs, score tiles by buffer
@@ -731,6 +764,11 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
 #pragma unroll
         for (int c = 0; c < Sh::kKeys; c += 32) tmem_ld32(t_su + c, x + c);
         tmem_wait_ld();
+        if (Sh::kApart) {
+          tc_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.s_read[s]);
+        }
         if (!__all_sync(0xffffffffu, key >= lo && key + Sh::kKeys <= hi)) {
           const int32_t from = key - lo;  // key + c is seen where 0 <= c + from < hi - lo
           const uint32_t seen = static_cast<uint32_t>(max(0, hi - lo));
@@ -746,10 +784,13 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
         const float f = grow ? (M == -INFINITY ? 0.f : ex2(M - top)) : 1.f;
         if (grow) M = top;
         l *= f;
-        if (j > 0 && __any_sync(0xffffffffu, grow)) {
-          // the outputs so far are complete (wide: the scores' arrival said so)
-          if (!kWide && !(ok = warp_wait(&sm.o_step[s], par(steps + j - 1)))) break;
-          if (!kWide) tc_after();
+        // the outputs so far are complete, and the weights read (wide, not apart: the scores' arrival said so)
+        const bool rescale = j > 0 && __any_sync(0xffffffffu, grow);
+        if (Sh::kApart ? j > 0 : (!kWide && rescale)) {
+          if (!(ok = warp_wait(&sm.o_step[s], par(steps + j - 1)))) break;
+          tc_after();
+        }
+        if (rescale) {
 #pragma unroll
           for (int c = 0; c < D; c += 16) {
             float o[16];
@@ -776,10 +817,14 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
               sum0 = __fadd2_rn(sum0, p);
             w[v] = pack_bf16(p.x, p.y);
           }
-          tmem_st8(t_su + c / 2, w);
+          tmem_st8(t_p + u * 64 + c / 2, w);
         }
         const float2 t = __fadd2_rn(sum0, sum1);
         l += t.x + t.y;
+      } else if (Sh::kApart) {
+        if (lane == 0) mbar_arrive(&sm.s_read[s]);
+        // no further ahead than the others: two arrivals of a warp must not fall into one phase of p_full
+        if (j > 0 && !(ok = warp_wait(&sm.o_step[s], par(steps + j - 1)))) break;
       }
       if (key + Sh::kKeys > g.kv) {
         // value rows beyond the request's keys: whatever is there must not meet a weight of zero
@@ -900,6 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.o_full[s], 2);
       mbar_init(&sm.o_free[s], 4);
       mbar_init(&sm.o_step[s], 1);
+      mbar_init(&sm.s_read[s], 4);
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&sm.s_full[s], 1);

@@ -271,6 +271,11 @@ ATTEND = [
     ([5, 3], [0, 0], 4, 2, 64, 16, False, {"causal": False}),  # no keys at all
     ([260], [2000], 1, 1, 128, 64, False, {}),
     ([70, 70, 70], [70, 1500, 333], 3, 1, 64, 32, False, {"scale": 2.0}),
+    # many tiles to a worker, and row tiles of which some or all rows have no token
+    ([150, 45, 200], [4000, 3001, 5003], 8, 8, 64, 32, False, {}),
+    ([150, 45, 200], [4000, 3001, 5003], 8, 8, 128, 16, False, {}),
+    ([150, 45, 200], [4000, 3001, 5003], 8, 8, 64, 64, False, {"causal": False}),
+    ([60, 3, 77], [5000, 4001, 3333], 20, 4, 64, 128, False, {"window": 2500}),
 ]
 
 
