@@ -778,12 +778,31 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
         }
         float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int c = 4; c < Sh::kKeys; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
+        for (int c = 4; c < Sh::kKeys; c += 4)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) mx[v] = fmaxf(mx[v], x[c + v]);
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * k2;
         const bool grow = live && (top > M + kGrow || (M == -INFINITY && top > M));
         const float f = grow ? (M == -INFINITY ? 0.f : ex2(M - top)) : 1.f;
         if (grow) M = top;
         l *= f;
+        const float ref = (M == -INFINITY) ? 0.f : M;
+        const float2 kk = make_float2(k2, k2), nr = make_float2(-ref, -ref);
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+        uint32_t w[Sh::kKeys / 2];
+#pragma unroll
+        for (int c = 0; c < Sh::kKeys / 2; ++c) {
+          const float2 d = __ffma2_rn(make_float2(x[2 * c], x[2 * c + 1]), kk, nr);
+          const float2 p = make_float2(ex2(d.x), ex2(d.y));
+          if (c & 1)
+            sum1 = __fadd2_rn(sum1, p);
+          else
+            sum0 = __fadd2_rn(sum0, p);
+          w[c] = pack_bf16(p.x, p.y);
+          if (!Sh::kApart && (c & 7) == 7) tmem_st8(t_p + u * 64 + (c - 7), w + (c - 7));
+        }
+        const float2 t = __fadd2_rn(sum0, sum1);
+        l += t.x + t.y;
         // the outputs so far are complete, and the weights read (wide, not apart: the scores' arrival said so)
         const bool rescale = j > 0 && __any_sync(0xffffffffu, grow);
         if (Sh::kApart ? j > 0 : (!kWide && rescale)) {
@@ -801,26 +820,10 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
             tmem_st16(t_o + c, o);
           }
         }
-        const float ref = (M == -INFINITY) ? 0.f : M;
-        const float2 kk = make_float2(k2, k2), nr = make_float2(-ref, -ref);
-        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+        if (Sh::kApart) {
 #pragma unroll
-        for (int c = 0; c < Sh::kKeys; c += 16) {
-          uint32_t w[8];
-#pragma unroll
-          for (int v = 0; v < 8; ++v) {
-            const float2 d = __ffma2_rn(make_float2(x[c + 2 * v], x[c + 2 * v + 1]), kk, nr);
-            const float2 p = make_float2(ex2(d.x), ex2(d.y));
-            if (v & 1)
-              sum1 = __fadd2_rn(sum1, p);
-            else
-              sum0 = __fadd2_rn(sum0, p);
-            w[v] = pack_bf16(p.x, p.y);
-          }
-          tmem_st8(t_p + u * 64 + c / 2, w);
+          for (int c = 0; c < Sh::kKeys / 2; c += 8) tmem_st8(t_p + u * 64 + c, w + c);
         }
-        const float2 t = __fadd2_rn(sum0, sum1);
-        l += t.x + t.y;
       } else if (Sh::kApart) {
         if (lane == 0) mbar_arrive(&sm.s_read[s]);
         // no further ahead than the others: two arrivals of a warp must not fall into one phase of p_full
