@@ -11,7 +11,7 @@
 // queries may be rotated in place), whose loads are under way before the
 // token's request has been found.  Two tokens a row, to search once for both,
 // were slower (18 us against 16 where a slot a thread was), and a torch copy of
-// 27 MB takes 9.9 us where rotating and scattering them takes 13.0.
+// 27 MB takes 9.9 us where rotating and scattering them takes 12.1.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -141,101 +141,92 @@ __device__ __forceinline__ void turn(float &x, float &y, float c, float s) {
   y = __fadd_rn(__fmul_rn(r, c), __fmul_rn(p, s));
 }
 
-// the rotation of a slot's two vectors
+// The cosines and sines of a slot's pairs: of the elements x .. x + N - 1 with
+// half a rotation further (halves), or of the N pairs of neighbours from x on.
 template <typename T>
-__device__ __forceinline__ void rotate_slot(const Place &p, bool halves, int x, int half, uint4 &u, uint4 &w) {
-  constexpr int N = Vec<T>::N;
-  // four pairs at a time: of the two halves, or of neighbours within each vector
-  const float4 nan = make_float4(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff), __int_as_float(0x7fffffff),
-                                 __int_as_float(0x7fffffff));
-  const float *cs = p.cs + (halves ? x : x / 2);
+struct Turns {
+  static constexpr int N = Vec<T>::N;
+  float4 c[N / 4], s[N / 4];
+  __device__ void load(const Place &p, bool halves, int x, int half) {
+    const float *cs = p.cs + (halves ? x : x / 2);
+    const float nan = __int_as_float(0x7fffffff);
 #pragma unroll
-  for (int q = 0; q < N / 4; ++q) {
-    float4 c = nan, s = nan;
-    if (p.pos_ok) {
-      c = __ldg(reinterpret_cast<const float4 *>(cs + 4 * q));
-      s = __ldg(reinterpret_cast<const float4 *>(cs + half + 4 * q));
-    }
-    if (halves) {
-      float4 f = Vec<T>::get(u, q), g = Vec<T>::get(w, q);
-      turn(f.x, g.x, c.x, s.x);
-      turn(f.y, g.y, c.y, s.y);
-      turn(f.z, g.z, c.z, s.z);
-      turn(f.w, g.w, c.w, s.w);
-      Vec<T>::put(u, q, f);
-      Vec<T>::put(w, q, g);
-    } else if (N == 8) {  // four pairs are one vector
-      uint4 &m = q ? w : u;
-      float4 f = Vec<T>::get(m, 0), g = Vec<T>::get(m, 1);
-      turn(f.x, f.y, c.x, s.x);
-      turn(f.z, f.w, c.y, s.y);
-      turn(g.x, g.y, c.z, s.z);
-      turn(g.z, g.w, c.w, s.w);
-      Vec<T>::put(m, 0, f);
-      Vec<T>::put(m, 1, g);
-    } else {  // two pairs in each
-      float4 f = Vec<T>::get(u, 0), g = Vec<T>::get(w, 0);
-      turn(f.x, f.y, c.x, s.x);
-      turn(f.z, f.w, c.y, s.y);
-      turn(g.x, g.y, c.z, s.z);
-      turn(g.z, g.w, c.w, s.w);
-      Vec<T>::put(u, 0, f);
-      Vec<T>::put(w, 0, g);
+    for (int q = 0; q < N / 4; ++q) {
+      c[q] = s[q] = make_float4(nan, nan, nan, nan);
+      if (p.pos_ok) {
+        c[q] = __ldg(reinterpret_cast<const float4 *>(cs + 4 * q));
+        s[q] = __ldg(reinterpret_cast<const float4 *>(cs + half + 4 * q));
+      }
     }
   }
-}
+  // the slot's two vectors rotated
+  __device__ void apply(bool halves, uint4 &u, uint4 &w) const {
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q) {
+      if (halves) {
+        float4 f = Vec<T>::get(u, q), g = Vec<T>::get(w, q);
+        turn(f.x, g.x, c[q].x, s[q].x);
+        turn(f.y, g.y, c[q].y, s[q].y);
+        turn(f.z, g.z, c[q].z, s[q].z);
+        turn(f.w, g.w, c[q].w, s[q].w);
+        Vec<T>::put(u, q, f);
+        Vec<T>::put(w, q, g);
+      } else {  // four pairs: a vector of eight, or two of four
+        uint4 &m = (N == 8 && q == 1) ? w : u, &n = (N == 8) ? m : w;
+        float4 f = Vec<T>::get(m, 0), g = Vec<T>::get(n, N == 8 ? 1 : 0);
+        turn(f.x, f.y, c[q].x, s[q].x);
+        turn(f.z, f.w, c[q].y, s[q].y);
+        turn(g.x, g.y, c[q].z, s[q].z);
+        turn(g.z, g.w, c[q].w, s[q].w);
+        Vec<T>::put(m, 0, f);
+        Vec<T>::put(n, N == 8 ? 1 : 0, g);
+      }
+    }
+  }
+};
 
-// Rows of the block: tokens; kItems slots of a thread under way.  Heads and
-// rotated parts in multiples of two vectors, everything 16-byte aligned.
+// Rows of the block: tokens.  A thread has one slot, two vectors (both halves
+// of its pairs), of every blockDim.x / slots-th head, kItems heads under way:
+// its cosines and sines are read once.  (Read again for each head, with the
+// head found by a division: 12.8 us where this takes 12.1 on 2220 tokens of 48
+// heads of 128, 34.7 where it takes 33.1 on 14 k tokens of 48 heads of 64; 56%
+// of the issue slots were busy.)  Heads and rotated parts in multiples of two
+// vectors, everything 16-byte aligned.
 template <typename T, int kItems>
 __global__ void __launch_bounds__(kItems == 1 ? kAppRow : kAppThreads, kItems == 1 ? 3 : 4) kv_append_vec(const __grid_constant__ AppendArgs a) {
   constexpr int N = Vec<T>::N;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   if (t >= a.T) return;
-  const int slots = a.D / (2 * N), items = (a.Hq + 2 * a.Hkv) * slots;
-  const int half = a.rot / 2;
+  const int slots = a.D / (2 * N), heads = a.Hq + 2 * a.Hkv, step = blockDim.x / slots;
+  const int half = a.rot / 2, h0 = threadIdx.x / slots, sl = threadIdx.x - h0 * slots;
+  const bool halves = !a.interleaved && sl * N < half;
+  const int x = halves ? sl * N : 2 * sl * N, y = halves ? half + sl * N : x + N;
+  const bool turns = x < a.rot;
   Place p;
+  Turns<T> cs;
   bool found = false;
-  for (int m0 = threadIdx.x; m0 - static_cast<int>(threadIdx.x & 31) < items; m0 += kItems * blockDim.x) {
+  for (int h = h0; h - h0 < heads; h += kItems * step) {  // the whole warp as often
     uint4 u[kItems], w[kItems];
-    int at[kItems];  // head, and the first vector's element; -1: no slot
-    // a slot's two vectors: both halves of rotated pairs, or neighbours
-    auto split = [&](int code, int &h, bool &rotates, bool &halves, int &x, int &y) {
-      const int sl = code & 0xffff;
-      h = code >> 16;
-      rotates = h < a.Hkv || h >= 2 * a.Hkv;
-      halves = !a.interleaved && rotates && sl * N < half;
-      x = halves ? sl * N : 2 * sl * N;
-      y = halves ? half + sl * N : x + N;
-    };
 #pragma unroll
     for (int q = 0; q < kItems; ++q) {
-      const int m = m0 + q * blockDim.x;
-      at[q] = -1;
-      if (m < items) {
-        int h = m / slots, x, y;
-        bool rotates, halves;
-        at[q] = (h << 16) | (m - h * slots);
-        split(at[q], h, rotates, halves, x, y);
+      if (h + q * step < heads) {
         const T *src;
-        head_rows<T>(a, t, h, src);
+        head_rows<T>(a, t, h + q * step, src);
         u[q] = *reinterpret_cast<const uint4 *>(src + x);
         w[q] = *reinterpret_cast<const uint4 *>(src + y);
       }
     }
     if (!found) {
       p = find_place(a, t);
+      if (turns) cs.load(p, halves, x, half);
       found = true;
     }
 #pragma unroll
     for (int q = 0; q < kItems; ++q) {
-      if (at[q] < 0) continue;
-      int h, x, y;
-      bool rotates, halves;
-      split(at[q], h, rotates, halves, x, y);
-      if (h < 2 * a.Hkv && !p.write) continue;
-      if (rotates && x < a.rot) rotate_slot<T>(p, halves, x, half, u[q], w[q]);
-      T *dst = head_out<T>(a, p, t, h);
+      const int hq = h + q * step;
+      if (hq >= heads || (hq < 2 * a.Hkv && !p.write)) continue;
+      if (turns && (hq < a.Hkv || hq >= 2 * a.Hkv)) cs.apply(halves, u[q], w[q]);
+      T *dst = head_out<T>(a, p, t, hq);
       *reinterpret_cast<uint4 *>(dst + x) = u[q];
       *reinterpret_cast<uint4 *>(dst + y) = w[q];
     }
@@ -283,20 +274,23 @@ void launch(const AppendArgs &a, cudaStream_t st) {
   for (int d = 0; d < 3; ++d) odd |= a.kc[d] | a.vc[d];
   const bool vec = at16(a.k) && at16(a.v) && at16(a.q) && at16(a.q_out) && at16(a.k_cache) && at16(a.v_cache) &&
                    at16(a.cos_sin) && odd % N == 0 && a.D % (2 * N) == 0 && a.rot % (2 * N) == 0;
-  if (!vec) {
+  // threads of a row: whole warps, and as many for each slot
+  const int slots = vec ? a.D / (2 * N) : 1;
+  int unit = 32;
+  while (unit % slots != 0) unit += 32;
+  if (!vec || unit > kAppThreads) {
     kv_append_any<T><<<static_cast<unsigned>(a.T), kAppThreads, 0, st>>>(a);
     return;
   }
-  // Many tokens: about six slots a thread, in two rounds of three (the second
-  // round's loads run beside the first one's stores; measured on 2220 tokens of
-  // 48 heads of 128 and 14 k tokens of 48 heads of 64: 13.0 and 34.7 us; three
-  // slots in one round 14.1 and 37.3, a slot a thread 16.0 and 41.3).  Few: a
-  // slot a thread, the shortest way through.
-  const int items = (a.Hq + 2 * a.Hkv) * (a.D / (2 * N));
+  // Many tokens: about six heads a thread, in two rounds of three (the second
+  // round's loads run beside the first one's stores): 12.1 and 33.1 us on the
+  // two batches above; three in one round 13.2 and 36.1, in rounds of two 12.7
+  // and 34.2, of four 13.4 and 39.0.  Few: one, the shortest way through.
+  const int items = (a.Hq + 2 * a.Hkv) * slots;
   const bool few = a.T < 2 * 152;
   const int share = few ? items : (items + 5) / 6;
-  const int most = few ? kAppRow : kAppThreads;
-  const int x = share >= most ? most : (share + 31) / 32 * 32;
+  const int most = (few ? kAppRow : kAppThreads) / unit * unit;
+  const int x = share >= most ? most : (share + unit - 1) / unit * unit;
   int y = kAppThreads / x < 1 ? 1 : kAppThreads / x;
   while (y > 1 && (a.T + y - 1) / y < 2 * 152) y /= 2;  // rather more blocks than fuller ones
   const dim3 grid(static_cast<unsigned>((a.T + y - 1) / y)), block(x, y);

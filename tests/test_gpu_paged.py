@@ -72,6 +72,11 @@ APPEND = [
     ([9], [30], 3, 3, 10, 6, True, 1, "fp32", False),
     ([4, 4], [8, 4], 2, 1, 256, 256, False, 16, "bf16", False),
     ([6], [6], 2, 2, 64, 0, False, 16, "bf16", False),
+    # many tokens, and heads whose slots are no power of two
+    ([320, 7, 1], [320, 500, 77], 5, 2, 96, 32, False, 16, "bf16", False),
+    ([330, 2], [600, 2], 9, 3, 80, 80, True, 32, "fp32", True),
+    ([40, 300], [41, 300], 3, 1, 144, 48, False, 16, "bf16", False),
+    ([310], [400], 12, 4, 1024, 512, False, 8, "fp32", False),
 ]
 
 
