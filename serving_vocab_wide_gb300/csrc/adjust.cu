@@ -17,7 +17,7 @@
 // listed entry that is drafted looks through the request's drafts (at most
 // SVW_MAX_LEN).
 //
-// Large batches (given a workspace), 231 us on the benchmark batch (5.9 TB/s):
+// Large batches (given a workspace), 228 us on the benchmark batch (6.0 TB/s):
 //   adjust_lists   a CTA per request lists its distinct tokens, ascending, with
 //                  their counts (20 us, mostly beside the rows' first loads);
 //   adjust_staged  a CTA per chunk of 4096 entries of a request: rows pass
@@ -25,11 +25,13 @@
 //                  the way; seven CTAs of three 8 KB stages per SM (four stages
 //                  and five CTAs: 240 us; the rows in registers and the listed
 //                  entries by a second trip to memory: 329);
-//   adjust_rows    in place, 97 us without masks and 267 with (only what
+//   adjust_rows    in place, 97 us without masks and 265 with (only what
 //                  changes is written), or rows that do not lie alike.
 // Small batches, one launch: adjust_chunks, a CTA counts the tokens of its chunk
-// itself by reading the whole history (on the benchmark batch: 329 us, each of
-// 38 chunks of a request waits for its loads).
+// itself by reading the whole history (4.1 us for one row of 32000; on the
+// benchmark batch: 329, each of 38 chunks of a request waits for its loads.
+// Counting beside staged rows' loads was slower than the lists for all but few
+// requests: 43 us against 39 for 544 fp32 rows of 32003).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
