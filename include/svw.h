@@ -504,10 +504,9 @@ svw_status kv_append(const void *k, int64_t k_token_stride, int64_t k_head_strid
  *              tokens and heads in elements; n_q_heads a multiple of
  *              n_kv_heads, at most 64 times it.
  *   cache      bf16; head_dim 64 or 128; page_size a power of two, 16 to 1024.
- *              Keys and values at places below kv_len must be finite (a row
- *              that a mask hides from a token may still reach it as 0 times
- *              its value); what lies beyond in the last page is not read into
- *              any result.
+ *              What a token does not see (later tokens, places behind its
+ *              window or beyond kv_len) may hold anything, NaN too; block-table
+ *              entries of pages that no token sees are not looked at.
  *   scale      finite, > 0;  window >= 0, 0 unless causal.
  *   out        device bf16 [total_new, n_q_heads, head_dim], contiguous.
  *   lse        device float [total_new, n_q_heads], natural logarithm; may be NULL.

@@ -53,9 +53,10 @@
 // the second product; l sums the unrounded weights in fp32.
 //
 // Masks are ranges of places: scores outside [lo, hi) become -inf by
-// selection (their products may be anything), key tiles that no row of the
-// unit sees are never loaded, and value rows beyond kv_len in the last tile,
-// which may hold NaN, are zeroed in shared memory before the product.
+// selection (their products may be anything), key tiles and pages that no row
+// of the unit sees are never loaded, value rows beyond kv_len in the last tile,
+// which may hold NaN, are zeroed in shared memory before the product, and a row
+// to which another token's NaN or infinity got is formed again (redo_row).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -112,6 +113,7 @@ struct Segment {
   int32_t key0;    // first key of the segment
   int32_t kv;      // keys of the request
   int32_t hk;      // key head
+  int32_t req;     // request
   int32_t part;    // workspace part (-1: the unit is complete)
   int32_t first;   // the workers that share the unit
   int32_t last;
@@ -261,6 +263,12 @@ __host__ __device__ constexpr uint32_t idesc(int N, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? (1u << 16) : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(kRows >> 4) << 24);
 }
+// the maximum, or NaN if one of them is
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -302,16 +310,21 @@ __device__ __forceinline__ bool read_request(const AttendArgs &a, int32_t i, Req
   if (r.bad) r.kv = 0;
   return c0 >= 0 && c1 >= c0 && c1 <= a.T;
 }
+// the first key that a token at place pos sees
+__device__ __forceinline__ int32_t first_key(const AttendArgs &a, int32_t pos) {
+  return a.window > 0 ? max(0, pos + 1 - min(a.window, max(pos + 1, 1))) : 0;
+}
+// of request r's token t0, and so of those after it
+__device__ __forceinline__ int32_t unit_first(const AttendArgs &a, const Request &r, int32_t t0) {
+  return first_key(a, r.kv - r.n + t0);
+}
 // the key tiles [k0, k1) that the unit of tokens [t0, t0 + nt) sees: at least one (which may be empty)
 template <int kKeys>
 __device__ __forceinline__ void unit_keys(const AttendArgs &a, const Request &r, int32_t t0, int32_t nt, int32_t &k0,
                                           int32_t &k1) {
-  const int32_t first = r.kv - r.n + t0;  // place of the unit's first token
   int32_t hi = r.kv;
-  if (a.causal) hi = min(hi, first + nt);
-  int32_t lo = 0;
-  if (a.window > 0) lo = max(0, first + 1 - min(a.window, max(first + 1, 1)));
-  k0 = lo / kKeys;
+  if (a.causal) hi = min(hi, r.kv - r.n + t0 + nt);
+  k0 = unit_first(a, r, t0) / kKeys;
   k1 = max(k0 + 1, (hi + kKeys - 1) / kKeys);
 }
 // the length of request r's part of the line
@@ -373,6 +386,7 @@ __device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtens
         const int32_t j1 = static_cast<int32_t>(min(static_cast<int64_t>(k1 - k0), e - at - Sh::kUnitCost));
         if (j0 >= j1) continue;
         // the segment's pages, 32 ids at a time, the next 32 under way
+        const int32_t first_page = unit_first(a, r, t0) >> shift;
         const int32_t p_end = (min(r.kv, (k0 + j1) * Sh::kKeys) + a.page_size - 1) >> shift;
         int32_t p_base = ((k0 + j0) * Sh::kKeys) >> shift;
         int32_t ids = (p_base + lane < p_end) ? __ldg(table + p_base + lane) : 0;
@@ -392,6 +406,7 @@ __device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtens
           s.key0 = (k0 + j0) * Sh::kKeys;
           s.kv = r.kv;
           s.hk = hk;
+          s.req = i;
           s.part = whole ? -1 : 2 * worker + (j0 == 0 ? 1 : 0);
           // position x of the line is worker ((x + 1) workers - 1) / W's
           s.first = static_cast<int32_t>(((at + Sh::kUnitCost + 1) * workers - 1) / W);
@@ -429,10 +444,12 @@ __device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtens
             ids = next_ids;
             next_ids = (p_base + 32 + lane < p_end) ? __ldg(table + p_base + 32 + lane) : 0;
           }
-          int32_t page = __shfl_sync(0xffffffffu, ids, min(31, ((key + lane * box) >> shift) - p_base));
-          if (lane < need && (page < 0 || page >= a.n_pages)) {
-            bad = true;
-            page = a.n_pages;  // outside the tensor: reads as zeros
+          const int32_t id = (key + lane * box) >> shift;
+          int32_t page = __shfl_sync(0xffffffffu, ids, min(31, id - p_base));
+          if (lane < need) {
+            const bool hidden = id < first_page;  // behind the window of all tokens: may be anyone's
+            bad |= !hidden && (page < 0 || page >= a.n_pages);
+            if (hidden || page < 0 || page >= a.n_pages) page = a.n_pages;  // outside the tensor: reads as zeros
           }
           const int row = key & (a.page_size - 1);  // 0 unless a page holds several tiles
           for (int v = kFrom; v < kTo && ok; ++v) {
@@ -730,6 +747,61 @@ __device__ __forceinline__ void mark_and_join(const AttendArgs &a, const Segment
   for (int q = row; q < n; q += kRows) a.marks[part_of(g.first, q)] = 0;
 }
 
+// ---------------------------- what a mask hides -----------------------------
+// A hidden key's weight is zero, and zero times a NaN or an infinity is NaN.  A
+// row with a NaN output whose hidden keys in the segment hold such a value is
+// formed again, by a warp, from the keys that it sees (the sum of its weights
+// needs nothing: scores are hidden by selection).  The loop over the hidden keys
+// first: they are few, and a NaN that a row sees is its result.
+template <int D>
+__device__ __noinline__ void redo_row(const AttendArgs &a, const Segment &g, int32_t key1, int32_t lo, int32_t hi, float M,
+                                      float inv, int32_t orow, int64_t prow) {
+  constexpr int E = D / 32;  // elements of a lane
+  const int lane = threadIdx.x & 31;
+  const int32_t *table = a.table + g.req * a.table_stride;
+  auto row_at = [&](const void *cache, const int64_t (&st)[3], int32_t j) -> const __nv_bfloat16 * {
+    const int32_t page = __ldg(table + j / a.page_size);
+    if (page < 0 || page >= a.n_pages) return nullptr;  // behind every token's window
+    return static_cast<const __nv_bfloat16 *>(cache) + page * st[0] + g.hk * st[1] + (j % a.page_size) * st[2] + lane * E;
+  };
+  bool bad = false;
+  auto look_at = [&](int32_t from, int32_t to) {
+    for (int32_t j = from; j < to; ++j) {
+      const __nv_bfloat16 *v = row_at(a.v_cache, a.vc, j);
+#pragma unroll
+      for (int e = 0; e < E; ++e) bad |= v && !(fabsf(__bfloat162float(v[e])) < INFINITY);
+    }
+  };
+  look_at(g.key0, min(lo, key1));
+  look_at(max(hi, g.key0), key1);
+  if (!__any_sync(0xffffffffu, bad)) return;
+  const __nv_bfloat16 *qp =
+      static_cast<const __nv_bfloat16 *>(a.q) + orow / a.Hq * a.q_ts + orow % a.Hq * a.q_hs + lane * E;
+  const float k2 = a.scale * kLog2e;
+  float q[E], acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) q[e] = __bfloat162float(qp[e]), acc[e] = 0.f;
+  for (int32_t j = max(lo, g.key0); j < min(hi, key1); ++j) {
+    const __nv_bfloat16 *k = row_at(a.k_cache, a.kc, j), *v = row_at(a.v_cache, a.vc, j);
+    if (!k) continue;
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s = fmaf(q[e], __bfloat162float(k[e]), s);
+#pragma unroll
+    for (int u = 16; u > 0; u >>= 1) s += __shfl_xor_sync(0xffffffffu, s, u);
+    const float p = __bfloat162float(__float2bfloat16_rn(ex2(fmaf(s, k2, -M))));  // as the product takes it
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(p, __bfloat162float(v[e]), acc[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    if (g.part >= 0)
+      a.part_o[prow * D + lane * E + e] = acc[e];
+    else
+      static_cast<__nv_bfloat16 *>(a.out)[static_cast<int64_t>(orow) * D + lane * E + e] = __float2bfloat16_rn(acc[e] * inv);
+  }
+}
+
 // ------------------------------- the softmax --------------------------------
 // Of stage s: a thread has one row and all keys of a tile.
 template <int D, bool kWide, bool kInside, typename C>
@@ -753,9 +825,8 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
     if (g.tiles == 0) break;
     const int tile = kWide ? s : 0;
     const int32_t pos = g.pos0 + tile * a.tile_tokens + tok_of_row;
-    int32_t hi = g.kv, lo = 0;
+    int32_t hi = g.kv, lo = first_key(a, pos);
     if (a.causal) hi = min(hi, pos + 1);
-    if (a.window > 0) lo = max(0, pos + 1 - min(a.window, max(pos + 1, 1)));
     const bool live = tok_of_row < (tile ? g.ntok1 : g.ntok0);
     const bool warp_live = __any_sync(0xffffffffu, live);
     if (!live) hi = INT32_MAX, lo = 0;  // rows of no token: never masked, never looked at
@@ -866,11 +937,16 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
 #pragma unroll
       for (int q = 0; q < 4; ++q) to[q] = __shfl_sync(0xffffffffu, orow, (lane & ~3) + q);
       const int piece = lane & 3;
+      bool odd = false;  // some output is NaN
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32];
         tmem_ld32(t_o + c, o);
         tmem_wait_ld();
+        float nan = o[0];
+#pragma unroll
+        for (int v = 1; v < 31; v += 2) nan = max3_nan(nan, o[v], o[v + 1]);
+        odd |= nan != nan || o[31] != o[31];
         uint32_t p[4][4];
         if (g.part < 0) {
 #pragma unroll
@@ -892,6 +968,18 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
             for (int q = 0; q < 4; ++q)
               if (to[q] >= 0) *reinterpret_cast<uint4 *>(dst + q * D + h * 16) = make_uint4(p[q][0], p[q][1], p[q][2], p[q][3]);
           }
+        }
+      }
+      // a weight of zero times a NaN or an infinity of a hidden key?
+      const int32_t key1 = min(g.kv, g.key0 + g.tiles * Sh::kKeys);
+      uint32_t again = __ballot_sync(0xffffffffu, live && odd && l == l && (lo > g.key0 || hi < key1));
+      if (again) {
+        __syncwarp();  // the rows are written
+        for (; again; again &= again - 1) {
+          const int from = __ffs(again) - 1;
+          redo_row<D>(a, g, key1, __shfl_sync(0xffffffffu, lo, from), __shfl_sync(0xffffffffu, hi, from),
+                      __shfl_sync(0xffffffffu, M, from), __shfl_sync(0xffffffffu, inv, from),
+                      __shfl_sync(0xffffffffu, orow, from), prow - lane + from);
         }
       }
       if (live) {

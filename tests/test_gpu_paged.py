@@ -368,6 +368,86 @@ def test_attend_bad_requests():
             assert torch.equal(out[s], good[0][s]) and torch.equal(lse[s], good[1][s])
 
 
+HIDDEN = [
+    # new, kv_len, hq, hkv, d, page, window: decoding, blocks, prompts, one long request
+    ([1, 1, 1], [700, 130, 64], 8, 2, 128, 16, 70),
+    ([17, 5], [900, 200], 4, 4, 64, 16, 33),
+    ([17, 5], [900, 200], 8, 1, 128, 64, 100),
+    ([150, 40], [700, 300], 4, 2, 64, 32, 90),
+    ([150, 40], [700, 300], 4, 2, 128, 16, 200),
+    ([9], [20000], 4, 1, 128, 16, 7000),
+]
+
+
+@pytest.mark.parametrize("new,kv,hq,hkv,d,page,window", HIDDEN)
+def test_attend_keys_behind_the_window_may_be_anything(new, kv, hq, hkv, d, page, window):
+    """What no token sees changes nothing: NaN, infinities, and the block
+    table's entries of pages that lie behind every token's window."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    rng = np.random.default_rng(sum(kv) + d)
+    kc, vc, table = _cache(rng, new, kv, hkv, d, page, torch.bfloat16)
+    q = torch.from_numpy(rng.normal(size=(int(np.sum(new)), hq, d))).to(torch.bfloat16).cuda()
+    kw = {"window": window}
+    clean = _check_attend(svw, new, kv, q, kc, vc, table, kw)
+    k2, v2, t2 = kc.clone(), vc.clone(), table.copy()
+    hidden = 0
+    for i, n in enumerate(new):
+        unseen = max(0, kv[i] - n + 1 - window)  # before the first token's window
+        for j in range(unseen):
+            s, r = int(table[i, j // page]), j % page
+            k2[s, :, r] = float("nan")
+            v2[s, :, r] = float("nan") if j % 2 else float("inf")
+        t2[i, :unseen // page] = np.resize([-1, kc.shape[0] + 7, 1 << 30], unseen // page)
+        hidden += unseen
+    assert hidden > 0
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = svw.paged_attention(q, k2, v2, _i32(t2), _i32(_cu(new)), _i32(kv), status=status, **kw)
+    assert int(status) == 0
+    assert torch.equal(lse, clean[1])
+    _compare_attend(new, kv, q, kc, vc, table, kw, out, lse)
+
+
+@pytest.mark.parametrize("new,kv,hq,hkv,d,page,window", HIDDEN)
+@pytest.mark.parametrize("what", ["values", "keys"])
+def test_attend_a_token_does_not_reach_those_before_it(new, kv, hq, hkv, d, page, window, what):
+    """A later token's NaN or infinity reaches the tokens that see it, and no
+    others."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    rng = np.random.default_rng(sum(kv) + d + 1)
+    kc, vc, table = _cache(rng, new, kv, hkv, d, page, torch.bfloat16)
+    q = torch.from_numpy(rng.normal(size=(int(np.sum(new)), hq, d))).to(torch.bfloat16).cuda()
+    k2, v2 = kc.clone(), vc.clone()
+    cu = _cu(new)
+    late = []
+    for i, n in enumerate(new):
+        j = kv[i] - (n + 1) // 2  # seen by the last half of the new tokens
+        late.append(cu[i] + n - (n + 1) // 2)
+        s, r = int(table[i, j // page]), j % page
+        if what == "keys":
+            k2[s, :, r, 1] = float("nan")
+        else:
+            v2[s, :, r, 3] = float("nan")
+            v2[s, :, r, 5] = float("inf")
+    out, lse = svw.paged_attention(q, k2, v2, _i32(table), _i32(cu), _i32(kv), window=window)
+    clean = svw.paged_attention(q, kc, vc, _i32(table), _i32(cu), _i32(kv), window=window)
+    got = out.clone()
+    for i, n in enumerate(new):
+        mine = got[late[i]:cu[i + 1]]
+        seen = torch.arange(mine.shape[0]) < window  # the token itself leaves the window again
+        assert bool(seen.all())
+        if what == "keys":
+            assert bool(mine.isnan().all()) and bool(lse[late[i]:cu[i + 1]].isnan().all())
+            mine[:] = clean[0][late[i]:cu[i + 1]]
+            lse[late[i]:cu[i + 1]] = clean[1][late[i]:cu[i + 1]]
+        else:
+            assert bool(mine[..., 3].isnan().all()) and bool(torch.isposinf(mine[..., 5]).all())
+            for e in (3, 5):
+                mine[..., e] = clean[0][late[i]:cu[i + 1], :, e]
+    _compare_attend(new, kv, q, kc, vc, table, {"window": window}, got, lse)
+
+
 def test_attend_streams_and_graph():
     import serving_vocab_wide_gb300 as svw
     import torch
