@@ -45,7 +45,7 @@
 // Measured (us; 32 query heads, 8 key heads of 128; of 6.78 TB/s and 1898
 // TFLOP/s): 64 decoding requests over 1000 to 16000 keys 209 (98%); 2220 new
 // tokens of 256 requests over 512 to 8192 keys 447 (95%); 17 tokens over 131000
-// keys 95 (84%); two prompts of 2048 over 8192 keys 370 (1668 TFLOP/s, 88%).
+// keys 95 (83%); two prompts of 2048 over 8192 keys 374 (1654 TFLOP/s, 87%).
 // The reference: exp2(x - M) is exact algebra for any M, so M follows the
 // row's maximum only when that has outgrown it by more than 8 (a factor 256:
 // far from overflow, and the same relative rounding of P); only then are l
@@ -263,12 +263,6 @@ __host__ __device__ constexpr uint32_t idesc(int N, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? (1u << 16) : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(kRows >> 4) << 24);
 }
-// the maximum, or NaN if one of them is
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -446,10 +440,9 @@ __device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtens
           }
           const int32_t id = (key + lane * box) >> shift;
           int32_t page = __shfl_sync(0xffffffffu, ids, min(31, id - p_base));
-          if (lane < need) {
-            const bool hidden = id < first_page;  // behind the window of all tokens: may be anyone's
-            bad |= !hidden && (page < 0 || page >= a.n_pages);
-            if (hidden || page < 0 || page >= a.n_pages) page = a.n_pages;  // outside the tensor: reads as zeros
+          if (lane < need && (page < 0 || page >= a.n_pages)) {
+            bad |= id >= first_page;  // those before lie behind every token's window
+            page = a.n_pages;         // outside the tensor: reads as zeros
           }
           const int row = key & (a.page_size - 1);  // 0 unless a page holds several tiles
           for (int v = kFrom; v < kTo && ok; ++v) {
@@ -749,20 +742,21 @@ __device__ __forceinline__ void mark_and_join(const AttendArgs &a, const Segment
 
 // ---------------------------- what a mask hides -----------------------------
 // A hidden key's weight is zero, and zero times a NaN or an infinity is NaN.  A
-// row with a NaN output whose hidden keys in the segment hold such a value is
+// row with a NaN among its outputs whose hidden keys in the segment hold such a value is
 // formed again, by a warp, from the keys that it sees (the sum of its weights
 // needs nothing: scores are hidden by selection).  The loop over the hidden keys
-// first: they are few, and a NaN that a row sees is its result.
+// first: they are few, and a NaN that a row sees is its result.  (The look at
+// the outputs' sum costs 1% of two prompts' time, 4% where units have 2 tiles.)
 template <int D>
-__device__ __noinline__ void redo_row(const AttendArgs &a, const Segment &g, int32_t key1, int32_t lo, int32_t hi, float M,
-                                      float inv, int32_t orow, int64_t prow) {
+__device__ __noinline__ void redo_row(const AttendArgs &a, int32_t req, int32_t hk, int32_t key0, int32_t key1, int32_t lo,
+                                      int32_t hi, float M, float inv, int32_t orow, int64_t prow) {  // prow -1: the result
   constexpr int E = D / 32;  // elements of a lane
   const int lane = threadIdx.x & 31;
-  const int32_t *table = a.table + g.req * a.table_stride;
+  const int32_t *table = a.table + req * a.table_stride;
   auto row_at = [&](const void *cache, const int64_t (&st)[3], int32_t j) -> const __nv_bfloat16 * {
     const int32_t page = __ldg(table + j / a.page_size);
     if (page < 0 || page >= a.n_pages) return nullptr;  // behind every token's window
-    return static_cast<const __nv_bfloat16 *>(cache) + page * st[0] + g.hk * st[1] + (j % a.page_size) * st[2] + lane * E;
+    return static_cast<const __nv_bfloat16 *>(cache) + page * st[0] + hk * st[1] + (j % a.page_size) * st[2] + lane * E;
   };
   bool bad = false;
   auto look_at = [&](int32_t from, int32_t to) {
@@ -772,8 +766,8 @@ __device__ __noinline__ void redo_row(const AttendArgs &a, const Segment &g, int
       for (int e = 0; e < E; ++e) bad |= v && !(fabsf(__bfloat162float(v[e])) < INFINITY);
     }
   };
-  look_at(g.key0, min(lo, key1));
-  look_at(max(hi, g.key0), key1);
+  look_at(key0, min(lo, key1));
+  look_at(max(hi, key0), key1);
   if (!__any_sync(0xffffffffu, bad)) return;
   const __nv_bfloat16 *qp =
       static_cast<const __nv_bfloat16 *>(a.q) + orow / a.Hq * a.q_ts + orow % a.Hq * a.q_hs + lane * E;
@@ -781,7 +775,7 @@ __device__ __noinline__ void redo_row(const AttendArgs &a, const Segment &g, int
   float q[E], acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) q[e] = __bfloat162float(qp[e]), acc[e] = 0.f;
-  for (int32_t j = max(lo, g.key0); j < min(hi, key1); ++j) {
+  for (int32_t j = max(lo, key0); j < min(hi, key1); ++j) {
     const __nv_bfloat16 *k = row_at(a.k_cache, a.kc, j), *v = row_at(a.v_cache, a.vc, j);
     if (!k) continue;
     float s = 0.f;
@@ -795,7 +789,7 @@ __device__ __noinline__ void redo_row(const AttendArgs &a, const Segment &g, int
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    if (g.part >= 0)
+    if (prow >= 0)
       a.part_o[prow * D + lane * E + e] = acc[e];
     else
       static_cast<__nv_bfloat16 *>(a.out)[static_cast<int64_t>(orow) * D + lane * E + e] = __float2bfloat16_rn(acc[e] * inv);
@@ -937,16 +931,19 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
 #pragma unroll
       for (int q = 0; q < 4; ++q) to[q] = __shfl_sync(0xffffffffu, orow, (lane & ~3) + q);
       const int piece = lane & 3;
-      bool odd = false;  // some output is NaN
+      // does the segment have keys hidden from one of the rows?  Then their outputs' sum is looked at for a NaN
+      const int32_t key1 = min(g.kv, g.key0 + g.tiles * Sh::kKeys);
+      const bool hides = __any_sync(0xffffffffu, live && (lo > g.key0 || hi < key1));
+      float2 odd = make_float2(0.f, 0.f);
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32];
         tmem_ld32(t_o + c, o);
         tmem_wait_ld();
-        float nan = o[0];
+        if (hides) {
 #pragma unroll
-        for (int v = 1; v < 31; v += 2) nan = max3_nan(nan, o[v], o[v + 1]);
-        odd |= nan != nan || o[31] != o[31];
+          for (int v = 0; v < 32; v += 2) odd = __fadd2_rn(odd, make_float2(o[v], o[v + 1]));
+        }
         uint32_t p[4][4];
         if (g.part < 0) {
 #pragma unroll
@@ -971,15 +968,15 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
         }
       }
       // a weight of zero times a NaN or an infinity of a hidden key?
-      const int32_t key1 = min(g.kv, g.key0 + g.tiles * Sh::kKeys);
-      uint32_t again = __ballot_sync(0xffffffffu, live && odd && l == l && (lo > g.key0 || hi < key1));
+      const float sum = odd.x + odd.y;
+      uint32_t again = __ballot_sync(0xffffffffu, live && sum != sum && l == l && (lo > g.key0 || hi < key1));
       if (again) {
         __syncwarp();  // the rows are written
         for (; again; again &= again - 1) {
           const int from = __ffs(again) - 1;
-          redo_row<D>(a, g, key1, __shfl_sync(0xffffffffu, lo, from), __shfl_sync(0xffffffffu, hi, from),
+          redo_row<D>(a, g.req, g.hk, g.key0, key1, __shfl_sync(0xffffffffu, lo, from), __shfl_sync(0xffffffffu, hi, from),
                       __shfl_sync(0xffffffffu, M, from), __shfl_sync(0xffffffffu, inv, from),
-                      __shfl_sync(0xffffffffu, orow, from), prow - lane + from);
+                      __shfl_sync(0xffffffffu, orow, from), g.part >= 0 ? prow - lane + from : -1);
         }
       }
       if (live) {
