@@ -20,7 +20,7 @@
 // Large batches (given a workspace), 228 us on the benchmark batch (6.0 TB/s):
 //   adjust_lists   a CTA per request lists its distinct tokens, ascending, with
 //                  their counts (20 us, mostly beside the rows' first loads);
-//   adjust_staged  a CTA per chunk of 4096 entries of a request: rows pass
+//   adjust_staged  a CTA per chunk of 8 KB of a request's rows: they pass
 //                  through shared memory by bulk copies, masked and adjusted on
 //                  the way; seven CTAs of three 8 KB stages per SM (four stages
 //                  and five CTAs: 240 us; the rows in registers and the listed
@@ -50,6 +50,13 @@ constexpr int kAdjThreads = 256;
 constexpr int kAdjBatch = 4;  // vectors of a thread under way
 constexpr int kAhead = 8;     // history tokens of a thread under way
 constexpr int kChunk = 4096;  // entries of a chunk, unless the batch is small
+// of the lists, and of rows that are staged: 8 KB (with 16 KB of fp32 there
+// are four CTAs of three stages per SM instead of seven: 544 masked rows of
+// 32003 took 33.1 us instead of 30.4; in place, through registers, the larger
+// chunks are the faster ones, 34 against 42)
+__host__ __device__ constexpr int list_shift(int es) { return es == 2 ? 12 : 11; }
+__host__ __device__ constexpr int list_chunk(int es) { return 1 << list_shift(es); }
+static_assert(list_chunk(2) == kChunk && list_chunk(4) * 2 == kChunk, "a chunk is one or two of the lists'");
 constexpr uint32_t kNothing = 0x100;  // no vector to write
 constexpr int32_t kPromptBit = static_cast<int32_t>(0x80000000u);
 constexpr int32_t kDraftBit = 0x40000000;  // lists: the token is drafted too
@@ -491,6 +498,11 @@ __global__ void __launch_bounds__(kListThreads, 2) adjust_lists(const __grid_con
   int32_t held[kAhead];
 #pragma unroll
   for (int q = 0; q < kAhead; ++q) held[q] = (tid + q * kListThreads < hn) ? __ldg(hist + tid + q * kListThreads) : -1;
+  // and so do the first bias and the draft of a thread: one trip to memory for all lists
+  const bool has_bias = s.b0 + tid < s.b1;
+  const int32_t bias_held = has_bias ? __ldg(a.bias_tokens + s.b0 + tid) : 0;
+  if (has_bias) bad |= !(__ldg(a.bias_values + s.b0 + tid) < INFINITY);
+  const int32_t draft = tid < L ? __ldg(a.tokens + s.d0 + tid) : 0;
   auto each = [&](auto &&f) {
 #pragma unroll
     for (int q = 0; q < kAhead; ++q)
@@ -520,11 +532,12 @@ __global__ void __launch_bounds__(kListThreads, 2) adjust_lists(const __grid_con
       if (u < static_cast<uint32_t>(n_tok)) atomicOr(bits + (u >> 5), 1u << (u & 31));
     };
     each([&](int32_t v, int32_t) { mark(v); });
-    for (int32_t p = s.b0 + tid; p < s.b1; p += kListThreads) {
+    if (has_bias) mark(bias_held);
+    for (int32_t p = s.b0 + tid + kListThreads; p < s.b1; p += kListThreads) {
       mark(__ldg(a.bias_tokens + p));
       bad |= !(__ldg(a.bias_values + p) < INFINITY);
     }
-    if (tid < L) mark(__ldg(a.tokens + s.d0 + tid));
+    if (tid < L) mark(draft);
     __syncthreads();
     // running counts of the words: a thread's stretch, a warp's, the block's
     const int per = (words + kListThreads - 1) / kListThreads, w0 = min(words, tid * per), w1 = min(words, w0 + per);
@@ -546,7 +559,7 @@ __global__ void __launch_bounds__(kListThreads, 2) adjust_lists(const __grid_con
     for (int w = w0; w < w1; ++w) {
       below[w] = before;
       const int32_t tok = lo + w * 32;
-      if (tok % kChunk == 0 && tok < a.V) offs[tok / kChunk] = base + before;
+      if ((tok & ((1 << a.list_shift) - 1)) == 0 && tok < a.V) offs[tok >> a.list_shift] = base + before;
       before += __popc(bits[w]);
     }
     __syncthreads();
@@ -573,12 +586,16 @@ __global__ void __launch_bounds__(kListThreads, 2) adjust_lists(const __grid_con
         else
           atomicAdd(cnt + e, 1);
       });
-      for (int32_t p = s.b0 + tid; p < s.b1; p += kListThreads) {
+      if (has_bias) {
+        const int e = place(bias_held);
+        if (e >= 0) atomicMax(bid + e, s.b0 + tid + 1);
+      }
+      for (int32_t p = s.b0 + tid + kListThreads; p < s.b1; p += kListThreads) {
         const int e = place(__ldg(a.bias_tokens + p));
         if (e >= 0) atomicMax(bid + e, p + 1);
       }
       if (tid < L) {
-        const int e = place(__ldg(a.tokens + s.d0 + tid));
+        const int e = place(draft);
         if (e >= 0) atomicOr(cnt + e, kDraftBit);
       }
       __syncthreads();
@@ -615,8 +632,9 @@ __device__ __forceinline__ Listed listed_of(const AdjustArgs &a, const Slices &s
     first = static_cast<int32_t>(all * c / a.chunks);
     last = static_cast<int32_t>(all * (c + 1) / a.chunks);
   } else {
-    first = __ldcg(offs + c);
-    last = __ldcg(offs + c + 1);
+    const int32_t of = a.chunk_len >> a.list_shift;  // the lists' chunks in one of the CTAs'
+    first = __ldcg(offs + c * of);
+    last = __ldcg(offs + min((c + 1) * of, a.list_chunks));
   }
   Listed l;
   l.n = last - first;
@@ -640,7 +658,7 @@ __device__ __forceinline__ int32_t drafted_before(const int32_t *drafts, int32_t
 // kListed entries and their biases at the start.
 constexpr int kStages = 3;
 constexpr int kListed = 256;
-__host__ __device__ constexpr int stage_bytes(int es) { return kChunk * es + 16; }
+__host__ __device__ constexpr int stage_bytes(int es) { return list_chunk(es) * es + 16; }
 __device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
                : "memory");
@@ -650,13 +668,13 @@ template <int DT>
 __global__ void __launch_bounds__(kAdjThreads, 7) adjust_staged(const __grid_constant__ AdjustArgs a) {
   using B = Bits<DT>;
   using T = typename B::T;
-  constexpr int EPV = 16 / sizeof(T), kStage = stage_bytes(sizeof(T));
+  constexpr int EPV = 16 / sizeof(T), kStage = stage_bytes(sizeof(T)), kWords = list_chunk(sizeof(T)) / 32;
   constexpr uint32_t kAll = (1u << EPV) - 1u;
   extern __shared__ __align__(16) unsigned char stages[];
   __shared__ int32_t drafts[SVW_MAX_LEN], mask_of[SVW_MAX_LEN + 1];
   __shared__ int4 held[kListed];
   __shared__ unsigned long long full[kStages];
-  __shared__ uint32_t mask_word[2][kChunk / 32 + 1];  // of this row and the next; one more for the last vector's reach
+  __shared__ uint32_t mask_word[2][kWords + 1];  // of this row and the next; one more for the last vector's reach
   const int tid = threadIdx.x;
   const unsigned item = blockIdx.x / static_cast<unsigned>(a.groups);
   const int group = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.groups));
@@ -687,14 +705,14 @@ __global__ void __launch_bounds__(kAdjThreads, 7) adjust_staged(const __grid_con
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     for (int q = 0; q < min(kStages, r.rows); ++q) fetch(q);
   }
-  if (tid < 2) mask_word[tid][kChunk / 32] = 0;
+  if (tid < 2) mask_word[tid][kWords] = 0;
   __syncthreads();
   // word tid of the chunk in row q's mask
   const int words = (r.len + 31) / 32;
   auto mask_at = [&](int q) {
     return (q < r.rows && mask_of[q] >= 0 && tid < words) ? __ldg(r.words(mask_of[q]) + (r.v0 >> 5) + tid) : 0u;
   };
-  if (tid < kChunk / 32) mask_word[0][tid] = mask_at(0);
+  if (tid < kWords) mask_word[0][tid] = mask_at(0);
   const Listed ls = listed_of(a, s, i, c);
   // an entry with its bias's value in the place of its place (a bias of 0 is none)
   auto entry = [&](int k) {
@@ -756,7 +774,7 @@ __global__ void __launch_bounds__(kAdjThreads, 7) adjust_staged(const __grid_con
           row[u] = static_cast<T>(B::bits(y));
       }
     }
-    if (tid < kChunk / 32) mask_word[(q + 1) & 1][tid] = next_word;
+    if (tid < kWords) mask_word[(q + 1) & 1][tid] = next_word;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
     if (mine >= 0) r.out[q * r.out_step + mine] = row[mine];
@@ -868,7 +886,7 @@ cudaError_t allow_shared() {
 size_t adjust_workspace(int64_t N, int64_t V, int64_t R, int64_t total_history, int64_t total_bias) {
   const int64_t listed = R + total_history + total_bias;
   if (!by_lists(N, V, R + N, listed)) return 0;
-  return round256(static_cast<size_t>(N) * ((V + kChunk - 1) / kChunk + 2) * 4) + round256(static_cast<size_t>(listed) * sizeof(int4));
+  return round256(static_cast<size_t>(N) * ((V + list_chunk(4) - 1) / list_chunk(4) + 2) * 4) + round256(static_cast<size_t>(listed) * sizeof(int4));
 }
 
 cudaError_t launch_adjust(const AdjustArgs &args, int dtype, cudaStream_t st) {
@@ -877,8 +895,10 @@ cudaError_t launch_adjust(const AdjustArgs &args, int dtype, cudaStream_t st) {
   const uintptr_t apart = reinterpret_cast<uintptr_t>(a.logits) - reinterpret_cast<uintptr_t>(a.out);
   const bool vec = (apart & 15u) == 0 && ((a.in_stride - a.out_stride) * es) % 16 == 0;
   const bool lists = a.ws && by_lists(a.N, a.V, a.R + a.N, a.R + a.total_history + a.total_bias);
-  a.chunk_len = kChunk;
-  a.list_chunks = static_cast<int32_t>((a.V + kChunk - 1) / kChunk);
+  const bool staged = lists && vec && a.out != a.logits;
+  a.chunk_len = staged ? list_chunk(es) : kChunk;
+  a.list_shift = list_shift(es);
+  a.list_chunks = static_cast<int32_t>((a.V + list_chunk(es) - 1) / list_chunk(es));
   // in place without a mask there is nothing to stream: the CTAs share out the lists evenly
   a.even = lists && a.out == a.logits && !a.mask;
   // smaller chunks where the batch would leave SMs without work
@@ -915,7 +935,7 @@ cudaError_t launch_adjust(const AdjustArgs &args, int dtype, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (vec && a.out != a.logits) {
+    if (staged) {
       cfg.dynamicSmemBytes = static_cast<size_t>(kStages) * stage_bytes(es);
       kernel = dtype == SVW_BF16 ? reinterpret_cast<void *>(adjust_staged<1>) : reinterpret_cast<void *>(adjust_staged<0>);
     } else {

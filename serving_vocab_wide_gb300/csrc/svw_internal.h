@@ -234,7 +234,7 @@ struct AdjustArgs {
   void *ws;  // NULL: the chunks' CTAs count for themselves
   // set by the launcher
   int32_t chunk_len, chunks, groups;  // entries of a CTA's chunk; CTAs of a request's vocabulary, of its rows
-  int32_t list_chunks, even;          // chunks of the lists; 1: CTAs of a request's vocabulary share its list evenly
+  int32_t list_chunks, list_shift, even;  // chunks of the lists, of 2^shift entries; 1: CTAs of a request's vocabulary share its list evenly
   int32_t *list_offs;  // [N][list_chunks + 2] a request's chunks in its list, its end, whether it is bad
   int4 *list;          // token, count word, bias place
 };
