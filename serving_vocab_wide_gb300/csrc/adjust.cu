@@ -17,21 +17,22 @@
 // listed entry that is drafted looks through the request's drafts (at most
 // SVW_MAX_LEN).
 //
-// Large batches (given a workspace), 228 us on the benchmark batch (6.0 TB/s):
+// Large batches (given a workspace), 225 us on the benchmark batch (6.0 TB/s):
 //   adjust_lists   a CTA per request lists its distinct tokens, ascending, with
-//                  their counts (20 us, mostly beside the rows' first loads);
+//                  their counts (16 us for 8192, partly beside the rows' first
+//                  loads);
 //   adjust_staged  a CTA per chunk of 8 KB of a request's rows: they pass
 //                  through shared memory by bulk copies, masked and adjusted on
 //                  the way; seven CTAs of three 8 KB stages per SM (four stages
 //                  and five CTAs: 240 us; the rows in registers and the listed
 //                  entries by a second trip to memory: 329);
-//   adjust_rows    in place, 97 us without masks and 265 with (only what
+//   adjust_rows    in place, 93 us without masks and 264 with (only what
 //                  changes is written), or rows that do not lie alike.
 // Small batches, one launch: adjust_chunks, a CTA counts the tokens of its chunk
 // itself by reading the whole history (4.1 us for one row of 32000; on the
 // benchmark batch: 329, each of 38 chunks of a request waits for its loads.
 // Counting beside staged rows' loads was slower than the lists for all but few
-// requests: 43 us against 39 for 544 fp32 rows of 32003).
+// requests: 43 us where the lists took 39 on 544 fp32 rows of 32003, now 34.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -458,25 +459,27 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_chunks(const __grid_con
 // ---------------------------------------------------------------------------
 constexpr int kListThreads = 512;
 constexpr int kListWords = 1 << 13;  // of a bitmap: 2^18 tokens of the vocabulary at a time
-constexpr int kListCounts = 6144;    // distinct tokens counted at a time
+constexpr int kListCounts = 4096;    // distinct tokens counted at a time (6144: the rows in place, with that much less
+                                     // L1 beside them, 110 us instead of 93)
 __host__ __device__ constexpr int list_words(int V) {  // a multiple of four
   return V >= kListWords * 32 ? kListWords : ((V + 127) / 128) * 4;
 }
 __host__ __device__ constexpr int list_bytes(int V, bool bias) {
-  return list_words(V) * 8 + kListCounts * 4 * (bias ? 2 : 1);
+  return list_words(V) * 8 + kListCounts * 4 * (bias ? 3 : 2);
 }
 
 // Request i's distinct tokens, ascending, with their counts and last bias
 // places: a bitmap of them in shared memory; a token's rank (the words' running
 // counts and the bits below its own) is its place in the list and, less the
-// window's start, in the array of counts.  (A hash table of the same tokens
-// took 52 us for 8182 of them, 4.5 thousand distinct, in its probes.)
+// window's start, in the arrays of tokens and counts.  (A hash table of the same
+// tokens took 52 us for 8182 of them, 4.5 thousand distinct, in its probes;
+// writing the list from the bitmap's words, 5 us of 16.)
 __global__ void __launch_bounds__(kListThreads, 2) adjust_lists(const __grid_constant__ AdjustArgs a) {
   extern __shared__ int32_t dyn[];
   const int words = list_words(a.V);
   uint32_t *bits = reinterpret_cast<uint32_t *>(dyn);
   int32_t *below = dyn + words;                                   // tokens in the words before
-  int32_t *cnt = below + words, *bid = cnt + kListCounts;
+  int32_t *tok = below + words, *cnt = tok + kListCounts, *bid = cnt + kListCounts;  // by rank
   __shared__ int32_t warp_sum[kListThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31;
   const int32_t i = blockIdx.x;
@@ -581,6 +584,7 @@ __global__ void __launch_bounds__(kListThreads, 2) adjust_lists(const __grid_con
       each([&](int32_t v, int32_t p) {
         const int e = place(v);
         if (e < 0) return;
+        tok[e] = v;
         if (p < s.pl)
           atomicOr(cnt + e, kPromptBit);
         else
@@ -588,22 +592,20 @@ __global__ void __launch_bounds__(kListThreads, 2) adjust_lists(const __grid_con
       });
       if (has_bias) {
         const int e = place(bias_held);
-        if (e >= 0) atomicMax(bid + e, s.b0 + tid + 1);
+        if (e >= 0) tok[e] = bias_held, atomicMax(bid + e, s.b0 + tid + 1);
       }
       for (int32_t p = s.b0 + tid + kListThreads; p < s.b1; p += kListThreads) {
-        const int e = place(__ldg(a.bias_tokens + p));
-        if (e >= 0) atomicMax(bid + e, p + 1);
+        const int32_t v = __ldg(a.bias_tokens + p);
+        const int e = place(v);
+        if (e >= 0) tok[e] = v, atomicMax(bid + e, p + 1);
       }
       if (tid < L) {
         const int e = place(draft);
-        if (e >= 0) atomicOr(cnt + e, kDraftBit);
+        if (e >= 0) tok[e] = draft, atomicOr(cnt + e, kDraftBit);
       }
       __syncthreads();
-      for (int w = tid; w < words; w += kListThreads) {
-        int32_t r = below[w] - r0;
-        for (uint32_t m = bits[w]; m != 0; m &= m - 1, ++r)
-          if (apart && r >= 0 && r < n) list[base + r0 + r] = make_int4(lo + w * 32 + __ffs(m) - 1, cnt[r], a.cu_bias ? bid[r] : 0, 0);
-      }
+      for (int r = tid; apart && r < n; r += kListThreads)
+        list[base + r0 + r] = make_int4(tok[r], cnt[r], a.cu_bias ? bid[r] : 0, 0);
       __syncthreads();
     }
     base += total;
