@@ -56,7 +56,7 @@
 // selection (their products may be anything), key tiles and pages that no row
 // of the unit sees are never loaded, value rows beyond kv_len in the last tile,
 // which may hold NaN, are zeroed in shared memory before the product, and a row
-// to which another token's NaN or infinity got is formed again (redo_row).
+// to which another token's NaN or infinity got is formed again (redo_rows).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -743,58 +743,96 @@ __device__ __forceinline__ void mark_and_join(const AttendArgs &a, const Segment
 }
 
 // ---------------------------- what a mask hides -----------------------------
-// A hidden key's weight is zero, and zero times a NaN or an infinity is NaN.  A
-// row with a NaN among its outputs whose hidden keys in the segment hold such a value is
-// formed again, by a warp, from the keys that it sees (the sum of its weights
-// needs nothing: scores are hidden by selection).  The loop over the hidden keys
-// first: they are few, and a NaN that a row sees is its result.  (The look at
-// the outputs' sum costs 1% of two prompts' time, 4% where units have 2 tiles.)
+// A hidden key's weight is zero, and zero times a NaN or an infinity is NaN.  So
+// a row with a NaN among its outputs, where a key hidden from one of the warp's
+// rows holds such a value, is formed again, by the warp, from the keys that it
+// sees (the sum of its weights needs nothing: scores are hidden by selection).
+// Keys that a mask hides within a segment are few; a NaN that a row sees is its
+// result.  (The look at the outputs' sum costs 1% of two prompts' time, 4% where
+// units have 2 tiles.)
+__device__ __forceinline__ const __nv_bfloat16 *cache_row(const AttendArgs &a, const void *cache, const int64_t (&st)[3],
+                                                          const int32_t *table, int32_t hk, int32_t j) {
+  const int32_t page = __ldg(table + j / a.page_size);
+  if (page < 0 || page >= a.n_pages) return nullptr;  // behind every token's window
+  return static_cast<const __nv_bfloat16 *>(cache) + page * st[0] + hk * st[1] + (j % a.page_size) * st[2];
+}
+// does a value of keys [from, to) hold a NaN or an infinity?  A lane per key.
 template <int D>
-__device__ __noinline__ void redo_row(const AttendArgs &a, int32_t req, int32_t hk, int32_t key0, int32_t key1, int32_t lo,
-                                      int32_t hi, float M, float inv, int32_t orow, int64_t prow) {  // prow -1: the result
-  constexpr int E = D / 32;  // elements of a lane
+__device__ __forceinline__ bool odd_values(const AttendArgs &a, const int32_t *table, int32_t hk, int32_t from, int32_t to) {
+  bool odd = false;
+  for (int32_t j = from + (threadIdx.x & 31); j < to; j += 32) {
+    const __nv_bfloat16 *v = cache_row(a, a.v_cache, a.vc, table, hk, j);
+    if (!v) continue;
+#pragma unroll 4
+    for (int e = 0; e < D; e += 8) {
+      const uint4 w = *reinterpret_cast<const uint4 *>(v + e);
+      for (uint32_t x : {w.x, w.y, w.z, w.w}) odd |= (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+    }
+  }
+  return __any_sync(0xffffffffu, odd);
+}
+// Of a warp: rows `again` (by lane) of the segment's keys [key0, key1).  from_prow: lane 0's row of the part, -1: the
+// outputs are the result.
+template <int D>
+__device__ __noinline__ void redo_rows(const AttendArgs &a, uint32_t again, int32_t req, int32_t hk, int32_t key0,
+                                       int32_t key1, int32_t lo, int32_t hi, float M, float inv, int32_t orow,
+                                       int64_t from_prow) {
+  constexpr int E = D / 32, kMany = 8;  // elements of a lane; keys under way
   const int lane = threadIdx.x & 31;
   const int32_t *table = a.table + req * a.table_stride;
-  auto row_at = [&](const void *cache, const int64_t (&st)[3], int32_t j) -> const __nv_bfloat16 * {
-    const int32_t page = __ldg(table + j / a.page_size);
-    if (page < 0 || page >= a.n_pages) return nullptr;  // behind every token's window
-    return static_cast<const __nv_bfloat16 *>(cache) + page * st[0] + hk * st[1] + (j % a.page_size) * st[2] + lane * E;
-  };
-  bool bad = false;
-  auto look_at = [&](int32_t from, int32_t to) {
-    for (int32_t j = from; j < to; ++j) {
-      const __nv_bfloat16 *v = row_at(a.v_cache, a.vc, j);
+  const bool mine = (again >> lane) & 1u;
+  const int32_t lo_most = __reduce_max_sync(0xffffffffu, mine ? lo : 0);
+  const int32_t hi_least = __reduce_min_sync(0xffffffffu, mine ? hi : INT32_MAX);
+  if (!odd_values<D>(a, table, hk, key0, min(lo_most, key1)) && !odd_values<D>(a, table, hk, max(hi_least, key0), key1))
+    return;
+  const float k2 = a.scale * kLog2e;
+  auto load = [&](const __nv_bfloat16 *p, float *x) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) bad |= v && !(fabsf(__bfloat162float(v[e])) < INFINITY);
+    for (int e = 0; e < E; e += 2) {
+      const float2 f = bf16x2_f2(p ? *reinterpret_cast<const uint32_t *>(p + lane * E + e) : 0u);
+      x[e] = f.x, x[e + 1] = f.y;
     }
   };
-  look_at(key0, min(lo, key1));
-  look_at(max(hi, key0), key1);
-  if (!__any_sync(0xffffffffu, bad)) return;
-  const __nv_bfloat16 *qp =
-      static_cast<const __nv_bfloat16 *>(a.q) + orow / a.Hq * a.q_ts + orow % a.Hq * a.q_hs + lane * E;
-  const float k2 = a.scale * kLog2e;
-  float q[E], acc[E];
+  for (; again; again &= again - 1) {
+    const int from = __ffs(again) - 1;
+    const int32_t row = __shfl_sync(0xffffffffu, orow, from);
+    const float ref = __shfl_sync(0xffffffffu, M, from), by = __shfl_sync(0xffffffffu, inv, from);
+    const int32_t begin = max(__shfl_sync(0xffffffffu, lo, from), key0);
+    const int32_t end = min(__shfl_sync(0xffffffffu, hi, from), key1);
+    float q[E], acc[E];
+    load(static_cast<const __nv_bfloat16 *>(a.q) + row / a.Hq * a.q_ts + row % a.Hq * a.q_hs, q);
 #pragma unroll
-  for (int e = 0; e < E; ++e) q[e] = __bfloat162float(qp[e]), acc[e] = 0.f;
-  for (int32_t j = max(lo, key0); j < min(hi, key1); ++j) {
-    const __nv_bfloat16 *k = row_at(a.k_cache, a.kc, j), *v = row_at(a.v_cache, a.vc, j);
-    if (!k) continue;
-    float s = 0.f;
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int32_t j0 = begin; j0 < end; j0 += kMany) {
+      float k[kMany][E], v[kMany][E], s[kMany];
 #pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], __bfloat162float(k[e]), s);
+      for (int u = 0; u < kMany; ++u) {
+        const bool in = j0 + u < end;
+        load(in ? cache_row(a, a.k_cache, a.kc, table, hk, j0 + u) : nullptr, k[u]);
+        load(in ? cache_row(a, a.v_cache, a.vc, table, hk, j0 + u) : nullptr, v[u]);
+        s[u] = 0.f;
 #pragma unroll
-    for (int u = 16; u > 0; u >>= 1) s += __shfl_xor_sync(0xffffffffu, s, u);
-    const float p = __bfloat162float(__float2bfloat16_rn(ex2(fmaf(s, k2, -M))));  // as the product takes it
+        for (int e = 0; e < E; ++e) s[u] = fmaf(q[e], k[u][e], s[u]);
+      }
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(p, __bfloat162float(v[e]), acc[e]);
-  }
+      for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if (prow >= 0)
-      a.part_o[prow * D + lane * E + e] = acc[e];
-    else
-      static_cast<__nv_bfloat16 *>(a.out)[static_cast<int64_t>(orow) * D + lane * E + e] = __float2bfloat16_rn(acc[e] * inv);
+        for (int u = 0; u < kMany; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+#pragma unroll
+      for (int u = 0; u < kMany; ++u) {
+        if (j0 + u >= end) break;
+        const float p = __bfloat162float(__float2bfloat16_rn(ex2(fmaf(s[u], k2, -ref))));  // as the product takes it
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(p, v[u][e], acc[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (from_prow >= 0)
+        a.part_o[(from_prow + from) * D + lane * E + e] = acc[e];
+      else
+        static_cast<__nv_bfloat16 *>(a.out)[static_cast<int64_t>(row) * D + lane * E + e] = __float2bfloat16_rn(acc[e] * by);
+    }
   }
 }
 
@@ -971,15 +1009,10 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
       }
       // a weight of zero times a NaN or an infinity of a hidden key?
       const float sum = odd.x + odd.y;
-      uint32_t again = __ballot_sync(0xffffffffu, live && sum != sum && l == l && (lo > g.key0 || hi < key1));
+      const uint32_t again = __ballot_sync(0xffffffffu, live && sum != sum && l == l && (lo > g.key0 || hi < key1));
       if (again) {
         __syncwarp();  // the rows are written
-        for (; again; again &= again - 1) {
-          const int from = __ffs(again) - 1;
-          redo_row<D>(a, g.req, g.hk, g.key0, key1, __shfl_sync(0xffffffffu, lo, from), __shfl_sync(0xffffffffu, hi, from),
-                      __shfl_sync(0xffffffffu, M, from), __shfl_sync(0xffffffffu, inv, from),
-                      __shfl_sync(0xffffffffu, orow, from), g.part >= 0 ? prow - lane + from : -1);
-        }
+        redo_rows<D>(a, again, g.req, g.hk, g.key0, key1, lo, hi, M, inv, orow, g.part >= 0 ? prow - lane : -1);
       }
       if (live) {
         if (g.part >= 0)
