@@ -825,6 +825,10 @@ __device__ __noinline__ void redo_rows(const AttendArgs &a, uint32_t again, int3
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = fmaf(p, v[u][e], acc[e]);
       }
+      bool all_nan = true;  // and so they stay: a cache full of NaN is soon done with
+#pragma unroll
+      for (int e = 0; e < E; ++e) all_nan &= acc[e] != acc[e];
+      if (__all_sync(0xffffffffu, all_nan)) break;
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) {
