@@ -97,7 +97,7 @@ struct Shape {
   static constexpr int kTile = kKeys * D * 2;              // of a key or value tile
   static constexpr int kHalf = kKeys * 128;
   static constexpr int kRing = (D == 128) ? 5 : 11;        // key and value tiles in flight of a worker
-  static constexpr int kControl = (D == 128) ? 3072 : 4096;
+  static constexpr int kControl = (D == 128 ? 3 : 4) << 10;  // a whole number of swizzle atoms
   static constexpr int kSmem = kControl + 2 * kQTile + kWorkers * kRing * kTile;
   // columns of tensor memory: scores of stage st, buffer u at st * 128 + u * 64; outputs at 256 + st * D; weights:
   __host__ __device__ static constexpr int weights(int st, int u) { return kApart ? 384 + st * 64 : st * 128 + u * 64; }
