@@ -766,6 +766,7 @@ svw_status paged_attention(const void *q, int64_t q_token_stride, int64_t q_head
   a.status = status;
   a.ws = workspace;
   a.tag = next_epoch();
+  a.fault = svw::test_fault();
   return svw::launch_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SVW_OK : SVW_ERR_CUDA;
 }
 

@@ -138,6 +138,7 @@ struct Control {
   unsigned long long s_full[4], p_full[4];  // 2 * stage + score buffer
   unsigned long long s_read[2];             // by stage (apart): the scores are in registers
   unsigned long long o_full[2], o_free[2], o_step[2];  // by stage: a segment's outputs; read; each tile's (narrow, apart)
+  unsigned long long drain[2];  // by worker: its issuer's products, once a wait has given up
   uint32_t tmem;
   int32_t err;
   int32_t complete[2];  // by stage: every part of the unit is there
@@ -428,7 +429,7 @@ __device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtens
               tma_load_3d(q_smem + s * Sh::kQTile + h * Sh::kQHalf, &tmQ, h * 64, hk * G, r.c0 + t0 + s * a.tile_tokens,
                           smem_u32(&sm.q_full[wk]));
         }
-        ++qc;
+        if (ok) ++qc;
         // the keys and values, a lane per page
         bool bad = false;
         for (int32_t j = j0; j < j1 && ok; ++j, ++count) {
@@ -450,6 +451,7 @@ __device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtens
           for (int v = kFrom; v < kTo && ok; ++v) {
             const int n = 2 * count + v, s = n % Sh::kRing;
             ok = n < Sh::kRing || warp_wait(&ln.empty[s], par(n / Sh::kRing - 1));
+            if (a.fault == 1 && v == 1 && worker % 2 == 0) ok = false;  // test-only: no values come
             if (!ok) break;
             if (v == 0 && j == j1 - 1 && __any_sync(0xffffffffu, bad) && lane == 0) {
               ln.seg_bad[sl] = 1;  // the last keys' arrival carries this to the segment's epilogue
@@ -1036,7 +1038,11 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
     steps += g.tiles;
     ++k;
   }
-  if (!ok && lane == 0) atomicOr(&sm.err, 1);
+  if (!ok) {
+    tmem_wait_st();  // before another warp frees the columns
+    tc_before();
+    if (lane == 0) atomicOr(&sm.err, 1);
+  }
 }
 
 // kInside: narrow, units joined by the last worker
@@ -1075,6 +1081,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ln.first_at = 0;
     }
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.drain[s], 1);
       mbar_init(&sm.q_full[s], 1);
       mbar_init(&sm.q_empty[s], 1);
       mbar_init(&sm.o_full[s], 2);
@@ -1191,11 +1198,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if ((warp == 1 || warp == 3) && (warp >> 1) < Sh::kWorkers) {
-      // an issuer's products: a commit on a barrier that nothing else uses any more
-      unsigned long long *bar = &sm.o_step[warp >> 1];
+      // an issuer's products: a commit by the thread that issued them, on a barrier of its own (earlier commits may
+      // still be on their way to all others)
+      unsigned long long *bar = &sm.drain[warp >> 1];
       if (elect_one()) {
-        mbar_init(bar, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         tc_commit(smem_u32(bar));
         mbar_wait_bounded(bar, 0);
       }

@@ -288,7 +288,8 @@ struct AttendArgs {
   float *lse;
   int32_t *status;
   void *ws;
-  int32_t tag;  // this call's, never 0
+  int32_t tag;    // this call's, never 0
+  int32_t fault;  // test-only (svw_set_fault): 1 = every second worker's values are not loaded
   // set by the launcher
   int32_t tile_tokens;  // tokens of a row tile
   int32_t part_rows;    // rows of a workspace part

@@ -1,0 +1,40 @@
+"""A bounded wait of the round's operators runs out, without a GPU fault: the
+call returns, the status word says so, and the same call afterwards gives the
+bits it gave before (svw_set_fault and svw_set_wait_limit, as in
+test_gpu_timeout)."""
+import numpy as np
+import pytest
+
+from test_gpu_timeout import _assert_recovered, _hooks, _run_three  # noqa: F401 (an autouse fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def _fp32(ts):
+    return [t.float() for t in ts]
+
+
+def _attend_inputs(new, kv, hq, hkv, d, page=64):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(sum(kv))
+    pages = [-(-n // page) for n in kv]
+    first = np.concatenate([[0], np.cumsum(pages)])
+    table = torch.zeros(len(kv), max(pages), dtype=torch.int32)
+    for i, n in enumerate(pages):
+        table[i, :n] = torch.arange(first[i], first[i + 1], dtype=torch.int32)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+    i32 = lambda a: torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
+    shape = (int(first[-1]), hkv, page, d)
+    return (r(sum(new), hq, d), r(*shape), r(*shape), table.cuda(), i32(np.concatenate([[0], np.cumsum(new)])), i32(kv))
+
+
+@pytest.mark.parametrize("new,kv,d", [
+    ([1], [20000], 128), ([1], [20000], 64),                        # joined by the last worker
+    ([1] * 40, [3000] * 40, 128), ([1] * 40, [3000] * 40, 64),      # joined by a kernel of its own
+    ([300], [2000], 128), ([300], [2000], 64)])                     # row tiles in pairs
+def test_attend_values_do_not_come(new, kv, d):
+    """The products of every second worker wait for values that are not loaded,
+    their scores already under way."""
+    import serving_vocab_wide_gb300 as svw
+    args = _attend_inputs(new, kv, 8, 2, d)
+    _assert_recovered(*_run_three(lambda st: _fp32(svw.paged_attention(*args, status=st))))
