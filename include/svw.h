@@ -515,7 +515,8 @@ svw_status kv_append(const void *k, int64_t k_token_stride, int64_t k_head_strid
  *   status     SVW_DEV_BAD_INPUT when a request's new-token range is invalid
  *              (nothing of it is written), its kv_len exceeds its block table
  *              or a page that it needs is not one of the cache's (its out and
- *              lse become NaN).
+ *              lse become NaN).  After SVW_DEV_TIMEOUT a captured call is
+ *              captured again before it is replayed.
  * q and the caches: 16-byte aligned, strides positive multiples of 8 elements
  * (those of dimensions of one do not count).
  * Scores and sums are fp32; the weights enter the second product in bf16.
@@ -594,9 +595,11 @@ svw_status svw_time_next_launch(const char *kernel, void *begin_event, void *end
  * (opd_loss, spec_verify_opd) issue no bulk copy, so their first wait
  * runs out with nothing in flight; every second worker of paged_attention
  * loads no values, so that the waits for its outputs run out behind its
- * scores.  The call returns, its status word holds SVW_DEV_TIMEOUT, and the
- * results of the affected rows are void.  Other values: SVW_ERR_INVALID_ARG.
- * Host-side state, shared by all threads.
+ * scores, and in a call of few tokens one warp of the other workers leaves
+ * before a part is marked, so that the others' wait for it runs out.  The call
+ * returns, its status word holds SVW_DEV_TIMEOUT, and the results of the
+ * affected rows are void.  Other values: SVW_ERR_INVALID_ARG.  Host-side
+ * state, shared by all threads.
  */
 svw_status svw_set_wait_limit(int64_t cycles);
 svw_status svw_set_fault(int32_t kind);

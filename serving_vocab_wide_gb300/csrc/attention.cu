@@ -139,6 +139,7 @@ struct Control {
   unsigned long long s_read[2];             // by stage (apart): the scores are in registers
   unsigned long long o_full[2], o_free[2], o_step[2];  // by stage: a segment's outputs; read; each tile's (narrow, apart)
   unsigned long long drain[2];  // by worker: its issuer's products, once a wait has given up
+  unsigned long long meet[2];   // by stage: its softmax warps, about a part (kInside)
   uint32_t tmem;
   int32_t err;
   int32_t complete[2];  // by stage: every part of the unit is there
@@ -715,33 +716,41 @@ __device__ __forceinline__ void join_rows(const AttendArgs &a, const Joint &jt, 
 // may both see them all: they write the same results).  No worker waits for
 // another.  The joiner takes the marks off again, so that a graph that replays
 // a call with its tag finds none.  A mark is 64 bits of the tag and the part's
-// number: what else has been in the workspace does not look like one.
+// number: what else has been in the workspace does not look like one.  The warps
+// meet at an mbarrier, whose wait ends where a hardware barrier's would not: one
+// of them may have given up a wait and gone.  False: such a warp did not come.
 __device__ __forceinline__ unsigned long long mark_of(const AttendArgs &a, int part) {
   return static_cast<unsigned long long>(static_cast<uint32_t>(a.tag)) * 0x9e3779b97f4a7c15ull ^
          static_cast<unsigned long long>(part + 1);
 }
 template <int D>
-__device__ __forceinline__ void mark_and_join(const AttendArgs &a, const Segment &g, int s, int row, int32_t *complete) {
+__device__ __forceinline__ bool mark_and_join(const AttendArgs &a, const Segment &g, int row, unsigned long long *bar,
+                                              int32_t &meetings, int32_t *complete) {
   const Joint jt = {g.last, g.tok0, g.ntok0, g.ntok1, g.hk, {}};
   const int n = g.last - g.first + 1;
-  auto meet = [&] { named_sync(1 + s, kRows); };
+  auto meet = [&] {
+    __syncwarp();
+    if ((row & 31) == 0) mbar_arrive(bar);
+    return warp_wait(bar, par(meetings++));
+  };
   __threadfence();  // this thread's share of the part
-  meet();
+  if (!meet()) return false;
   if (row == 0) {
     *complete = 1;
     *reinterpret_cast<volatile unsigned long long *>(a.marks + g.part) = mark_of(a, g.part);
     __threadfence();
   }
-  meet();
+  if (!meet()) return false;
   for (int q = row; q < n; q += kRows) {
     const int part = part_of(g.first, q);
     if (*reinterpret_cast<volatile unsigned long long *>(a.marks + part) != mark_of(a, part)) *complete = 0;
   }
-  meet();
-  if (*reinterpret_cast<volatile int32_t *>(complete) == 0) return;
+  if (!meet()) return false;
+  if (*reinterpret_cast<volatile int32_t *>(complete) == 0) return true;
   __threadfence();
   join_rows<D, 8>(a, jt, g.first, row >> 5, kRows / 32);
   for (int q = row; q < n; q += kRows) a.marks[part_of(g.first, q)] = 0;
+  return true;
 }
 
 // ---------------------------- what a mask hides -----------------------------
@@ -857,6 +866,7 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
   const uint32_t t_o = tmem + lanes + 256 + s * D;
   const float k2 = a.scale * kLog2e;
   int32_t count = 0, k = 0, steps = 0, sc[2] = {0, 0};  // ring tiles, segments, outputs, score tiles by buffer
+  int32_t meetings = 0;
   bool ok = true;
   while (true) {
     const int sl = k % kSegRing;
@@ -1033,7 +1043,10 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
       mbar_arrive(&sm.o_free[s]);
       mbar_arrive(&ln.seg_empty[sl]);
     }
-    if (kInside && g.part >= 0) mark_and_join<D>(a, g, s, row, &sm.complete[s]);
+    if (kInside && g.part >= 0) {
+      if (a.fault == 1 && s == 1 && quad == 3) ok = false;  // test-only: as if this warp's wait had run out
+      if (!ok || !(ok = mark_and_join<D>(a, g, row, &sm.meet[s], meetings, &sm.complete[s]))) break;
+    }
     count += 2 * g.tiles;
     steps += g.tiles;
     ++k;
@@ -1088,6 +1101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.o_free[s], 4);
       mbar_init(&sm.o_step[s], 1);
       mbar_init(&sm.s_read[s], 4);
+      mbar_init(&sm.meet[s], 4);
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&sm.s_full[s], 1);

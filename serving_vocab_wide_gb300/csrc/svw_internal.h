@@ -289,7 +289,7 @@ struct AttendArgs {
   int32_t *status;
   void *ws;
   int32_t tag;    // this call's, never 0
-  int32_t fault;  // test-only (svw_set_fault): 1 = every second worker's values are not loaded
+  int32_t fault;  // test-only (svw_set_fault): 1 = every second worker's values are not loaded, and a warp of the others leaves early
   // set by the launcher
   int32_t tile_tokens;  // tokens of a row tile
   int32_t part_rows;    // rows of a workspace part
