@@ -593,12 +593,13 @@ svw_status svw_time_next_launch(const char *kernel, void *begin_event, void *end
  * svw_set_fault -- 0: none (default); 1: in the next calls until reset, CTA 0
  * of verify_stats (spec_verify) and cluster 0 of opd_fast_kernel
  * (opd_loss, spec_verify_opd) issue no bulk copy, so their first wait
- * runs out with nothing in flight; every second worker of paged_attention
- * loads no values, so that the waits for its outputs run out behind its
- * scores, and in a call of few tokens one warp of the other workers leaves
- * before a part is marked, so that the others' wait for it runs out.  The call
- * returns, its status word holds SVW_DEV_TIMEOUT, and the results of the
- * affected rows are void.  Other values: SVW_ERR_INVALID_ARG.  Host-side
+ * runs out with nothing in flight, and so does CTA 0 of adjust_staged
+ * (logits_adjust, a large batch out of place); every second worker of
+ * paged_attention loads no values, so that the waits for its outputs run out
+ * behind its scores, and in a call of few tokens one warp of the other workers
+ * leaves before a part is marked, so that the others' wait for it runs out.
+ * The call returns, its status word holds SVW_DEV_TIMEOUT, and the results of
+ * the affected rows are void.  Other values: SVW_ERR_INVALID_ARG.  Host-side
  * state, shared by all threads.
  */
 svw_status svw_set_wait_limit(int64_t cycles);

@@ -697,6 +697,7 @@ __global__ void __launch_bounds__(kAdjThreads, 7) adjust_staged(const __grid_con
     return static_cast<uint32_t>((r.len - head) / EPV * 16);
   };
   auto fetch = [&](int q) {  // by thread 0
+    if (a.fault == 1 && blockIdx.x == 0) return;  // test-only
     int head;
     const uint32_t bytes = interior(q, head);
     mbar_arrive_expect_tx(&full[q % kStages], bytes);
@@ -724,6 +725,7 @@ __global__ void __launch_bounds__(kAdjThreads, 7) adjust_staged(const __grid_con
   };
   if (!ls.bad && tid < min(ls.n, kListed)) held[tid] = entry(tid);
   __syncthreads();
+  int fetched = min(kStages, r.rows);  // rows
   bool ok = true;
   for (int q = 0; q < r.rows; ++q) {
     T *row = at(q);
@@ -738,7 +740,7 @@ __global__ void __launch_bounds__(kAdjThreads, 7) adjust_staged(const __grid_con
     const uint32_t next_word = mask_at(q + 1);
     const uint32_t *word = mask_word[q & 1];
     auto allowed = [&](int u) { return m < 0 || ((word[u >> 5] >> (u & 31)) & 1u); };
-    ok = mbar_wait_bounded(&full[q % kStages], static_cast<uint32_t>((q / kStages) & 1)) && ok;
+    ok = mbar_wait_bounded(&full[q % kStages], static_cast<uint32_t>((q / kStages) & 1));
     if (m >= 0 || spoilt) {
       if (mine >= 0) {
         if (spoilt)
@@ -764,7 +766,8 @@ __global__ void __launch_bounds__(kAdjThreads, 7) adjust_staged(const __grid_con
         *x = y;
       }
     }
-    __syncthreads();
+    ok = __syncthreads_and(ok) != 0;
+    if (!ok) break;  // all threads: a stage whose copy is late is not filled again
     if (!spoilt) {
       for (int k = tid; k < ls.n; k += kAdjThreads) {
         const int4 e = k < kListed ? held[k] : entry(k);
@@ -787,11 +790,18 @@ __global__ void __launch_bounds__(kAdjThreads, 7) adjust_staged(const __grid_con
       if (q >= 1 && q - 1 + kStages < r.rows) {
         asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
         fetch(q - 1 + kStages);
+        fetched = q + kStages;
       }
     }
   }
-  if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-  if (!ok && a.status) atomicOr(a.status, SVW_DEV_TIMEOUT);
+  if (tid == 0) {
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    if (!ok) {  // a wait gave up: what is in flight lands before the CTA goes
+      if (a.status) atomicOr(a.status, SVW_DEV_TIMEOUT);
+      for (int q = max(0, fetched - kStages); q < fetched; ++q)
+        mbar_wait_bounded(&full[q % kStages], static_cast<uint32_t>((q / kStages) & 1));
+    }
+  }
 }
 
 // In place (only what changes is written), or rows that do not lie alike: through registers.

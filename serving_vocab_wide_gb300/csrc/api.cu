@@ -607,6 +607,7 @@ svw_status logits_adjust(const void *logits, int64_t logits_stride, svw_dtype dt
   a.mask_words = (static_cast<int64_t>(V) + 31) / 32;
   a.mask_row = mask_row;
   a.status = status;
+  a.fault = svw::test_fault();
   a.ws = workspace;
   return svw::launch_adjust(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SVW_OK : SVW_ERR_CUDA;
 }

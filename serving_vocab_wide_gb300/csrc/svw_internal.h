@@ -231,7 +231,8 @@ struct AdjustArgs {
   int64_t mask_rows, mask_words;
   const int32_t *mask_row;
   int32_t *status;
-  void *ws;  // NULL: the chunks' CTAs count for themselves
+  int32_t fault;  // test-only (svw_set_fault): 1 = CTA 0 of adjust_staged copies nothing in
+  void *ws;       // NULL: the chunks' CTAs count for themselves
   // set by the launcher
   int32_t chunk_len, chunks, groups;  // entries of a CTA's chunk; CTAs of a request's vocabulary, of its rows
   int32_t list_chunks, list_shift, even;  // chunks of the lists, of 2^shift entries; 1: CTAs of a request's vocabulary share its list evenly

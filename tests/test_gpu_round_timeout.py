@@ -47,3 +47,20 @@ def test_attend_a_warp_does_not_come_to_the_join(new, kv, d):
     import serving_vocab_wide_gb300 as svw
     args = _attend_inputs(new, kv, 8, 2, d)
     _assert_recovered(*_run_three(lambda st: _fp32(svw.paged_attention(*args, status=st))))
+
+
+@pytest.mark.parametrize("V,dtype", [(20488, "bf16"), (20489, "fp32")])
+def test_adjust_rows_do_not_come(V, dtype):
+    """A CTA whose rows do not reach shared memory stops at the first of them."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    n, each = 150, 4
+    R = n * each
+    assert svw.logits_adjust_workspace_size(n, V, R, 0, 0) > 0
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = torch.randn(R + n, V, generator=g, device="cuda").to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    cu = torch.arange(0, R + 1, each, dtype=torch.int32, device="cuda")
+    tokens = torch.randint(0, V, (R,), generator=g, device="cuda", dtype=torch.int32)
+    rep = 1 + torch.rand(n, generator=g, device="cuda")
+    call = lambda st: _fp32([svw.logits_adjust(x, cu, tokens, repetition=rep, total_draft_rows=R, status=st)])
+    _assert_recovered(*_run_three(call))
