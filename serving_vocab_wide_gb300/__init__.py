@@ -476,12 +476,19 @@ def _torch():
     return torch
 
 
-def _lent(stream, *ts):
-    """Tensors allocated here and used on another stream than the current one
-    stay the allocator's to reuse only after that stream is done with them."""
-    if stream is not None:
-        for t in ts:
-            t.record_stream(stream)
+def _empty(stream, gpu, shape, dtype, device, returned=True):
+    """An empty tensor to be written on `stream` (None: the current one).  It
+    comes from that stream's pool: what the current stream has given back may
+    still be in use there.  The program reads what is returned to it on the
+    current stream, so it is reused only after that one is done with it too."""
+    torch = _torch()
+    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(gpu):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 @functools.lru_cache(maxsize=64)
@@ -554,15 +561,13 @@ def logits_adjust(logits, cu_draft, draft_tokens=None, *, history=None, cu_histo
     elif mask_row is not None:
         raise SvwError("mask_row comes with a mask")
     if out is None:
-        out = torch.empty((rows, V), dtype=logits.dtype, device=logits.device)
-        _lent(stream, out)
+        out = _empty(stream, gpu, (rows, V), logits.dtype, logits.device)
     elif out is not logits and (out.dtype is not logits.dtype or out.get_device() != gpu or out.shape != logits.shape
                                 or out.stride(1) != 1):
         raise SvwError("out must be like logits")
     if workspace is None:
         if need := logits_adjust_workspace_size(N, V, R, n_history, n_bias):
-            workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
-            _lent(stream, workspace)
+            workspace = _empty(stream, gpu, need, torch.uint8, logits.device, returned=False)
     elif _off(workspace, torch.uint8, gpu):
         raise SvwError(f"workspace must be a contiguous uint8 tensor on cuda:{gpu}")
     # a single row has no pitch of its own
@@ -654,8 +659,7 @@ def kv_append(k, v, k_cache, v_cache, block_table, cu_new, kv_len, *, cos_sin=No
         if qh[0] != T:
             raise SvwError("q must have as many tokens as k")
         if q_out is None:
-            q_out = torch.empty(qh, dtype=dtype, device=q.device)
-            _lent(stream, q_out)
+            q_out = _empty(stream, gpu, qh, dtype, q.device)
         elif _off(q_out, dtype, gpu) or q_out.shape != qh:
             raise SvwError("q_out must be like q, contiguous")
     elif q_out is not None:
@@ -699,20 +703,17 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, *, scale: 
     if kv_len.numel() != N:
         raise SvwError(f"kv_len must have {N} elements")
     if out is None:
-        out = torch.empty(qh, dtype=dtype, device=q.device)
-        _lent(stream, out)
+        out = _empty(stream, gpu, qh, dtype, q.device)
     elif _off(out, dtype, gpu) or out.shape != qh:
         raise SvwError("out must be like q, contiguous")
     if lse is None:
         if want_lse:
-            lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
-            _lent(stream, lse)
+            lse = _empty(stream, gpu, (T, hq), torch.float32, q.device)
     elif _off(lse, torch.float32, gpu) or lse.numel() != T * hq:
         raise SvwError(f"lse must be a contiguous float32 [{T}, {hq}] tensor on cuda:{gpu}")
     if workspace is None:
         need = paged_attention_workspace_size(T, hq, shape[1], dim)
-        workspace = torch.empty(max(1, need), dtype=torch.uint8, device=q.device)
-        _lent(stream, workspace)
+        workspace = _empty(stream, gpu, max(1, need), torch.uint8, q.device, returned=False)
     elif _off(workspace, torch.uint8, gpu):
         raise SvwError(f"workspace must be a contiguous uint8 tensor on cuda:{gpu}")
     rc = lib().paged_attention(q.data_ptr(), qs[0], qs[1], _dtype_code(q), hq, N, cu_new.data_ptr(), T,

@@ -571,3 +571,24 @@ def test_paged_refusals():
     out, lse = att(q=q[:0], cu_new=none)
     assert out.shape == (0, hq, d) and lse.shape == (0, hq)
     assert app(k=k[:0], v=v[:0], cu_new=none) is None
+
+
+@pytest.mark.parametrize("n,kv,hq", [(1, 60000, 8), (20, 30000, 4), (150, 9000, 4)])
+def test_attend_on_two_streams_without_a_wait(n, kv, hq):
+    """Calls that make their own workspaces, in turn on the current stream and on
+    another, the second before the first has ended: neither disturbs the other."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(kv)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+    pages = -(-kv // 64)
+    rest = (r(pages, 2, 64, 128), r(pages, 2, 64, 128), _i32(np.arange(pages)[None]), _i32([0, n]), _i32([kv]))
+    qs = [r(n, hq, 128) for _ in range(2)]
+    want = [svw.paged_attention(q, *rest) for q in qs]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(10):
+        got = [svw.paged_attention(qs[0], *rest), svw.paged_attention(qs[1], *rest, stream=side)]
+        torch.cuda.synchronize()
+        for (o, l), (wo, wl) in zip(got, want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
