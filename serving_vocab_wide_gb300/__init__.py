@@ -476,6 +476,12 @@ def _torch():
     return torch
 
 
+def _need_current(stream, gpu):
+    """The library launches on the current device: the tensors' GPU has to be it, and the stream's."""
+    if _torch()._C._cuda_getDevice() != gpu or (stream is not None and stream.device.index != gpu):
+        raise SvwError(f"cuda:{gpu} must be the current device, and the stream's")
+
+
 def _empty(stream, gpu, shape, dtype, device, returned=True):
     """An empty tensor to be written on `stream` (None: the current one).  It
     comes from that stream's pool: what the current stream has given back may
@@ -520,6 +526,7 @@ def logits_adjust(logits, cu_draft, draft_tokens=None, *, history=None, cu_histo
     gpu = logits.get_device()
     if gpu < 0 or logits.dim() != 2 or logits.stride(1) != 1:
         raise SvwError("logits must be a CUDA matrix with contiguous rows")
+    _need_current(stream, gpu)
     rows, V = logits.shape
     N = cu_draft.numel() - 1
     R = int(cu_draft[-1].item()) if total_draft_rows is None else int(total_draft_rows)
@@ -635,6 +642,7 @@ def kv_append(k, v, k_cache, v_cache, block_table, cu_new, kv_len, *, cos_sin=No
     i32 = torch.int32
     N = cu_new.numel() - 1
     cache, gpu, shape = _paged(k_cache, v_cache, block_table, N)
+    _need_current(stream, gpu)
     dim, dtype = shape[3], k_cache.dtype
     kh, ks = _heads("k", k, dim, dtype, gpu)
     vh, vs = _heads("v", v, dim, dtype, gpu)
@@ -695,6 +703,7 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, *, scale: 
     i32 = torch.int32
     N = cu_new.numel() - 1
     cache, gpu, shape = _paged(k_cache, v_cache, block_table, N)
+    _need_current(stream, gpu)
     dim, dtype = shape[3], k_cache.dtype
     qh, qs = _heads("q", q, dim, dtype, gpu)
     T, hq, _ = qh

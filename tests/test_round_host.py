@@ -120,3 +120,20 @@ def test_memory_comes_from_the_stream_that_uses_it(host, name, outputs, workspac
     _calls()[name]()
     assert all(t.pool is current and not t.recorded for t in host.made)
     assert host.calls[1][1][-1] == current.cuda_stream
+
+
+@pytest.mark.parametrize("name", ["paged_attention", "kv_append", "logits_adjust"])
+def test_another_gpu_than_the_current_one_is_refused(host, name):
+    """The library launches on the current device: tensors or a stream of another
+    one are refused before anything is taken or launched."""
+    host.device = 1
+    with pytest.raises(svw.SvwError, match="current"):
+        _calls()[name]()
+    host.device = 0
+    with pytest.raises(svw.SvwError, match="current"):
+        _calls(stream=Stream(9, gpu=1))[name]()
+    assert not host.made and not host.calls
+    _calls(stream=Stream(9))[name]()
+    host.device = 1
+    _calls(gpu=1, stream=Stream(11, gpu=1))[name]()
+    assert len(host.calls) == 2
