@@ -591,8 +591,8 @@ def logits_adjust(logits, cu_draft, draft_tokens=None, *, history=None, cu_histo
     return out
 
 
-# svw_paged_kv, field by field
-_pack_paged = struct.Struct("@2P6qPq5i").pack
+# svw_paged_kv, field by field; its end is padded as a C struct's is
+_pack_paged = struct.Struct("@2P6qPq5i0q").pack
 
 
 def _paged(k_cache, v_cache, block_table, N):

@@ -137,3 +137,16 @@ def test_another_gpu_than_the_current_one_is_refused(host, name):
     host.device = 1
     _calls(gpu=1, stream=Stream(11, gpu=1))[name]()
     assert len(host.calls) == 2
+
+
+def test_the_cache_is_handed_over_whole():
+    """The bytes of svw_paged_kv: as many as the library copies, each field in its place."""
+    k, v, table = Tensor((10, 2, 16, 64), BF16), Tensor((10, 2, 16, 64), BF16), Tensor((3, 4), I32)
+    k.data_ptr, v.data_ptr, table.data_ptr = (lambda: 0x1000), (lambda: 0x2000), (lambda: 0x3000)
+    packed, gpu, shape = svw._paged(k, v, table, 3)
+    assert len(packed) == ctypes.sizeof(svw._PagedKV) == 104
+    c = svw._PagedKV.from_buffer_copy(packed)
+    assert (c.k, c.v, c.block_table) == (0x1000, 0x2000, 0x3000)
+    assert list(c.k_stride) == list(c.v_stride) == [2048, 1024, 64]
+    assert (c.table_stride, c.max_pages, c.n_pages, c.page_size, c.n_kv_heads, c.head_dim) == (4, 4, 10, 16, 2, 64)
+    assert gpu == 0 and shape == k.shape
