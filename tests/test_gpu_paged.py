@@ -592,3 +592,34 @@ def test_attend_on_two_streams_without_a_wait(n, kv, hq):
         torch.cuda.synchronize()
         for (o, l), (wo, wl) in zip(got, want):
             assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+@pytest.mark.parametrize("hkv,d,rot,dtype", [(2, 64, 32, "bf16"), (1, 128, 64, "fp32"), (3, 10, 6, "fp32"), (3, 10, 4, "bf16")])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("tokens", [3, 400])
+def test_append_a_query_without_a_position_is_nan(hkv, d, rot, dtype, inter, tokens):
+    """All of it, the elements that are not rotated too; its key and value are not
+    written, the other tokens are as ever."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    rng = np.random.default_rng(d + rot)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    new, kv = [tokens], [tokens + 20]
+    kc, vc, table = _cache(rng, new, kv, hkv, d, 16, dt)
+    q, k, v = _append_inputs(rng, new, 2 * hkv, hkv, d, dt)
+    cs = torch.from_numpy(rng.normal(size=(40, rot)).astype(np.float32)).cuda()
+    pos = rng.integers(0, 40, tokens).astype(np.int32)
+    pos[[0, tokens // 2]] = [40, -1]
+    k_old, v_old = kc.clone(), vc.clone()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = svw.kv_append(k, v, kc, vc, _i32(table), _i32(_cu(new)), _i32(kv), cos_sin=cs, interleaved=inter,
+                        positions=_i32(pos), q=q, status=status)
+    assert int(status) == svw.SVW_DEV_BAD_INPUT
+    bad = torch.from_numpy((pos < 0) | (pos >= 40)).cuda()
+    assert bool(out[bad].isnan().all()) and not bool(out[~bad].isnan().any())
+    for t in torch.nonzero(bad).flatten().tolist():
+        s, r = int(table[0, (20 + t) // 16]), (20 + t) % 16
+        assert torch.equal(kc[s, :, r], k_old[s, :, r]) and torch.equal(vc[s, :, r], v_old[s, :, r])
+    good = svw.kv_append(k, v, kc, vc, _i32(table), _i32(_cu(new)), _i32(kv), cos_sin=cs, interleaved=inter,
+                         positions=_i32(np.clip(pos, 0, 39)), q=q)
+    assert torch.equal(out[~bad], good[~bad])
