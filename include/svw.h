@@ -514,8 +514,9 @@ svw_status kv_append(const void *k, int64_t k_token_stride, int64_t k_head_strid
  *              bytes; contents need not be initialised; not preserved.
  *   status     SVW_DEV_BAD_INPUT when a request's new-token range is invalid
  *              (nothing of it is written), its kv_len exceeds its block table
- *              or a page that it needs is not one of the cache's (its out and
- *              lse become NaN).  After SVW_DEV_TIMEOUT a captured call is
+ *              (its out and lse become NaN) or a page that a token sees is not
+ *              one of the cache's (that token's out and lse become NaN, those
+ *              of tokens that do not see it are right).  After SVW_DEV_TIMEOUT a captured call is
  *              captured again before it is replayed.
  * q and the caches: 16-byte aligned, strides positive multiples of 8 elements
  * (those of dimensions of one do not count).

@@ -126,7 +126,7 @@ struct Lane {  // of a worker
   unsigned long long full[kRing], empty[kRing];
   unsigned long long seg_full[kSegRing], seg_empty[kSegRing];
   Segment seg[kSegRing];
-  int32_t seg_bad[kSegRing];
+  int32_t seg_bad[kSegRing];  // 1: a page that is none of the cache's, 2: every token is bad
   int32_t issued[2], q_issued;  // key tiles, value tiles; query tiles
   int32_t first_req;
   int64_t first_at;
@@ -409,7 +409,7 @@ __device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtens
           // position x of the line is worker ((x + 1) workers - 1) / W's
           s.first = static_cast<int32_t>(((at + Sh::kUnitCost + 1) * workers - 1) / W);
           s.last = static_cast<int32_t>(((at + cost) * workers - 1) / W);
-          ln.seg_bad[sl] = r.bad ? 1 : 0;
+          ln.seg_bad[sl] = r.bad ? 2 : 0;
           if (j0 == 0 && !whole) {
             joint.last = s.last;
             joint.tok0 = s.tok0;
@@ -851,6 +851,15 @@ __device__ __noinline__ void redo_rows(const AttendArgs &a, uint32_t again, int3
   }
 }
 
+// Does a row that sees keys [from, to) see one in a page that is none of the cache's?  Its result is NaN; rows that do
+// not are right, whatever unit they share.
+__device__ __noinline__ bool sees_bad_page(const AttendArgs &a, int32_t req, int32_t from, int32_t to) {
+  const int32_t *table = a.table + req * a.table_stride;
+  for (int32_t p = from / a.page_size; from < to && p <= (to - 1) / a.page_size; ++p)
+    if (const int32_t page = __ldg(table + p); page < 0 || page >= a.n_pages) return true;
+  return false;
+}
+
 // ------------------------------- the softmax --------------------------------
 // Of stage s: a thread has one row and all keys of a tile.
 template <int D, bool kWide, bool kInside, typename C>
@@ -978,7 +987,10 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
     if (!(ok = warp_wait(&sm.o_full[s], par(k)))) break;
     tc_after();
     if (warp_live) {
-      if (*reinterpret_cast<volatile int32_t *>(&ln.seg_bad[sl]) != 0) l = kNaN;
+      // keys of the segment that exist; those beyond them no row sees
+      const int32_t key1 = min(g.kv, g.key0 + g.tiles * Sh::kKeys);
+      const int32_t bad = *reinterpret_cast<volatile int32_t *>(&ln.seg_bad[sl]);
+      if (bad == 2 || (bad == 1 && live && sees_bad_page(a, g.req, max(lo, g.key0), min(hi, key1)))) l = kNaN;
       const int32_t tok = g.tok0 + tile * a.tile_tokens + tok_of_row;
       const int32_t orow = live ? tok * a.Hq + g.hk * G + head_of_row : -1;  // below 2^31, checked by the host
       const int64_t prow = static_cast<int64_t>(max(g.part, 0)) * a.part_rows + tile * kRows + row;
@@ -988,7 +1000,6 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
       for (int q = 0; q < 4; ++q) to[q] = __shfl_sync(0xffffffffu, orow, (lane & ~3) + q);
       const int piece = lane & 3;
       // does the segment have keys hidden from one of the rows?  Then their outputs' sum is looked at for a NaN
-      const int32_t key1 = min(g.kv, g.key0 + g.tiles * Sh::kKeys);
       const bool hides = __any_sync(0xffffffffu, live && (lo > g.key0 || hi < key1));
       float2 odd = make_float2(0.f, 0.f);
 #pragma unroll 1

@@ -623,3 +623,35 @@ def test_append_a_query_without_a_position_is_nan(hkv, d, rot, dtype, inter, tok
     good = svw.kv_append(k, v, kc, vc, _i32(table), _i32(_cu(new)), _i32(kv), cos_sin=cs, interleaved=inter,
                          positions=_i32(np.clip(pos, 0, 39)), q=q)
     assert torch.equal(out[~bad], good[~bad])
+
+
+@pytest.mark.parametrize("new,kv,hq,hkv,d,page,first,window", [
+    ([300], [2000], 8, 2, 128, 64, 1728, 0), ([300], [2000], 8, 2, 64, 16, 1840, 0),  # row tiles in pairs
+    ([300], [2000], 8, 2, 128, 16, 1760, 100),
+    ([40, 3], [2000, 100], 2, 2, 128, 16, 1984, 0), ([40, 3], [2000, 100], 2, 2, 64, 16, 1968, 20),
+    ([17], [20000], 4, 1, 128, 16, 19984, 0),
+    ([3], [20001], 4, 1, 128, 16, 20000, 0), ([3], [20000], 4, 1, 64, 64, 64, 19871)])  # joined by the last worker
+def test_attend_a_bad_page_reaches_the_tokens_that_see_it(new, kv, hq, hkv, d, page, first, window):
+    """The page of places first .. first + page - 1 of request 0 is none of the
+    cache's: tokens that see one of them are NaN, the others as with a good page."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    rng = np.random.default_rng(first)
+    kc, vc, table = _cache(rng, new, kv, hkv, d, page, torch.bfloat16)
+    q = torch.from_numpy(rng.normal(size=(int(np.sum(new)), hq, d))).to(torch.bfloat16).cuda()
+    rest = (_i32(_cu(new)), _i32(kv))
+    good = svw.paged_attention(q, kc, vc, _i32(table), *rest, window=window)
+    at = kv[0] - new[0] + np.arange(new[0])
+    sees = at >= first
+    if window:
+        sees &= at - window < first + page - 1
+    assert sees.any() and not sees.all()
+    sees = torch.from_numpy(np.concatenate([sees, np.zeros(sum(new[1:]), bool)])).cuda()
+    for plant in (-1, kc.shape[0]):
+        t2 = table.copy()
+        t2[0, first // page] = plant
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = svw.paged_attention(q, kc, vc, _i32(t2), *rest, window=window, status=status)
+        assert int(status) == svw.SVW_DEV_BAD_INPUT
+        assert bool(out[sees].isnan().all()) and bool(lse[sees].isnan().all())
+        assert torch.equal(out[~sees], good[0][~sees]) and torch.equal(lse[~sees], good[1][~sees])
