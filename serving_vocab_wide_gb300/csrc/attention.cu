@@ -783,19 +783,39 @@ __device__ __forceinline__ bool odd_values(const AttendArgs &a, const int32_t *t
   return __any_sync(0xffffffffu, odd);
 }
 // Of a warp: rows `again` (by lane) of the segment's keys [key0, key1).  from_prow: lane 0's row of the part, -1: the
-// outputs are the result.
+// outputs are the result.  bad_page: the segment has a page that is none of the cache's; rows that see one of its keys
+// become NaN, and the lane is told so (the others are right, whatever unit they share).
 template <int D>
-__device__ __noinline__ void redo_rows(const AttendArgs &a, uint32_t again, int32_t req, int32_t hk, int32_t key0,
-                                       int32_t key1, int32_t lo, int32_t hi, float M, float inv, int32_t orow,
-                                       int64_t from_prow) {
+__device__ __noinline__ bool redo_rows(const AttendArgs &a, uint32_t again, bool bad_page, int32_t req, int32_t hk,
+                                       int32_t key0, int32_t key1, int32_t lo, int32_t hi, float M, float inv,
+                                       int32_t orow, int64_t from_prow) {
   constexpr int E = D / 32, kMany = 8;  // elements of a lane; keys under way
   const int lane = threadIdx.x & 31;
   const int32_t *table = a.table + req * a.table_stride;
+  auto put = [&](int from, int32_t row, int e, float x, float by) {
+    if (from_prow >= 0)
+      a.part_o[(from_prow + from) * D + lane * E + e] = x;
+    else
+      static_cast<__nv_bfloat16 *>(a.out)[static_cast<int64_t>(row) * D + lane * E + e] = __float2bfloat16_rn(x * by);
+  };
+  bool spoilt = false;
+  if (bad_page) {
+    const int32_t from = max(lo, key0), to = orow >= 0 ? min(hi, key1) : 0;
+    for (int32_t p = from / a.page_size; !spoilt && from < to && p <= (to - 1) / a.page_size; ++p)
+      if (const int32_t page = __ldg(table + p); page < 0 || page >= a.n_pages) spoilt = true;
+    const uint32_t rows = __ballot_sync(0xffffffffu, spoilt);
+    for (uint32_t left = rows; left; left &= left - 1) {
+      const int32_t row = __shfl_sync(0xffffffffu, orow, __ffs(left) - 1);
+      for (int e = 0; e < E; ++e) put(__ffs(left) - 1, row, e, kNaN, 1.f);
+    }
+    again &= ~rows;
+    if (!again) return spoilt;
+  }
   const bool mine = (again >> lane) & 1u;
   const int32_t lo_most = __reduce_max_sync(0xffffffffu, mine ? lo : 0);
   const int32_t hi_least = __reduce_min_sync(0xffffffffu, mine ? hi : INT32_MAX);
   if (!odd_values<D>(a, table, hk, key0, min(lo_most, key1)) && !odd_values<D>(a, table, hk, max(hi_least, key0), key1))
-    return;
+    return spoilt;
   const float k2 = a.scale * kLog2e;
   auto load = [&](const __nv_bfloat16 *p, float *x) {
 #pragma unroll
@@ -842,22 +862,9 @@ __device__ __noinline__ void redo_rows(const AttendArgs &a, uint32_t again, int3
       if (__all_sync(0xffffffffu, all_nan)) break;
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (from_prow >= 0)
-        a.part_o[(from_prow + from) * D + lane * E + e] = acc[e];
-      else
-        static_cast<__nv_bfloat16 *>(a.out)[static_cast<int64_t>(row) * D + lane * E + e] = __float2bfloat16_rn(acc[e] * by);
-    }
+    for (int e = 0; e < E; ++e) put(from, row, e, acc[e], by);
   }
-}
-
-// Does a row that sees keys [from, to) see one in a page that is none of the cache's?  Its result is NaN; rows that do
-// not are right, whatever unit they share.
-__device__ __noinline__ bool sees_bad_page(const AttendArgs &a, int32_t req, int32_t from, int32_t to) {
-  const int32_t *table = a.table + req * a.table_stride;
-  for (int32_t p = from / a.page_size; from < to && p <= (to - 1) / a.page_size; ++p)
-    if (const int32_t page = __ldg(table + p); page < 0 || page >= a.n_pages) return true;
-  return false;
+  return spoilt;
 }
 
 // ------------------------------- the softmax --------------------------------
@@ -987,10 +994,8 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
     if (!(ok = warp_wait(&sm.o_full[s], par(k)))) break;
     tc_after();
     if (warp_live) {
-      // keys of the segment that exist; those beyond them no row sees
-      const int32_t key1 = min(g.kv, g.key0 + g.tiles * Sh::kKeys);
       const int32_t bad = *reinterpret_cast<volatile int32_t *>(&ln.seg_bad[sl]);
-      if (bad == 2 || (bad == 1 && live && sees_bad_page(a, g.req, max(lo, g.key0), min(hi, key1)))) l = kNaN;
+      if (bad == 2) l = kNaN;
       const int32_t tok = g.tok0 + tile * a.tile_tokens + tok_of_row;
       const int32_t orow = live ? tok * a.Hq + g.hk * G + head_of_row : -1;  // below 2^31, checked by the host
       const int64_t prow = static_cast<int64_t>(max(g.part, 0)) * a.part_rows + tile * kRows + row;
@@ -1000,6 +1005,7 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
       for (int q = 0; q < 4; ++q) to[q] = __shfl_sync(0xffffffffu, orow, (lane & ~3) + q);
       const int piece = lane & 3;
       // does the segment have keys hidden from one of the rows?  Then their outputs' sum is looked at for a NaN
+      const int32_t key1 = min(g.kv, g.key0 + g.tiles * Sh::kKeys);
       const bool hides = __any_sync(0xffffffffu, live && (lo > g.key0 || hi < key1));
       float2 odd = make_float2(0.f, 0.f);
 #pragma unroll 1
@@ -1037,9 +1043,10 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
       // a weight of zero times a NaN or an infinity of a hidden key?
       const float sum = odd.x + odd.y;
       const uint32_t again = __ballot_sync(0xffffffffu, live && sum != sum && l == l && (lo > g.key0 || hi < key1));
-      if (again) {
+      if (again != 0 || bad == 1) {
         __syncwarp();  // the rows are written
-        redo_rows<D>(a, again, g.req, g.hk, g.key0, key1, lo, hi, M, inv, orow, g.part >= 0 ? prow - lane : -1);
+        if (redo_rows<D>(a, again, bad == 1, g.req, g.hk, g.key0, key1, lo, hi, M, inv, orow, g.part >= 0 ? prow - lane : -1))
+          l = kNaN;
       }
       if (live) {
         if (g.part >= 0)
