@@ -717,9 +717,10 @@ __global__ void __launch_bounds__(kAdjThreads, 7) adjust_staged(const __grid_con
   };
   if (tid < kWords) mask_word[0][tid] = mask_at(0);
   const Listed ls = listed_of(a, s, i, c);
-  // an entry with its bias's value in the place of its place (a bias of 0 is none)
+  // an entry with its bias's value in the place of its place, and whether there is one
   auto entry = [&](int k) {
     int4 e = __ldcg(ls.list + k);
+    e.w = e.z;
     if (e.z != 0) e.z = __float_as_int(__ldg(a.bias_values + e.z - 1));
     return e;
   };
@@ -775,7 +776,7 @@ __global__ void __launch_bounds__(kAdjThreads, 7) adjust_staged(const __grid_con
         if (!allowed(u)) continue;
         const int32_t n = (e.y & ~(kPromptBit | kDraftBit)) + drafted_before(drafts, e.y, e.x, group + q * a.groups);
         float y = B::value(row[u]);
-        if (adjust_entry(f, n, n > 0 || (e.y & kPromptBit) != 0, e.z != 0, __int_as_float(e.z), y))
+        if (adjust_entry(f, n, n > 0 || (e.y & kPromptBit) != 0, e.w != 0, __int_as_float(e.z), y))
           row[u] = static_cast<T>(B::bits(y));
       }
     }

@@ -391,3 +391,23 @@ def test_adjust_bad_requests_of_a_large_batch():
         _compare(out, c, good, ~mine)
     with pytest.raises(svw.SvwError):
         svw.logits_adjust(c["t"].cuda(), *a, workspace=ws[:need - 1], **kw)
+
+
+@pytest.mark.parametrize("requests", [2, 900])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_adjust_a_bias_of_zero_is_added(requests, dtype):
+    """-0 with a bias of +0 is +0, in small batches, large ones and in place; with
+    a bias of -0, or none, it stays -0."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    V, N = 8200, requests
+    x = torch.full((N, V), -0.0, dtype=torch.bfloat16 if dtype == "bf16" else torch.float32, device="cuda")
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    cu = i32([0] * (N + 1))
+    kw = {"bias_tokens": i32([5, 4097, 8199] * N), "bias_values": torch.tensor([0.0, -0.0, 0.0] * N, device="cuda"),
+          "cu_bias": i32([3 * n for n in range(N + 1)]), "total_draft_rows": 0}
+    assert (svw.logits_adjust_workspace_size(N, V, 0, 0, 3 * N) > 0) == (N > 2)
+    want = torch.zeros_like(x).copysign(x)
+    want[:, [5, 8199]] = 0.0
+    for out in (svw.logits_adjust(x, cu, **kw), svw.logits_adjust(x, cu, out=x, **kw)):
+        assert bool((out == 0).all()) and torch.equal(torch.signbit(out), torch.signbit(want))
