@@ -467,7 +467,8 @@ typedef struct svw_paged_kv {
  * interleaved; elements from rot_dim on are copied, as is all of v.
  *
  *   k, v       device [total_new, n_kv_heads, head_dim], of type dtype as the
- *              cache is; strides of tokens and heads in elements.
+ *              cache is; strides of tokens and heads in elements (those of
+ *              dimensions of one do not count).
  *   q, q_out   device [total_new, n_q_heads, head_dim], q strided like k,
  *              q_out contiguous; both NULL: no queries.  q_out may be q
  *              itself when q is contiguous.

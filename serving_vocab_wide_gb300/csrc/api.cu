@@ -645,6 +645,13 @@ svw_status kv_append(const void *k, int64_t k_token_stride, int64_t k_head_strid
   if (k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 || v_head_stride < 0 || q_token_stride < 0 ||
       q_head_stride < 0)
     return SVW_ERR_INVALID_ARG;
+  // the stride of a dimension of one is never used
+  if (total_new <= 1) {
+    k_token_stride = v_token_stride = 0;
+    q_token_stride = static_cast<int64_t>(n_q_heads) * cache->head_dim;
+  }
+  if (cache->n_kv_heads == 1) k_head_stride = v_head_stride = 0;
+  if (n_q_heads == 1) q_head_stride = cache->head_dim;
   // rotated in place only where every element keeps its place
   if (q && q == q_out &&
       (q_head_stride != cache->head_dim || q_token_stride != static_cast<int64_t>(n_q_heads) * cache->head_dim))

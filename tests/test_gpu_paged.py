@@ -655,3 +655,25 @@ def test_attend_a_bad_page_reaches_the_tokens_that_see_it(new, kv, hq, hkv, d, p
         assert int(status) == svw.SVW_DEV_BAD_INPUT
         assert bool(out[sees].isnan().all()) and bool(lse[sees].isnan().all())
         assert torch.equal(out[~sees], good[0][~sees]) and torch.equal(lse[~sees], good[1][~sees])
+
+
+@pytest.mark.parametrize("T,hq", [(1, 4), (9, 1), (1, 1)])
+def test_append_queries_in_place_where_a_dimension_is_one(T, hq):
+    """A split of one token's projection, or of one head, is contiguous whatever
+    its strides say of that dimension: rotated in place as any other."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    rng = np.random.default_rng(T + hq)
+    d, kv = 64, [30]
+    kc, vc, table = _cache(rng, [T], kv, 1, d, 16, torch.bfloat16)
+    qkv = torch.from_numpy(rng.normal(size=(T, (hq + 2) * d))).to(torch.bfloat16).cuda()
+    k, v = qkv[:, hq * d:(hq + 1) * d].view(T, 1, d), qkv[:, (hq + 1) * d:].view(T, 1, d)
+    q = qkv[:, :hq * d].view(T, hq, d)
+    if T > 1:
+        q = torch.as_strided(q.contiguous(), (T, hq, d), (hq * d, 7, 1))
+    assert q.is_contiguous()
+    cs = torch.from_numpy(rng.normal(size=(40, d)).astype(np.float32)).cuda()
+    where = (_i32(table), _i32(_cu([T])), _i32(kv))
+    want = svw.kv_append(k, v, kc, vc, *where, cos_sin=cs, q=q.clone())
+    out = svw.kv_append(k, v, kc, vc, *where, cos_sin=cs, q=q, q_out=q)
+    assert out is q and torch.equal(out, want)
