@@ -475,10 +475,11 @@ typedef struct svw_paged_kv {
  *   cu_new     device int32 [N+1], cu_new[0] = 0, cu_new[N] = total_new.
  *   cos_sin    device float [max_pos, rot_dim]; NULL with rot_dim = 0: no
  *              rotation.  rot_dim even, <= head_dim <= 1024.
- *   status     SVW_DEV_BAD_INPUT when a token's place is negative or beyond
- *              its block table, its page is not one of the cache's, or its
- *              position is outside [0, max_pos): such a token is not written
- *              (its query, if its position is bad, becomes NaN).
+ *   status     SVW_DEV_BAD_INPUT when a token is in no request's valid range
+ *              of new tokens, its place is negative or beyond its block table,
+ *              its page is not one of the cache's, or its position is outside
+ *              [0, max_pos): such a token is not written (its query, if its
+ *              position is bad, becomes NaN).
  * Two new tokens never share a place; pages shared by requests must not be
  * written.  One kernel launch, no workspace.
  */

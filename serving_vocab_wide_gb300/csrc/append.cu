@@ -68,7 +68,7 @@ __device__ __forceinline__ Place find_place(const AppendArgs &a, int64_t t) {
   after = __shfl_sync(0xffffffffu, after, k);
   len = __shfl_sync(0xffffffffu, len, k);
   Place p;
-  const bool owned = (first >= 0 && first <= t && t < after);  // some request's token
+  const bool owned = (first >= 0 && first <= t && t < after && after <= a.T);  // some request's token
   const int64_t place = static_cast<int64_t>(len) - after + t;
   const int64_t pos = a.positions ? __ldg(a.positions + t) : (owned ? place : -1);
   p.pos_ok = a.rot == 0 || (pos >= 0 && pos < a.max_pos);

@@ -677,3 +677,21 @@ def test_append_queries_in_place_where_a_dimension_is_one(T, hq):
     want = svw.kv_append(k, v, kc, vc, *where, cos_sin=cs, q=q.clone())
     out = svw.kv_append(k, v, kc, vc, *where, cos_sin=cs, q=q, q_out=q)
     assert out is q and torch.equal(out, want)
+
+
+def test_append_a_range_beyond_the_tokens_is_not_written():
+    """A request whose new tokens would end behind the last one given is bad, as it
+    is for paged_attention: none of it is written, the others are."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    rng = np.random.default_rng(5)
+    kc, vc, table = _cache(rng, [3, 5], [20, 20], 2, 64, 16, torch.bfloat16)
+    q, k, v = _append_inputs(rng, [3, 3], 4, 2, 64, torch.bfloat16)
+    k_old = kc.clone()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = svw.kv_append(k, v, kc, vc, _i32(table), _i32([0, 3, 8]), _i32([20, 20]), q=q, status=status)
+    assert int(status) == svw.SVW_DEV_BAD_INPUT and torch.equal(out, q)  # no rotation
+    changed = (kc != k_old) & ~(kc.isnan() & k_old.isnan())
+    rows = {(int(p), int(r)) for p, _, r, _ in changed.nonzero().tolist()}
+    assert rows == {(int(table[0, p // 16]), p % 16) for p in (17, 18, 19)}
+    assert np.array_equal(_dense(kc, table[0], 20)[17:], k[:3].double().cpu().numpy())
