@@ -1093,6 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (base & 1023u) {  // the swizzle atoms need it; never seen
     if (tid == 0 && a.status) atomicOr(a.status, SVW_DEV_TIMEOUT);
+    if (tid < Sh::kWorkers) a.joints[blockIdx.x * Sh::kWorkers + tid].last = -1;  // nothing to join
     return;
   }
   if (tid == 0) {
