@@ -411,3 +411,138 @@ def test_adjust_a_bias_of_zero_is_added(requests, dtype):
     want[:, [5, 8199]] = 0.0
     for out in (svw.logits_adjust(x, cu, **kw), svw.logits_adjust(x, cu, out=x, **kw)):
         assert bool((out == 0).all()) and torch.equal(torch.signbit(out), torch.signbit(want))
+
+
+# ---------------------------------------------------------------------------
+# batches whose lists are counted first
+# ---------------------------------------------------------------------------
+def _large(c):
+    import serving_vocab_wide_gb300 as svw
+    return svw.logits_adjust_workspace_size(len(c["cu"]) - 1, c["V"], int(c["cu"][-1]), len(c["history"]),
+                                            sum(map(len, c["biases"]))) > 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [20000, 20003])
+@pytest.mark.parametrize("pad_in,pad_out,off_in,off_out", [(8, 8, 0, 0), (5, 3, 0, 0), (16, 0, 1, 1), (1, 1, 3, 3), (8, 8, 0, 1)])
+def test_adjust_large_strides_and_alignment(dtype, V, pad_in, pad_out, off_in, off_out):
+    """Rows of any pitch and start, lying alike or differently, apart and in place."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    c = _case(13, [3, 2, 3] * 50, V, dtype, hist=(0, 60))
+    assert _large(c)
+    rows, t = c["rows"], c["t"]
+    ints = torch.int16 if dtype == "bf16" else torch.int32
+    place = lambda pad, at: torch.full((rows * (V + pad) + at + 8,), 77.0, dtype=t.dtype, device="cuda")
+    bi, bo = place(pad_in, off_in), place(pad_out, off_out)
+    x = torch.as_strided(bi, (rows, V), (V + pad_in, 1), off_in)
+    y = torch.as_strided(bo, (rows, V), (V + pad_out, 1), off_out)
+    x.copy_(t)
+    a, kw = _args(c)
+    svw.logits_adjust(x, *a, out=y, **kw)
+    _compare(y, c)
+    assert torch.equal(x.cpu().view(ints), t.view(ints))
+    apart = y.clone()
+    svw.logits_adjust(x, *a, out=x, **kw)
+    assert torch.equal(x.contiguous().view(ints), apart.view(ints))
+    for buf, v in ((bo, y), (bi, x)):
+        v.fill_(77.0)
+        assert bool((buf == 77.0).all()), "nothing outside the rows is written"
+
+
+@pytest.mark.parametrize("dtype,lens,V", [("bf16", [2, 0, 5], 262208), ("fp32", [3, 1], 262209), ("bf16", [4] * 9, 1 << 20)])
+def test_adjust_vocabularies_of_several_ranges(dtype, lens, V):
+    """The lists' bitmap holds 2^18 tokens at a time."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    c = _case(91, lens, V, dtype, hist=(5000, 9000), nbias=40)
+    rng = np.random.default_rng(92)
+    h = rng.integers(0, V, len(c["history"])).astype(np.int32)
+    h[::97] = rng.integers(max(0, V - 200), V, len(h[::97]))  # the last range, and both sides of a boundary
+    h[1::89] = (1 << 18) + rng.integers(-3, 3, len(h[1::89]))
+    c["history"] = h
+    c["tokens"][0] = 1 << 18
+    assert _large(c)
+    a, kw = _args(c)
+    x = c["t"].cuda()
+    out = svw.logits_adjust(x, *a, **kw)
+    _compare(out, c)
+    svw.logits_adjust(x, *a, out=x, **kw)
+    ints = torch.int16 if dtype == "bf16" else torch.int32
+    assert torch.equal(out.view(ints), x.view(ints))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_adjust_large_graph_and_streams(in_place):
+    """The two launches captured and replayed with other logits and histories,
+    and on two streams at once."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    c = _case(43, [3, 5, 0] * 60, 15001, "bf16", hist=(0, 90))
+    assert _large(c)
+    a, kw = _args(c)
+    x = c["t"].cuda()
+    want = svw.logits_adjust(x, *a, **kw)
+    buf = x.clone()
+    out = buf if in_place else torch.zeros_like(x)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        svw.logits_adjust(buf, *a, out=out, **kw)
+    other = x.flip(1).contiguous()
+    history = kw["history"].clone()
+    for n in range(4):
+        src = x if n % 2 == 0 else other
+        kw["history"].copy_(history if n < 2 else history.flip(0))
+        buf.copy_(src)
+        g.replay()
+        fresh = svw.logits_adjust(src, *a, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), fresh.view(torch.int16)), n
+    kw["history"].copy_(history)
+    copies = [x.clone() for _ in range(4)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()] * 2
+    torch.cuda.synchronize()
+    got = [svw.logits_adjust(y, *a, stream=s, out=y if in_place else None, **kw) for y, s in zip(copies, streams)]
+    torch.cuda.synchronize()
+    for y in got:
+        assert torch.equal(y.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_adjust_large_bad_mask_rows_and_nan(in_place):
+    """Mask rows out of range make their rows NaN, and only those; NaN logits
+    vanish where a mask hides them."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    c = _case(35, [2, 3, 1] * 120, 12001, "bf16", hist=(0, 50))
+    assert _large(c)
+    c["t"][:, ::7] = float("nan")
+    c["x"] = c["t"].double().numpy()
+    good = _reference(c)
+    bad = np.zeros(c["rows"], bool)
+    for r, v in ((5, 4), (77, -2), (c["rows"] - 1, 1 << 30)):
+        c["mask_row"][r], bad[r] = v, True
+    a, kw = _args(c)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x = c["t"].cuda()
+    out = svw.logits_adjust(x, *a, status=status, out=x if in_place else None, **kw)
+    assert int(status) == svw.SVW_DEV_BAD_INPUT
+    assert bool(out[torch.from_numpy(bad).cuda()].isnan().all())
+    _compare(out, c, good, ~bad)
+
+
+def test_adjust_large_offsets_beyond_32_bits():
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    V, pitch = 60000, (1 << 24) + 8
+    c = _case(9, [9] * 18, V, "bf16", hist=(0, 100))  # the last rows start beyond 2^31 elements
+    assert _large(c) and (c["rows"] - 1) * pitch > 1 << 31
+    buf = torch.empty((c["rows"] - 1) * pitch + V, dtype=torch.bfloat16, device="cuda")
+    x = torch.as_strided(buf, (c["rows"], V), (pitch, 1))
+    x.copy_(c["t"])
+    a, kw = _args(c)
+    want = _reference(c)
+    _compare(svw.logits_adjust(x, *a, **kw), c, want)
+    svw.logits_adjust(x, *a, out=x, **kw)
+    _compare(x, c, want)

@@ -695,3 +695,37 @@ def test_append_a_range_beyond_the_tokens_is_not_written():
     rows = {(int(p), int(r)) for p, _, r, _ in changed.nonzero().tolist()}
     assert rows == {(int(table[0, p // 16]), p % 16) for p in (17, 18, 19)}
     assert np.array_equal(_dense(kc, table[0], 20)[17:], k[:3].double().cpu().numpy())
+
+
+@pytest.mark.parametrize("new,kv,hq,hkv,d", [
+    ([17] * 6, [700, 1700, 9000, 64, 3000, 17], 8, 2, 128), ([17] * 6, [700, 1700, 9000, 64, 3000, 17], 8, 2, 64),
+    ([300, 40], [3000, 900], 8, 2, 128), ([300, 40], [3000, 900], 8, 2, 64)])
+def test_attend_joined_apart_replays_with_other_keys(new, kv, hq, hkv, d):
+    """The same with the join as a kernel of its own: captured, replayed after the
+    cache has changed, and beside another stream's call."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    rng = np.random.default_rng(26)
+    kc, vc, table = _cache(rng, new, kv, hkv, d, 64, torch.bfloat16)
+    T = sum(new)
+    q = torch.from_numpy(rng.normal(size=(T, hq, d))).to(torch.bfloat16).cuda()
+    args = (q, kc, vc, _i32(table), _i32(_cu(new)), _i32(kv))
+    out, lse = torch.zeros_like(q), torch.zeros(T, hq, device="cuda")
+    ws = torch.empty(svw.paged_attention_workspace_size(T, hq, hkv, d), dtype=torch.uint8, device="cuda")
+    svw.paged_attention(*args, out=out, lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        svw.paged_attention(*args, out=out, lse=lse, workspace=ws)
+    side = torch.cuda.Stream()
+    for n in range(10):
+        vc.mul_(-1)
+        q.mul_(0.9)
+        torch.cuda.synchronize()
+        g.replay()
+        beside = svw.paged_attention(*args, stream=side)
+        want = svw.paged_attention(*args)
+        torch.cuda.synchronize()
+        for o, l in ((out, lse), beside):
+            assert torch.equal(o, want[0]) and torch.equal(l, want[1]), n
+    _compare_attend(new, kv, q, kc, vc, table, {}, out, lse)
