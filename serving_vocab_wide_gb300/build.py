@@ -15,7 +15,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libsvw.so")
 SOURCES = ["api.cu", "verify.cu", "early.cu", "filtered.cu", "opd.cu", "fused.cu", "lengthhead.cu", "noalloc.cu",
            "adjust.cu", "append.cu", "attention.cu"]
-HEADERS = ["svw_device.cuh", "svw_internal.h", "svw_sample.cuh", "opd_common.cuh"]
+HEADERS = ["svw_device.cuh", "svw_internal.h", "steps_internal.h", "svw_sample.cuh", "opd_common.cuh"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

@@ -40,8 +40,8 @@
 #include <cstdint>
 #include <mutex>
 
+#include "steps_internal.h"
 #include "svw_device.cuh"
-#include "svw_internal.h"
 
 namespace svw {
 

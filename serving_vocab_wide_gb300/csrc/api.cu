@@ -9,7 +9,7 @@
 #include <mutex>
 #include <cuda_runtime.h>
 
-#include "svw_internal.h"
+#include "steps_internal.h"
 
 namespace svw {
 bool opd_supported(int64_t V, int esize);

@@ -17,8 +17,8 @@
 
 #include <cstdint>
 
+#include "steps_internal.h"
 #include "svw_device.cuh"
-#include "svw_internal.h"
 
 namespace svw {
 
