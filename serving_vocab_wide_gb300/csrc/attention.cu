@@ -139,7 +139,6 @@ struct Control {
   unsigned long long s_read[2];             // by stage (apart): the scores are in registers
   unsigned long long o_full[2], o_free[2], o_step[2];  // by stage: a segment's outputs; read; each tile's (narrow, apart)
   unsigned long long drain[2];  // by worker: its issuer's products, once a wait has given up
-  unsigned long long meet[2];   // by stage: its softmax warps, about a part (kInside)
   uint32_t tmem;
   int32_t err;
   int32_t complete[2];  // by stage: every part of the unit is there
@@ -716,36 +715,43 @@ __device__ __forceinline__ void join_rows(const AttendArgs &a, const Joint &jt, 
 // may both see them all: they write the same results).  No worker waits for
 // another.  The joiner takes the marks off again, so that a graph that replays
 // a call with its tag finds none.  A mark is 64 bits of the tag and the part's
-// number: what else has been in the workspace does not look like one.  The warps
-// meet at an mbarrier, whose wait ends where a hardware barrier's would not: one
-// of them may have given up a wait and gone.  False: such a warp did not come.
+// number: what else has been in the workspace does not look like one.
+//
+// A warp that has given up a wait must not leave the others at a barrier.  So
+// all four of a stage vote before each part, and once at their end: one that
+// goes votes too, its next barrier being the others' next one, and they go with
+// it.  Behind a vote nothing waits for anything but the four.
+__device__ __forceinline__ bool all_here(int s, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.and.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u), "r"(1 + s), "r"(kRows)
+      : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ unsigned long long mark_of(const AttendArgs &a, int part) {
   return static_cast<unsigned long long>(static_cast<uint32_t>(a.tag)) * 0x9e3779b97f4a7c15ull ^
          static_cast<unsigned long long>(part + 1);
 }
+// false: a warp has gone
 template <int D>
-__device__ __forceinline__ bool mark_and_join(const AttendArgs &a, const Segment &g, int row, unsigned long long *bar,
-                                              int32_t &meetings, int32_t *complete) {
+__device__ __forceinline__ bool mark_and_join(const AttendArgs &a, const Segment &g, int s, int row, int32_t *complete) {
   const Joint jt = {g.last, g.tok0, g.ntok0, g.ntok1, g.hk, {}};
   const int n = g.last - g.first + 1;
-  auto meet = [&] {
-    __syncwarp();
-    if ((row & 31) == 0) mbar_arrive(bar);
-    return warp_wait(bar, par(meetings++));
-  };
   __threadfence();  // this thread's share of the part
-  if (!meet()) return false;
+  if (!all_here(s, true)) return false;
   if (row == 0) {
     *complete = 1;
     *reinterpret_cast<volatile unsigned long long *>(a.marks + g.part) = mark_of(a, g.part);
     __threadfence();
   }
-  if (!meet()) return false;
+  named_sync(1 + s, kRows);
   for (int q = row; q < n; q += kRows) {
     const int part = part_of(g.first, q);
     if (*reinterpret_cast<volatile unsigned long long *>(a.marks + part) != mark_of(a, part)) *complete = 0;
   }
-  if (!meet()) return false;
+  named_sync(1 + s, kRows);
   if (*reinterpret_cast<volatile int32_t *>(complete) == 0) return true;
   __threadfence();
   join_rows<D, 8>(a, jt, g.first, row >> 5, kRows / 32);
@@ -882,8 +888,7 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
   const uint32_t t_o = tmem + lanes + 256 + s * D;
   const float k2 = a.scale * kLog2e;
   int32_t count = 0, k = 0, steps = 0, sc[2] = {0, 0};  // ring tiles, segments, outputs, score tiles by buffer
-  int32_t meetings = 0;
-  bool ok = true;
+  bool ok = true, voted = false;  // voted: the stage's warps have agreed to go
   while (true) {
     const int sl = k % kSegRing;
     if (!(ok = warp_wait(&ln.seg_full[sl], par(k / kSegRing)))) break;
@@ -1063,12 +1068,13 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
     }
     if (kInside && g.part >= 0) {
       if (a.fault == 1 && s == 1 && quad == 3) ok = false;  // test-only: as if this warp's wait had run out
-      if (!ok || !(ok = mark_and_join<D>(a, g, row, &sm.meet[s], meetings, &sm.complete[s]))) break;
+      if (!ok || (voted = !mark_and_join<D>(a, g, s, row, &sm.complete[s]))) break;
     }
     count += 2 * g.tiles;
     steps += g.tiles;
     ++k;
   }
+  if (kInside && !voted) all_here(s, ok);
   if (!ok) {
     tmem_wait_st();  // before another warp frees the columns
     tc_before();
@@ -1120,7 +1126,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.o_free[s], 4);
       mbar_init(&sm.o_step[s], 1);
       mbar_init(&sm.s_read[s], 4);
-      mbar_init(&sm.meet[s], 4);
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&sm.s_full[s], 1);
