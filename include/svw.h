@@ -90,8 +90,9 @@ svw_status svw_device_status(int32_t status_word);
 #define SVW_MAX_LEN 32
 
 /*
- * svw_workspace_size -- one workspace size for every entry point on a batch
- * shape: the largest of svw_verify_workspace_size, svw_verify_early_workspace_size,
+ * svw_workspace_size -- one workspace size for every entry point that verifies
+ * or distils a batch shape (the steps before a verification, logits_adjust and
+ * paged_attention, have their own): the largest of svw_verify_workspace_size, svw_verify_early_workspace_size,
  * svw_verify_filtered_workspace_size (both dtypes), svw_opd_workspace_size and
  * svw_verify_opd_workspace_size for (n_requests, total_draft_rows, V), so
  * that a caller can size one buffer before it knows which call or dtype it
@@ -414,7 +415,8 @@ svw_status length_head_label(const int32_t *accept_len, const int32_t *cu_draft,
  *                  initialised; not preserved; or NULL.  With it the lists of
  *                  a large batch are counted once per request instead of once
  *                  per 4096 entries of its vocabulary; the results are the
- *                  same.
+ *                  same.  (Where offsets run backwards, requests that begin
+ *                  inside an earlier one's lists are bad too with it.)
  */
 size_t svw_logits_adjust_workspace_size(int32_t n_requests, int32_t V, int64_t total_draft_rows, int64_t total_history,
                                         int64_t total_bias);

@@ -19,15 +19,16 @@
 //
 // Large batches (given a workspace), 225 us on the benchmark batch (6.0 TB/s):
 //   adjust_lists   a CTA per request lists its distinct tokens, ascending, with
-//                  their counts (16 us for 8192, partly beside the rows' first
-//                  loads);
+//                  their counts (15 to 17 us by itself where the longest
+//                  history has 8192, partly beside the rows' first loads);
 //   adjust_staged  a CTA per chunk of 8 KB of a request's rows: they pass
 //                  through shared memory by bulk copies, masked and adjusted on
 //                  the way; seven CTAs of three 8 KB stages per SM (four stages
 //                  and five CTAs: 240 us; the rows in registers and the listed
 //                  entries by a second trip to memory: 329);
-//   adjust_rows    in place, 93 us without masks and 264 with (only what
-//                  changes is written), or rows that do not lie alike.
+//   adjust_rows    in place, 92 us without masks and 258 with (only what
+//                  changes is written; a vector's load waits for its mask
+//                  word), or rows that do not lie alike.
 // Small batches, one launch: adjust_chunks, a CTA counts the tokens of its chunk
 // itself by reading the whole history (4.1 us for one row of 32000; on the
 // benchmark batch: 329, each of 38 chunks of a request waits for its loads.
@@ -472,8 +473,9 @@ __host__ __device__ constexpr int list_bytes(int V, bool bias) {
 // places: a bitmap of them in shared memory; a token's rank (the words' running
 // counts and the bits below its own) is its place in the list and, less the
 // window's start, in the arrays of tokens and counts.  (A hash table of the same
-// tokens took 52 us for 8182 of them, 4.5 thousand distinct, in its probes;
-// writing the list from the bitmap's words, 5 us of 16.)
+// tokens took 52 us for 8182 of them, 4.5 thousand distinct, in its probes.  With
+// the list written from the bitmap's words, not by rank, the benchmark batch in
+// place took 97 us where it takes 92.)
 __global__ void __launch_bounds__(kListThreads, 2) adjust_lists(const __grid_constant__ AdjustArgs a) {
   extern __shared__ int32_t dyn[];
   const int words = list_words(a.V);

@@ -44,8 +44,10 @@
 //           heads of 64, two prompts over 4381 keys: 187 -> 177 us).
 // Measured (us; 32 query heads, 8 key heads of 128; of 6.78 TB/s and 1898
 // TFLOP/s): 64 decoding requests over 1000 to 16000 keys 209 (98%); 2220 new
-// tokens of 256 requests over 512 to 8192 keys 447 (95%); 17 tokens over 131000
-// keys 95 (83%); two prompts of 2048 over 8192 keys 374 (1654 TFLOP/s, 87%).
+// tokens of 256 requests over 512 to 8192 keys 448 (95%); 17 tokens over 131000
+// keys 95 (83%); two prompts of 2048 over 8192 keys 371 to 391 in short runs
+// (1580 to 1670 TFLOP/s, 83 to 88%) and 417 to 432 in long ones, at the power
+// limit (75 to 78%).
 // The reference: exp2(x - M) is exact algebra for any M, so M follows the
 // row's maximum only when that has outgrown it by more than 8 (a factor 256:
 // far from overflow, and the same relative rounding of P); only then are l
@@ -1380,8 +1382,10 @@ cudaError_t launch_attention(const AttendArgs &args, cudaStream_t st) {
   // more would read the keys once per tile in the narrow form.
   const bool wide = a.T * G > static_cast<int64_t>(kRows) * a.N;
   // A short call of few tokens: joined by the last worker.  (The launch that this
-  // saves is 6 us of the host's time; on the GPU the join costs 1.2 us more there,
-  // one warpgroup's, than as a kernel of its own: 13.0 against 11.8 for one token.)
+  // saves is 6 us of the host's time.  On the GPU, against a kernel of its own, 32
+  // query heads of 128 on 8 key heads: one token over 777 keys 12.5 and 12.9 us,
+  // over 60000 48.6 and 50.0, 32 tokens over 4000 88.2 and 87.8; with 64 on 4, so
+  // that one warpgroup joins 16 rows of many parts, 4 tokens over 2000 21.6 and 16.6.)
   const bool inside = !wide && a.T <= 32 && a.T * G <= 16 * static_cast<int64_t>(a.N);
   if (a.D == 128)
     return wide ? launch<128, true, false>(a, st) : inside ? launch<128, false, true>(a, st) : launch<128, false, false>(a, st);
