@@ -1,4 +1,4 @@
-"""A bounded wait of the round's operators runs out, without a GPU fault: the
+"""A bounded wait of a verification round's steps runs out, without a GPU fault: the
 call returns, the status word says so, and the same call afterwards gives the
 bits it gave before (svw_set_fault and svw_set_wait_limit, as in
 test_gpu_timeout)."""

@@ -1,4 +1,4 @@
-"""What the Python calls of the round's operators do on the host, with stand-ins
+"""What the Python calls of a verification round do on the host, with stand-ins
 for the GPU's tensors and streams: where memory is taken, on which device they
 launch, what they hand to the library."""
 import contextlib
