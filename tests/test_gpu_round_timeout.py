@@ -42,8 +42,8 @@ def test_attend_values_do_not_come(new, kv, d):
 
 @pytest.mark.parametrize("new,kv,d", [([1], [20000], 128), ([1] * 5, [700, 1, 9000, 64, 30000], 64)])
 def test_attend_a_warp_does_not_come_to_the_join(new, kv, d):
-    """Where the last worker joins, a warp that has given up leaves the other
-    three of its worker waiting: their wait runs out as well."""
+    """Where the last worker joins, a warp that has given up does not leave the
+    other three of its worker at a barrier: they go with it."""
     import serving_vocab_wide_gb300 as svw
     args = _attend_inputs(new, kv, 8, 2, d)
     _assert_recovered(*_run_three(lambda st: _fp32(svw.paged_attention(*args, status=st))))
