@@ -602,8 +602,9 @@ svw_status svw_time_next_launch(const char *kernel, void *begin_event, void *end
  * (logits_adjust, a large batch out of place); every second worker of
  * paged_attention loads no values, so that the waits for its outputs run out
  * behind its scores, and in a call of few tokens one warp of the other workers
- * leaves before a part is marked, as if a wait of its own had run out.  The call returns, its status word holds SVW_DEV_TIMEOUT, and the results of
- * the affected rows are void.  Other values: SVW_ERR_INVALID_ARG.  Host-side
+ * leaves before a part is marked, as if a wait of its own had run out.  The
+ * call returns, its status word holds SVW_DEV_TIMEOUT, and the results of the
+ * affected rows are void.  Other values: SVW_ERR_INVALID_ARG.  Host-side
  * state, shared by all threads.
  */
 svw_status svw_set_wait_limit(int64_t cycles);
