@@ -8,7 +8,8 @@
  * spec_verify_filtered: top-k / top-p filtered distributions), plus the
  * adaptive length head that sets the next round's verified lengths
  * (length_head, length_head_label), and the steps of a round that precede the
- * verification (kv_append, paged_attention, logits_adjust):
+ * verification (kv_append, paged_attention, logits_adjust; kv_append_norm,
+ * paged_attention_fp8 and kv_gather with a cache of 8 bits):
  *
  *  spec_verify  batched speculative verification of a ragged batch.  Defined
  *               by "DFlash 阅读笔记：并行起草、目标特征与精确验证" §5.1 (greedy
@@ -41,7 +42,7 @@
  *    vectorised / bulk-copy path; any other shape takes a scalar path with the
  *    same results.
  *  - Inputs are read-only; outputs must not alias inputs, except where an
- *    entry point says so (logits_adjust, kv_append's queries).
+ *    entry point says so (logits_adjust, kv_append's and kv_append_norm's queries).
  */
 #ifndef SVW_H_
 #define SVW_H_
@@ -65,7 +66,9 @@ typedef enum svw_status {
   SVW_ERR_TIMEOUT = 7      /* device-detected: see svw_device_status()               */
 } svw_status;
 
-typedef enum svw_dtype { SVW_F32 = 0, SVW_BF16 = 1 } svw_dtype;
+/* SVW_E4M3: 8-bit floats (4 bits of exponent, 3 of mantissa, largest 448, no
+ * infinity), the type of a cache where an entry point says so. */
+typedef enum svw_dtype { SVW_F32 = 0, SVW_BF16 = 1, SVW_E4M3 = 2 } svw_dtype;
 
 /*
  * Bits OR-ed into the device status word.  The word is a bit set, not an
@@ -493,6 +496,59 @@ svw_status kv_append(const void *k, int64_t k_token_stride, int64_t k_head_strid
                      const svw_paged_kv *cache, int32_t *status, void *stream);
 
 /*
+ * kv_append_norm -- kv_append with a norm of each head of keys and queries
+ * ahead of the rotation, into a cache of the new tokens' type or of 8 bits.
+ *
+ * In fp32, for each head x of a token's keys (queries likewise, with q_weight):
+ *   y_e = x_e k_weight_e / sqrt(mean_e x_e^2 + eps)       (k_weight NULL: y = x)
+ * its pairs rotated as kv_append's are.  Into a cache of SVW_E4M3 a key of head
+ * h is written as the code nearest to y / k_scale[h], a value as the one nearest
+ * to v / v_scale[h] (ties to even; beyond +-448, infinities too: +-448; NaN:
+ * NaN), so that code x scale stands for it; into a cache of dtype as it is.
+ * Rounded once.
+ *
+ * Arguments and results as for kv_append, except:
+ *   k_weight, q_weight  device float [head_dim]; NULL: no norm.  q_weight needs q.
+ *   eps          finite, >= 0.
+ *   cache_dtype  dtype or SVW_E4M3.  The cache's strides count its elements.
+ *   k_scale, v_scale  device float [n_kv_heads], normal numbers > 0, of an e4m3
+ *                cache only; NULL: 1.  Another number: that head's codes are
+ *                NaN, and SVW_DEV_BAD_INPUT.
+ */
+svw_status kv_append_norm(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                          int64_t v_token_stride, int64_t v_head_stride, const void *q, int64_t q_token_stride,
+                          int64_t q_head_stride, void *q_out, svw_dtype dtype, int32_t n_q_heads, int32_t N,
+                          const int32_t *cu_new, int64_t total_new, const int32_t *kv_len, const int32_t *positions,
+                          const float *k_weight, const float *q_weight, float eps, const float *cos_sin,
+                          int64_t max_pos, int32_t rot_dim, int32_t interleaved, const svw_paged_kv *cache,
+                          svw_dtype cache_dtype, const float *k_scale, const float *v_scale, int32_t *status,
+                          void *stream);
+
+/*
+ * kv_gather -- cached keys and values read back, packed: what a request keeps
+ * when it leaves for another cache, or what a drafter reads of it.
+ *
+ * Output token t of request i (0 <= t < cu_out[i+1] - cu_out[i]) is its cached
+ * token first[i] + t, in fp32 code x scale of its head (an e4m3 cache), rounded
+ * once to out_dtype.
+ *
+ *   cache        of cache_dtype (any svw_dtype); head_dim <= 1024.
+ *   k_scale, v_scale  as for kv_append_norm.
+ *   cu_out       device int32 [N+1], cu_out[0] = 0, cu_out[N] = total_out.
+ *   first        device int32 [N], >= 0; NULL: 0.
+ *   k_out, v_out device [total_out, n_kv_heads, head_dim] of out_dtype (SVW_F32
+ *                or SVW_BF16), contiguous; one of them may be NULL.
+ *   status       SVW_DEV_BAD_INPUT when a token is in no request's valid range,
+ *                lies before place 0 or beyond its block table, or its page is
+ *                not one of the cache's (the token becomes NaN), or a scale is
+ *                not a normal number > 0 (that head becomes NaN).
+ * One kernel launch, no workspace.
+ */
+svw_status kv_gather(const svw_paged_kv *cache, svw_dtype cache_dtype, const float *k_scale, const float *v_scale,
+                     int32_t N, const int32_t *cu_out, int64_t total_out, const int32_t *first, void *k_out,
+                     void *v_out, svw_dtype out_dtype, int32_t *status, void *stream);
+
+/*
  * paged_attention -- attention of each request's new tokens over its cached
  * keys (the new tokens' own ones included, as kv_append leaves them).
  *
@@ -536,6 +592,30 @@ svw_status paged_attention(const void *q, int64_t q_token_stride, int64_t q_head
                            size_t workspace_bytes, void *stream);
 
 /*
+ * paged_attention_fp8 -- paged_attention over a cache of SVW_E4M3, as
+ * kv_append_norm leaves it: with K and V the codes,
+ *   s_j = scale k_scale[hk] q . K_j,  out = v_scale[hk] sum_j softmax_j(s) V_j,
+ *   lse = log sum_j exp(s_j).
+ *
+ * Arguments, results and workspace size as for paged_attention, except:
+ *   cache        codes of one byte; caches 16-byte aligned, strides positive
+ *                multiples of 16.
+ *   k_scale, v_scale  device float [n_kv_heads], normal numbers > 0; NULL: 1.
+ *                Another number: the query heads of that key head become NaN,
+ *                and SVW_DEV_BAD_INPUT.
+ * A query with a NaN or an infinity becomes NaN throughout.  Scores and sums are
+ * fp32; a query enters its products as two e4m3 numbers under a scale of its
+ * own, which is exact down to 2^-10 of its largest element (and within 2^-17 of
+ * that one below), and the weights as two, which is as near as bf16 down to 2^-7
+ * of the largest (and within 2^-15 of that one below).
+ */
+svw_status paged_attention_fp8(const void *q, int64_t q_token_stride, int64_t q_head_stride, svw_dtype dtype,
+                               int32_t n_q_heads, int32_t N, const int32_t *cu_new, int64_t total_new,
+                               const int32_t *kv_len, const svw_paged_kv *cache, const float *k_scale,
+                               const float *v_scale, float scale, int32_t causal, int32_t window, void *out,
+                               float *lse, int32_t *status, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * spec_verify_noalloc -- spec_verify for callers that cannot allocate device
  * memory.  No counterpart on the pages: it exists only because some callers
  * have no allocator to hand over a workspace (a plain C serving loop, a
@@ -576,7 +656,8 @@ svw_status spec_verify_noalloc(const void *target_logits, const void *draft_logi
  * "verify_finalize", "verify_early_cluster", "filter_rows", "filtered_finalize",
  * "opd_fast_kernel", "opd_fix_parts", "opd_fix_grad", "opd_exact_kernel",
  * "fused_finalize", "length_head_mma", "length_head_final", "adjust_lists",
- * "logits_adjust", "kv_append", "paged_attention", "attention_join") records
+ * "logits_adjust", "kv_append", "kv_append_norm", "kv_gather", "paged_attention", "paged_attention_fp8",
+ * "attention_join") records
  * begin_event just before it and end_event just after it on the launch stream (cudaEvent_t handles passed as void*, owned
  * by the caller).  kernel = NULL disarms.  The library records nothing
  * unless armed.  Lets a benchmark time one kernel of a multi-kernel call with

@@ -21,6 +21,7 @@ from .build import LIB_PATH, build  # noqa: F401
 
 SVW_F32 = 0
 SVW_BF16 = 1
+SVW_E4M3 = 2
 SVW_DEV_BAD_INPUT = 1
 SVW_DEV_TIMEOUT = 2
 SVW_ERR_BAD_INPUT = 6
@@ -102,11 +103,19 @@ def lib():
             L.kv_append.argtypes = [P, I64, I64, P, I64, I64, P, I64, I64, P, ctypes.c_int, I32, I32, P, I64, P,
                                     P, P, I64, I32, I32, P, P, P]
             L.kv_append.restype = ctypes.c_int
+            L.kv_append_norm.argtypes = [P, I64, I64, P, I64, I64, P, I64, I64, P, ctypes.c_int, I32, I32, P, I64, P,
+                                         P, P, P, F, P, I64, I32, I32, P, ctypes.c_int, P, P, P, P]
+            L.kv_append_norm.restype = ctypes.c_int
+            L.kv_gather.argtypes = [P, ctypes.c_int, P, P, I32, P, I64, P, P, P, ctypes.c_int, P, P]
+            L.kv_gather.restype = ctypes.c_int
             L.svw_paged_attention_workspace_size.argtypes = [I64, I32, I32, I32]
             L.svw_paged_attention_workspace_size.restype = SZ
             L.paged_attention.argtypes = [P, I64, I64, ctypes.c_int, I32, I32, P, I64, P, P, F, I32, I32, P, P, P,
                                           P, SZ, P]
             L.paged_attention.restype = ctypes.c_int
+            L.paged_attention_fp8.argtypes = [P, I64, I64, ctypes.c_int, I32, I32, P, I64, P, P, P, P, F, I32, I32, P,
+                                              P, P, P, SZ, P]
+            L.paged_attention_fp8.restype = ctypes.c_int
             L.svw_time_next_launch.argtypes = [ctypes.c_char_p, P, P]
             L.svw_time_next_launch.restype = ctypes.c_int
             L.svw_set_wait_limit.argtypes = [I64]
@@ -729,6 +738,188 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, *, scale: 
                                kv_len.data_ptr(), cache, float(dim ** -0.5 if scale is None else scale),
                                1 if causal else 0, int(window), out.data_ptr(), _addr(lse), _addr(status),
                                workspace.data_ptr(), workspace.numel(), _stream_of(stream, gpu))
+    if rc:
+        _check(rc)
+    return out, lse
+
+
+@functools.lru_cache(maxsize=None)
+def _codes():
+    """The codes of the types that a cache may have."""
+    import torch
+    return {torch.float32: SVW_F32, torch.bfloat16: SVW_BF16, torch.float8_e4m3fn: SVW_E4M3}
+
+
+def _cache_code(dtype):
+    code = _codes().get(dtype)
+    if code is None:
+        raise SvwError(f"the caches must be float32, bfloat16 or float8_e4m3fn, got {dtype}")
+    return code
+
+
+def _scales(k_scale, v_scale, heads, code, gpu):
+    """k_scale and v_scale are per-head factors of a cache of 8 bits (None: 1)."""
+    if k_scale is None and v_scale is None:
+        return
+    if code != SVW_E4M3:
+        raise SvwError("k_scale and v_scale come with float8_e4m3fn caches")
+    _need_like(gpu, _torch().float32, ("k_scale", "v_scale"), (k_scale, v_scale))
+    if (k_scale is not None and k_scale.numel() != heads) or (v_scale is not None and v_scale.numel() != heads):
+        raise SvwError(f"k_scale and v_scale must have {heads} elements")
+
+
+def kv_append_norm(k, v, k_cache, v_cache, block_table, cu_new, kv_len, *, k_weight=None, q_weight=None,
+                   eps: float = 1e-6, k_scale=None, v_scale=None, cos_sin=None, interleaved: bool = False,
+                   positions=None, q=None, q_out=None, status=None, stream=None):
+    """kv_append with an RMS norm of each head of keys and queries ahead of the
+    rotation, into caches of k's type or of float8_e4m3fn.  Returns the queries,
+    normed and rotated (None without q).
+
+    Arguments as for kv_append, and: k_weight, q_weight: float32 [head_dim]
+    (None: no norm); k_scale, v_scale: float32 [heads] of float8_e4m3fn caches, in
+    which x / scale is written (None: 1).
+    """
+    torch = _torch()
+    i32, f32 = torch.int32, torch.float32
+    N = cu_new.numel() - 1
+    cache, gpu, shape = _paged(k_cache, v_cache, block_table, N)
+    _need_current(stream, gpu)
+    heads, dim, dtype, code = shape[1], shape[3], k.dtype, _cache_code(k_cache.dtype)
+    if code != SVW_E4M3 and dtype is not k_cache.dtype:
+        raise SvwError("the caches must be of k's type or float8_e4m3fn")
+    kh, ks = _heads("k", k, dim, dtype, gpu)
+    vh, vs = _heads("v", v, dim, dtype, gpu)
+    T = kh[0]
+    if kh[1] != heads or vh != kh:
+        raise SvwError("k and v must have the cache's heads and one length")
+    if _off(cu_new, i32, gpu) or _off(kv_len, i32, gpu) or _off(positions, i32, gpu) or _off(status, i32, gpu):
+        _need_like(gpu, i32, ("cu_new", "kv_len", "positions", "status"), (cu_new, kv_len, positions, status))
+    if kv_len.numel() != N:
+        raise SvwError(f"kv_len must have {N} elements")
+    if positions is not None and positions.numel() != T:
+        raise SvwError(f"positions must have {T} elements")
+    if _off(k_weight, f32, gpu) or _off(q_weight, f32, gpu):
+        _need_like(gpu, f32, ("k_weight", "q_weight"), (k_weight, q_weight))
+    if (k_weight is not None and k_weight.numel() != dim) or (q_weight is not None and q_weight.numel() != dim):
+        raise SvwError(f"k_weight and q_weight must have {dim} elements")
+    _scales(k_scale, v_scale, heads, code, gpu)
+    max_pos = rot = 0
+    if cos_sin is not None:
+        if _off(cos_sin, f32, gpu) or cos_sin.dim() != 2:
+            raise SvwError(f"cos_sin must be a contiguous float32 [max_pos, rot_dim] tensor on cuda:{gpu}")
+        max_pos, rot = cos_sin.shape
+    hq, qs = 0, (0, 0)
+    if q is not None:
+        qh, qs = _heads("q", q, dim, dtype, gpu)
+        hq = qh[1]
+        if qh[0] != T:
+            raise SvwError("q must have as many tokens as k")
+        if q_out is None:
+            q_out = _empty(stream, gpu, qh, dtype, q.device)
+        elif _off(q_out, dtype, gpu) or q_out.shape != qh:
+            raise SvwError("q_out must be like q, contiguous")
+    elif q_out is not None or q_weight is not None:
+        raise SvwError("q_out and q_weight come with q")
+    rc = lib().kv_append_norm(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _addr(q), qs[0], qs[1],
+                              _addr(q_out), _dtype_code(k), hq, N, cu_new.data_ptr(), T, kv_len.data_ptr(),
+                              _addr(positions), _addr(k_weight), _addr(q_weight), eps, _addr(cos_sin), max_pos, rot,
+                              1 if interleaved else 0, cache, code, _addr(k_scale), _addr(v_scale), _addr(status),
+                              _stream_of(stream, gpu))
+    if rc:
+        _check(rc)
+    return q_out
+
+
+def kv_gather(k_cache, v_cache, block_table, cu_out, *, first=None, k_scale=None, v_scale=None,
+              total_out: int | None = None, dtype=None, k_out=None, v_out=None, status=None, stream=None):
+    """Cached keys and values read back, packed.  Returns (k, v): [total_out,
+    heads, head_dim] of `dtype` (bfloat16 or float32; bfloat16 by default).
+
+    The caches, of float32, bfloat16 or float8_e4m3fn with k_scale and v_scale, and
+    block_table as for kv_append_norm; cu_out: int32 [N + 1] offsets of the
+    requests' tokens in the outputs; first: int32 [N], the place of each request's
+    first one (None: 0).  `total_out` (= cu_out[-1]) may be passed to avoid a
+    device read, as the outputs may be.
+    """
+    torch = _torch()
+    i32 = torch.int32
+    N = cu_out.numel() - 1
+    cache, gpu, shape = _paged(k_cache, v_cache, block_table, N)
+    _need_current(stream, gpu)
+    code = _cache_code(k_cache.dtype)
+    if _off(cu_out, i32, gpu) or _off(first, i32, gpu) or _off(status, i32, gpu):
+        _need_like(gpu, i32, ("cu_out", "first", "status"), (cu_out, first, status))
+    if first is not None and first.numel() != N:
+        raise SvwError(f"first must have {N} elements")
+    _scales(k_scale, v_scale, shape[1], code, gpu)
+    given = k_out if k_out is not None else v_out
+    if total_out is None:
+        total_out = int(cu_out[-1].item()) if given is None else given.shape[0]
+    if dtype is None:
+        dtype = torch.bfloat16 if given is None else given.dtype
+    out_code = _cache_code(dtype)
+    if out_code == SVW_E4M3:
+        raise SvwError("k_out and v_out must be bfloat16 or float32")
+    want = (total_out, shape[1], shape[3])
+    if k_out is None:
+        k_out = _empty(stream, gpu, want, dtype, k_cache.device)
+    elif _off(k_out, dtype, gpu) or k_out.shape != want:
+        raise SvwError(f"k_out must be a contiguous {dtype} tensor of {want} on cuda:{gpu}")
+    if v_out is None:
+        v_out = _empty(stream, gpu, want, dtype, k_cache.device)
+    elif _off(v_out, dtype, gpu) or v_out.shape != want:
+        raise SvwError(f"v_out must be a contiguous {dtype} tensor of {want} on cuda:{gpu}")
+    rc = lib().kv_gather(cache, code, _addr(k_scale), _addr(v_scale), N, cu_out.data_ptr(), total_out, _addr(first),
+                         k_out.data_ptr(), v_out.data_ptr(), out_code, _addr(status), _stream_of(stream, gpu))
+    if rc:
+        _check(rc)
+    return k_out, v_out
+
+
+def paged_attention_fp8(q, k_cache, v_cache, block_table, cu_new, kv_len, *, k_scale=None, v_scale=None,
+                        scale: float | None = None, causal: bool = True, window: int = 0, out=None, lse=None,
+                        want_lse: bool = True, status=None, workspace=None, stream=None):
+    """paged_attention over float8_e4m3fn caches, as kv_append_norm leaves them.
+    Returns (out, lse).
+
+    Arguments as for paged_attention, and k_scale, v_scale: float32 [heads], by
+    which a head's codes are multiplied (None: 1).  The workspace is
+    paged_attention's.
+    """
+    torch = _torch()
+    i32, bf16 = torch.int32, torch.bfloat16
+    N = cu_new.numel() - 1
+    cache, gpu, shape = _paged(k_cache, v_cache, block_table, N)
+    _need_current(stream, gpu)
+    heads, dim = shape[1], shape[3]
+    if k_cache.dtype is not torch.float8_e4m3fn:
+        raise SvwError(f"the caches must be float8_e4m3fn, got {k_cache.dtype}")
+    qh, qs = _heads("q", q, dim, bf16, gpu)
+    T, hq, _ = qh
+    if _off(cu_new, i32, gpu) or _off(kv_len, i32, gpu) or _off(status, i32, gpu):
+        _need_like(gpu, i32, ("cu_new", "kv_len", "status"), (cu_new, kv_len, status))
+    if kv_len.numel() != N:
+        raise SvwError(f"kv_len must have {N} elements")
+    _scales(k_scale, v_scale, heads, SVW_E4M3, gpu)
+    if out is None:
+        out = _empty(stream, gpu, qh, bf16, q.device)
+    elif _off(out, bf16, gpu) or out.shape != qh:
+        raise SvwError("out must be like q, contiguous")
+    if lse is None:
+        if want_lse:
+            lse = _empty(stream, gpu, (T, hq), torch.float32, q.device)
+    elif _off(lse, torch.float32, gpu) or lse.numel() != T * hq:
+        raise SvwError(f"lse must be a contiguous float32 [{T}, {hq}] tensor on cuda:{gpu}")
+    if workspace is None:
+        need = paged_attention_workspace_size(T, hq, heads, dim)
+        workspace = _empty(stream, gpu, max(1, need), torch.uint8, q.device, returned=False)
+    elif _off(workspace, torch.uint8, gpu):
+        raise SvwError(f"workspace must be a contiguous uint8 tensor on cuda:{gpu}")
+    rc = lib().paged_attention_fp8(q.data_ptr(), qs[0], qs[1], SVW_BF16, hq, N, cu_new.data_ptr(), T,
+                                   kv_len.data_ptr(), cache, _addr(k_scale), _addr(v_scale),
+                                   float(dim ** -0.5 if scale is None else scale), 1 if causal else 0, int(window),
+                                   out.data_ptr(), _addr(lse), _addr(status), workspace.data_ptr(), workspace.numel(),
+                                   _stream_of(stream, gpu))
     if rc:
         _check(rc)
     return out, lse

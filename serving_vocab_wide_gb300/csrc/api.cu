@@ -22,7 +22,7 @@ constexpr int64_t kMaxHeadPositions = 1 << 20;  // length head: N k (32-bit offs
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-int esize_of(svw_dtype d) { return d == SVW_BF16 ? 2 : 4; }
+int esize_of(svw_dtype d) { return d == SVW_E4M3 ? 1 : d == SVW_BF16 ? 2 : 4; }
 
 }  // namespace
 
@@ -612,7 +612,7 @@ svw_status logits_adjust(const void *logits, int64_t logits_stride, svw_dtype dt
   return svw::launch_adjust(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SVW_OK : SVW_ERR_CUDA;
 }
 
-// the cache's own fields, checked once for both of its calls
+// the cache's own fields, checked once for all of its calls
 static svw_status check_cache(const svw_paged_kv *c) {
   if (!c || !c->k || !c->v || !c->block_table) return SVW_ERR_INVALID_ARG;
   if (c->n_pages <= 0 || c->page_size <= 0 || c->max_pages <= 0 || c->n_kv_heads <= 0 || c->head_dim <= 0 ||
@@ -624,17 +624,20 @@ static svw_status check_cache(const svw_paged_kv *c) {
   return SVW_OK;
 }
 
-svw_status kv_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
-                     int64_t v_token_stride, int64_t v_head_stride, const void *q, int64_t q_token_stride,
-                     int64_t q_head_stride, void *q_out, svw_dtype dtype, int32_t n_q_heads, int32_t N,
-                     const int32_t *cu_new, int64_t total_new, const int32_t *kv_len, const int32_t *positions,
-                     const float *cos_sin, int64_t max_pos, int32_t rot_dim, int32_t interleaved,
-                     const svw_paged_kv *cache, int32_t *status, void *stream) {
-  if (dtype != SVW_F32 && dtype != SVW_BF16) return SVW_ERR_UNSUPPORTED;
+// what kv_append and kv_append_norm take alike, checked and in the kernels' form
+static svw_status append_args(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                              int64_t v_token_stride, int64_t v_head_stride, const void *q, int64_t q_token_stride,
+                              int64_t q_head_stride, void *q_out, svw_dtype dtype, int32_t n_q_heads, int32_t N,
+                              const int32_t *cu_new, int64_t total_new, const int32_t *kv_len,
+                              const int32_t *positions, const float *cos_sin, int64_t max_pos, int32_t rot_dim,
+                              int32_t interleaved, const svw_paged_kv *cache, svw_dtype cache_dtype, int32_t *status,
+                              svw::AppendArgs &a) {
+  if ((dtype != SVW_F32 && dtype != SVW_BF16) || (cache_dtype != dtype && cache_dtype != SVW_E4M3))
+    return SVW_ERR_UNSUPPORTED;
   if (N <= 0 || total_new < 0 || n_q_heads < 0) return SVW_ERR_INVALID_ARG;
   const svw_status cs = check_cache(cache);
   if (cs != SVW_OK) return cs;
-  const int es = esize_of(dtype);
+  const int es = esize_of(dtype), ces = esize_of(cache_dtype);
   if (cache->head_dim > 1024 || total_new > INT32_MAX || n_q_heads > 4096 || cache->n_kv_heads > 4096)
     return SVW_ERR_UNSUPPORTED;
   if (!cu_new || !kv_len || (total_new > 0 && (!k || !v)) || (q == nullptr) != (q_out == nullptr))
@@ -656,12 +659,10 @@ svw_status kv_append(const void *k, int64_t k_token_stride, int64_t k_head_strid
   if (q && q == q_out &&
       (q_head_stride != cache->head_dim || q_token_stride != static_cast<int64_t>(n_q_heads) * cache->head_dim))
     return SVW_ERR_INVALID_ARG;
-  if (!aligned(k, es) || !aligned(v, es) || !aligned(q, es) || !aligned(q_out, es) || !aligned(cache->k, es) ||
-      !aligned(cache->v, es) || !aligned(cu_new, 4) || !aligned(kv_len, 4) || !aligned(positions, 4) ||
+  if (!aligned(k, es) || !aligned(v, es) || !aligned(q, es) || !aligned(q_out, es) || !aligned(cache->k, ces) ||
+      !aligned(cache->v, ces) || !aligned(cu_new, 4) || !aligned(kv_len, 4) || !aligned(positions, 4) ||
       !aligned(cos_sin, 4) || !aligned(status, 4))
     return SVW_ERR_MISALIGNED;
-  if (total_new == 0) return SVW_OK;
-  svw::AppendArgs a{};
   a.k = k;
   a.v = v;
   a.q = q;
@@ -696,7 +697,93 @@ svw_status kv_append(const void *k, int64_t k_token_stride, int64_t k_head_strid
   a.n_pages = cache->n_pages;
   a.page_size = cache->page_size;
   a.status = status;
+  return SVW_OK;
+}
+
+svw_status kv_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                     int64_t v_token_stride, int64_t v_head_stride, const void *q, int64_t q_token_stride,
+                     int64_t q_head_stride, void *q_out, svw_dtype dtype, int32_t n_q_heads, int32_t N,
+                     const int32_t *cu_new, int64_t total_new, const int32_t *kv_len, const int32_t *positions,
+                     const float *cos_sin, int64_t max_pos, int32_t rot_dim, int32_t interleaved,
+                     const svw_paged_kv *cache, int32_t *status, void *stream) {
+  svw::AppendArgs a{};
+  const svw_status s = append_args(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, q,
+                                   q_token_stride, q_head_stride, q_out, dtype, n_q_heads, N, cu_new, total_new,
+                                   kv_len, positions, cos_sin, max_pos, rot_dim, interleaved, cache, dtype, status, a);
+  if (s != SVW_OK || total_new == 0) return s;
   return svw::launch_append(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SVW_OK : SVW_ERR_CUDA;
+}
+
+svw_status kv_append_norm(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                          int64_t v_token_stride, int64_t v_head_stride, const void *q, int64_t q_token_stride,
+                          int64_t q_head_stride, void *q_out, svw_dtype dtype, int32_t n_q_heads, int32_t N,
+                          const int32_t *cu_new, int64_t total_new, const int32_t *kv_len, const int32_t *positions,
+                          const float *k_weight, const float *q_weight, float eps, const float *cos_sin,
+                          int64_t max_pos, int32_t rot_dim, int32_t interleaved, const svw_paged_kv *cache,
+                          svw_dtype cache_dtype, const float *k_scale, const float *v_scale, int32_t *status,
+                          void *stream) {
+  svw::AppendNormArgs a{};
+  const svw_status s = append_args(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, q,
+                                   q_token_stride, q_head_stride, q_out, dtype, n_q_heads, N, cu_new, total_new,
+                                   kv_len, positions, cos_sin, max_pos, rot_dim, interleaved, cache, cache_dtype,
+                                   status, a);
+  if (s != SVW_OK) return s;
+  if (!(eps >= 0.f) || !std::isfinite(eps) || (q_weight && !q)) return SVW_ERR_INVALID_ARG;
+  if (cache_dtype != SVW_E4M3 && (k_scale || v_scale)) return SVW_ERR_INVALID_ARG;
+  if (!aligned(k_weight, 4) || !aligned(q_weight, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+    return SVW_ERR_MISALIGNED;
+  if (total_new == 0) return SVW_OK;
+  a.k_weight = k_weight;
+  a.q_weight = q_weight;
+  a.eps = eps;
+  a.codes = cache_dtype == SVW_E4M3 ? 1 : 0;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return svw::launch_append_norm(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SVW_OK : SVW_ERR_CUDA;
+}
+
+svw_status kv_gather(const svw_paged_kv *cache, svw_dtype cache_dtype, const float *k_scale, const float *v_scale,
+                     int32_t N, const int32_t *cu_out, int64_t total_out, const int32_t *first, void *k_out,
+                     void *v_out, svw_dtype out_dtype, int32_t *status, void *stream) {
+  if ((cache_dtype != SVW_F32 && cache_dtype != SVW_BF16 && cache_dtype != SVW_E4M3) ||
+      (out_dtype != SVW_F32 && out_dtype != SVW_BF16))
+    return SVW_ERR_UNSUPPORTED;
+  if (N <= 0 || total_out < 0) return SVW_ERR_INVALID_ARG;
+  const svw_status cs = check_cache(cache);
+  if (cs != SVW_OK) return cs;
+  if (cache->head_dim > 1024 || total_out > INT32_MAX || cache->n_kv_heads > 4096) return SVW_ERR_UNSUPPORTED;
+  if (!cu_out || (total_out > 0 && !k_out && !v_out)) return SVW_ERR_INVALID_ARG;
+  if (cache_dtype != SVW_E4M3 && (k_scale || v_scale)) return SVW_ERR_INVALID_ARG;
+  const int ces = esize_of(cache_dtype), es = esize_of(out_dtype);
+  if (!aligned(cache->k, ces) || !aligned(cache->v, ces) || !aligned(k_out, es) || !aligned(v_out, es) ||
+      !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(cu_out, 4) || !aligned(first, 4) || !aligned(status, 4))
+    return SVW_ERR_MISALIGNED;
+  if (total_out == 0) return SVW_OK;
+  svw::GatherArgs a{};
+  a.k_cache = cache->k;
+  a.v_cache = cache->v;
+  for (int d = 0; d < 3; ++d) {
+    a.kc[d] = cache->k_stride[d];
+    a.vc[d] = cache->v_stride[d];
+  }
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.Hkv = cache->n_kv_heads;
+  a.D = cache->head_dim;
+  a.N = N;
+  a.cu = cu_out;
+  a.T = total_out;
+  a.first = first;
+  a.table = cache->block_table;
+  a.table_stride = cache->table_stride;
+  a.max_pages = cache->max_pages;
+  a.n_pages = cache->n_pages;
+  a.page_size = cache->page_size;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.status = status;
+  return svw::launch_gather(a, cache_dtype, out_dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SVW_OK
+                                                                                                          : SVW_ERR_CUDA;
 }
 
 size_t svw_paged_attention_workspace_size(int64_t total_new, int32_t n_q_heads, int32_t n_kv_heads,
@@ -707,11 +794,13 @@ size_t svw_paged_attention_workspace_size(int64_t total_new, int32_t n_q_heads, 
   return svw::attention_workspace(total_new, n_q_heads / n_kv_heads, head_dim);
 }
 
-svw_status paged_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, svw_dtype dtype,
-                           int32_t n_q_heads, int32_t N, const int32_t *cu_new, int64_t total_new,
-                           const int32_t *kv_len, const svw_paged_kv *cache, float scale, int32_t causal,
-                           int32_t window, void *out, float *lse, int32_t *status, void *workspace,
-                           size_t workspace_bytes, void *stream) {
+// paged_attention, or with codes paged_attention_fp8
+static svw_status attention_entry(bool codes, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                                  svw_dtype dtype, int32_t n_q_heads, int32_t N, const int32_t *cu_new,
+                                  int64_t total_new, const int32_t *kv_len, const svw_paged_kv *cache,
+                                  const float *k_scale, const float *v_scale, float scale, int32_t causal,
+                                  int32_t window, void *out, float *lse, int32_t *status, void *workspace,
+                                  size_t workspace_bytes, void *stream) {
   if (dtype != SVW_BF16) return SVW_ERR_UNSUPPORTED;
   if (N <= 0 || total_new < 0 || n_q_heads <= 0) return SVW_ERR_INVALID_ARG;
   const svw_status cs = check_cache(cache);
@@ -724,20 +813,21 @@ svw_status paged_attention(const void *q, int64_t q_token_stride, int64_t q_head
   if (!cu_new || !kv_len || (total_new > 0 && (!q || !out))) return SVW_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale) || window < 0 || (window > 0 && !causal)) return SVW_ERR_INVALID_ARG;
   if (q_token_stride < 0 || q_head_stride < 0) return SVW_ERR_INVALID_ARG;
-  // the stride of a dimension of one is never used: any multiple of 8 will do
+  // the stride of a dimension of one is never used: any multiple of 16 bytes will do
   svw_paged_kv c = *cache;
   if (total_new <= 1) q_token_stride = D;
   if (n_q_heads == 1) q_head_stride = D;
   if (c.n_pages == 1) c.k_stride[0] = c.v_stride[0] = D;
   if (c.n_kv_heads == 1) c.k_stride[1] = c.v_stride[1] = D;
-  int64_t odd = q_token_stride | q_head_stride;
+  int64_t odd = q_token_stride | q_head_stride, odd_cache = 0;
   bool shared = q_token_stride == 0 || q_head_stride == 0;  // a dimension repeated by a stride of zero
   for (int d = 0; d < 3; ++d) {
-    odd |= c.k_stride[d] | c.v_stride[d];
+    odd_cache |= c.k_stride[d] | c.v_stride[d];
     shared |= c.k_stride[d] == 0 || c.v_stride[d] == 0;
   }
   if (shared) return SVW_ERR_UNSUPPORTED;
-  if (!aligned(q, 16) || !aligned(cache->k, 16) || !aligned(cache->v, 16) || (odd & 7) || !aligned(out, 16) ||
+  if (!aligned(q, 16) || !aligned(cache->k, 16) || !aligned(cache->v, 16) || (odd & 7) ||
+      (odd_cache & (codes ? 15 : 7)) || !aligned(out, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
       !aligned(lse, 4) || !aligned(cu_new, 4) || !aligned(kv_len, 4) || !aligned(status, 4) ||
       !aligned(workspace, 256))
     return SVW_ERR_MISALIGNED;
@@ -757,6 +847,8 @@ svw_status paged_attention(const void *q, int64_t q_token_stride, int64_t q_head
   a.kv_len = kv_len;
   a.k_cache = cache->k;
   a.v_cache = cache->v;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
   for (int d = 0; d < 3; ++d) {
     a.kc[d] = c.k_stride[d];
     a.vc[d] = c.v_stride[d];
@@ -775,7 +867,27 @@ svw_status paged_attention(const void *q, int64_t q_token_stride, int64_t q_head
   a.ws = workspace;
   a.tag = next_epoch();
   a.fault = svw::test_fault();
-  return svw::launch_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SVW_OK : SVW_ERR_CUDA;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = codes ? svw::launch_attention_fp8(a, st) : svw::launch_attention(a, st);
+  return e == cudaSuccess ? SVW_OK : SVW_ERR_CUDA;
+}
+
+svw_status paged_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, svw_dtype dtype,
+                           int32_t n_q_heads, int32_t N, const int32_t *cu_new, int64_t total_new,
+                           const int32_t *kv_len, const svw_paged_kv *cache, float scale, int32_t causal,
+                           int32_t window, void *out, float *lse, int32_t *status, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+  return attention_entry(false, q, q_token_stride, q_head_stride, dtype, n_q_heads, N, cu_new, total_new, kv_len, cache,
+                         nullptr, nullptr, scale, causal, window, out, lse, status, workspace, workspace_bytes, stream);
+}
+
+svw_status paged_attention_fp8(const void *q, int64_t q_token_stride, int64_t q_head_stride, svw_dtype dtype,
+                               int32_t n_q_heads, int32_t N, const int32_t *cu_new, int64_t total_new,
+                               const int32_t *kv_len, const svw_paged_kv *cache, const float *k_scale,
+                               const float *v_scale, float scale, int32_t causal, int32_t window, void *out,
+                               float *lse, int32_t *status, void *workspace, size_t workspace_bytes, void *stream) {
+  return attention_entry(true, q, q_token_stride, q_head_stride, dtype, n_q_heads, N, cu_new, total_new, kv_len, cache,
+                         k_scale, v_scale, scale, causal, window, out, lse, status, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

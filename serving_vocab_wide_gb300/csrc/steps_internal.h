@@ -1,5 +1,6 @@
 // steps_internal.h -- host-side declarations of the steps around a verification
-// (logits_adjust, kv_append, paged_attention).  Not part of the public interface.
+// (logits_adjust, kv_append, paged_attention; kv_append_norm, kv_gather,
+// paged_attention_fp8).  Not part of the public interface.
 #pragma once
 
 #include "svw_internal.h"
@@ -61,6 +62,33 @@ struct AppendArgs {
 };
 cudaError_t launch_append(const AppendArgs &a, int dtype, cudaStream_t stream);
 
+// kv_append_norm (append_norm.cu)
+struct AppendNormArgs : AppendArgs {
+  const float *k_weight, *q_weight;  // NULL: no norm
+  float eps;
+  int32_t codes;  // 1: the cache is e4m3
+  const float *k_scale, *v_scale;  // NULL: 1
+};
+cudaError_t launch_append_norm(const AppendNormArgs &a, int dtype, cudaStream_t stream);
+
+// kv_gather (gather.cu)
+struct GatherArgs {
+  const void *k_cache, *v_cache;
+  int64_t kc[3], vc[3];  // page, head, row strides in elements
+  const float *k_scale, *v_scale;  // NULL: 1
+  int32_t Hkv, D;
+  int32_t N;
+  const int32_t *cu;
+  int64_t T;
+  const int32_t *first;
+  const int32_t *table;
+  int64_t table_stride;
+  int32_t max_pages, n_pages, page_size;
+  void *k_out, *v_out;
+  int32_t *status;
+};
+cudaError_t launch_gather(const GatherArgs &a, int cache_dtype, int out_dtype, cudaStream_t stream);
+
 // paged_attention (attention.cu)
 // the unit that a worker's last segment begins and does not finish
 struct alignas(16) AttendJoint {
@@ -77,6 +105,7 @@ struct AttendArgs {
   const int32_t *kv_len;
   const void *k_cache, *v_cache;
   int64_t kc[3], vc[3];
+  const float *k_scale, *v_scale;  // of an e4m3 cache; NULL: 1
   const int32_t *table;
   int64_t table_stride;
   int32_t max_pages, n_pages, page_size;
@@ -98,5 +127,6 @@ struct AttendArgs {
 };
 size_t attention_workspace(int64_t T, int32_t G, int32_t D);  // G: query heads of a key head
 cudaError_t launch_attention(const AttendArgs &a, cudaStream_t stream);
+cudaError_t launch_attention_fp8(const AttendArgs &a, cudaStream_t stream);  // attention_fp8.cu
 
 }  // namespace svw
