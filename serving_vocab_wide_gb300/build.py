@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(BUILD_DIR, "libsvw.so")
 SOURCES = ["api.cu", "verify.cu", "early.cu", "filtered.cu", "opd.cu", "fused.cu", "lengthhead.cu", "noalloc.cu",
            "adjust.cu", "append.cu", "append_norm.cu", "gather.cu", "attention.cu", "attention_fp8.cu"]
 HEADERS = ["svw_device.cuh", "svw_internal.h", "steps_internal.h", "svw_sample.cuh", "opd_common.cuh",
-           "append_device.cuh", "e4m3.cuh"]
+           "append_device.cuh", "attention.cuh", "e4m3.cuh"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
