@@ -73,6 +73,36 @@ __device__ __forceinline__ Place find_place(const AppendArgs &a, int64_t t) {
   return p;
 }
 
+// By one warp: of each lane's token t the last request i with cu[i] <= t.  The
+// tokens follow one another from the first lane's on; those behind `last` count
+// as it does.
+__device__ __forceinline__ int32_t request_of(const int32_t *cu, int32_t N, int64_t t, int64_t last) {
+  const int lane = threadIdx.x & 31;
+  auto search = [&](int32_t lo, int64_t x) {  // in [lo, N), 32 probes a round
+    int32_t n = N - lo;
+    while (n > 1) {
+      const int32_t step = (n + 31) / 32;
+      const bool le = (lane * step < n) && (__ldg(cu + lo + lane * step) <= x);
+      const unsigned b = __ballot_sync(0xffffffffu, le);
+      const int k = b ? 31 - __clz(b) : 0;
+      n = min(step, n - k * step);
+      lo += k * step;
+    }
+    return lo;
+  };
+  int32_t lo = search(0, __shfl_sync(0xffffffffu, t, 0));
+  int32_t hi = __ldg(cu + lo + 1) > last ? lo : search(lo, last);  // often the same request
+  if (t > last) t = last;
+  while (hi > lo) {
+    const int32_t mid = lo + (hi - lo + 1) / 2;
+    if (__ldg(cu + mid) <= t)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
 // source of head h of the token (keys, then values, then queries)
 template <typename T>
 __device__ __forceinline__ void head_rows(const AppendArgs &a, int64_t t, int h, const T *&src) {

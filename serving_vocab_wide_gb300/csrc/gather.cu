@@ -15,32 +15,28 @@ namespace svw {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kTile = 32;  // tokens of a block, at most: one warp finds them
 
 // where a token lies: page -1 if nowhere
 struct Where {
   int32_t page, row;
 };
-// The token's request is the last one i with cu[i] <= t.
-__device__ __forceinline__ Where find(const GatherArgs &a, int64_t t) {
-  int32_t lo = 0, hi = a.N;  // the answer lies in [lo, hi)
-  while (hi - lo > 1) {
-    const int32_t mid = lo + (hi - lo) / 2;
-    if (__ldg(a.cu + mid) <= t)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  const int32_t c0 = __ldg(a.cu + lo), c1 = __ldg(a.cu + lo + 1);
+// By one warp: where its lanes' tokens lie, which follow one another up to `last`.
+__device__ __forceinline__ Where find(const GatherArgs &a, int64_t t, int64_t last) {
+  const int32_t i = request_of(a.cu, a.N, t, last);
+  const int32_t c0 = __ldg(a.cu + i), c1 = __ldg(a.cu + i + 1);
   Where w = {-1, 0};
-  if (!(c0 >= 0 && c0 <= t && t < c1 && c1 <= a.T)) return w;
-  const int64_t first = a.first ? __ldg(a.first + lo) : 0;
-  if (first < 0) return w;
-  const int64_t place = first + (t - c0);
-  const int64_t at = place / a.page_size;
-  if (at >= a.max_pages) return w;
-  w.row = static_cast<int32_t>(place - at * a.page_size);
-  const int32_t page = __ldg(a.table + lo * a.table_stride + at);
-  if (page >= 0 && page < a.n_pages) w.page = page;
+  if (t > last) return w;
+  if (c0 >= 0 && c0 <= t && t < c1 && c1 <= a.T) {
+    const int64_t first = a.first ? __ldg(a.first + i) : 0, place = first + (t - c0);
+    const int32_t at = first < 0 || place > INT32_MAX ? a.max_pages : static_cast<int32_t>(place) / a.page_size;
+    if (at < a.max_pages) {
+      w.row = static_cast<int32_t>(place) - at * a.page_size;
+      const int32_t page = __ldg(a.table + i * a.table_stride + at);
+      if (page >= 0 && page < a.n_pages) w.page = page;
+    }
+  }
+  if (w.page < 0 && a.status) atomicOr(a.status, SVW_DEV_BAD_INPUT);
   return w;
 }
 
@@ -48,12 +44,105 @@ __device__ __forceinline__ float entry(const uint8_t *p) { return e4m3x2_f2(*p).
 __device__ __forceinline__ float entry(const __nv_bfloat16 *p) { return ld_f(p); }
 __device__ __forceinline__ float entry(const float *p) { return *p; }
 
-// one CTA per token, entry by entry
+// the elements of a 16-byte vector of a cache, as floats
+__device__ __forceinline__ void open(const uint4 &w, float (&f)[16]) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 g = e4m3x2_f2((i & 1) ? in[i / 2] >> 16 : in[i / 2]);
+    f[2 * i] = g.x, f[2 * i + 1] = g.y;
+  }
+}
+__device__ __forceinline__ void open(const uint4 &w, float (&f)[8]) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 g = bf16x2_f2(in[i]);
+    f[2 * i] = g.x, f[2 * i + 1] = g.y;
+  }
+}
+__device__ __forceinline__ void open(const uint4 &w, float (&f)[4]) {
+  f[0] = __uint_as_float(w.x), f[1] = __uint_as_float(w.y), f[2] = __uint_as_float(w.z), f[3] = __uint_as_float(w.w);
+}
+template <int E>
+__device__ __forceinline__ void put(__nv_bfloat16 *dst, const float (&f)[E]) {
+  if constexpr (E == 4) {
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(Vec<__nv_bfloat16>::two(f[0], f[1]), Vec<__nv_bfloat16>::two(f[2], f[3]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; e += 8)
+      *reinterpret_cast<uint4 *>(dst + e) =
+          make_uint4(Vec<__nv_bfloat16>::two(f[e], f[e + 1]), Vec<__nv_bfloat16>::two(f[e + 2], f[e + 3]),
+                     Vec<__nv_bfloat16>::two(f[e + 4], f[e + 5]), Vec<__nv_bfloat16>::two(f[e + 6], f[e + 7]));
+  }
+}
+template <int E>
+__device__ __forceinline__ void put(float *dst, const float (&f)[E]) {
+#pragma unroll
+  for (int e = 0; e < E; e += 4) *reinterpret_cast<float4 *>(dst + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+}
+
+// A block has a tile of tokens: its first warp finds them, then a thread has one
+// 16-byte vector of keys or values (or every blockDim.x-th) of every
+// blockDim.y-th token, kItems of them under way.  Everything 16-byte aligned.
+template <typename C, typename O, int kItems>
+__global__ void __launch_bounds__(kThreads) gather_vec(const __grid_constant__ GatherArgs a) {
+  constexpr int E = 16 / sizeof(C);
+  __shared__ int64_t at[2][kTile];  // of keys and values, in elements; -1: nowhere
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tile;
+  const int tokens = static_cast<int>(min(static_cast<int64_t>(a.tile), a.T - t0));
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x;
+  if (tid < 32) {
+    const Where w = find(a, t0 + tid, t0 + tokens - 1);
+    if (tid < tokens) {
+      at[0][tid] = w.page < 0 ? -1 : w.page * a.kc[0] + w.row * a.kc[2];
+      at[1][tid] = w.page < 0 ? -1 : w.page * a.vc[0] + w.row * a.vc[2];
+    }
+  }
+  __syncthreads();
+  const int of_head = a.D / E, of_side = a.Hkv * of_head;
+  for (int s = threadIdx.x; s < 2 * of_side; s += blockDim.x) {
+    const int side = s >= of_side, i = s - side * of_side, h = i / of_head;
+    O *out = static_cast<O *>(side ? a.v_out : a.k_out);
+    if (!out) continue;
+    const float scale = sizeof(C) == 1 ? head_scale(side ? a.v_scale : a.k_scale, h, a.status) : 1.f;
+    const C *in = static_cast<const C *>(side ? a.v_cache : a.k_cache) + h * (side ? a.vc[1] : a.kc[1]) + (i - h * of_head) * E;
+    out += t0 * (of_side * E) + i * E;
+    for (int t = threadIdx.y; t < tokens; t += kItems * blockDim.y) {
+      uint4 w[kItems];
+      bool ok[kItems];
+#pragma unroll
+      for (int q = 0; q < kItems; ++q) {
+        const int tq = t + q * blockDim.y;
+        const int64_t from = tq < tokens ? at[side][tq] : -1;
+        ok[q] = from >= 0;
+        if (ok[q]) w[q] = ld_stream(in + from);
+      }
+#pragma unroll
+      for (int q = 0; q < kItems; ++q) {
+        const int tq = t + q * blockDim.y;
+        if (tq >= tokens) break;
+        float f[E];
+        open(w[q], f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] = !ok[q] ? __uint_as_float(kNaNs) : sizeof(C) == 1 ? __fmul_rn(f[e], scale) : f[e];
+        put<E>(out + static_cast<int64_t>(tq) * (of_side * E), f);
+      }
+    }
+  }
+}
+
+// any sizes, strides and alignments: one CTA per token, entry by entry
 template <typename C, typename O>
 __global__ void __launch_bounds__(kThreads) gather_any(const __grid_constant__ GatherArgs a) {
+  __shared__ Where found;
   const int64_t t = blockIdx.x;
-  const Where w = find(a, t);
-  if (w.page < 0 && threadIdx.x == 0 && a.status) atomicOr(a.status, SVW_DEV_BAD_INPUT);
+  if (threadIdx.x < 32) {
+    const Where w = find(a, t + threadIdx.x, t);
+    if (threadIdx.x == 0) found = w;
+  }
+  __syncthreads();
+  const Where w = found;
   const int each = a.Hkv * a.D;
   for (int e = threadIdx.x; e < 2 * each; e += kThreads) {
     const bool is_v = e >= each;
@@ -72,8 +161,20 @@ __global__ void __launch_bounds__(kThreads) gather_any(const __grid_constant__ G
 }
 
 template <typename C, typename O>
-void launch(const GatherArgs &a, cudaStream_t st) {
-  gather_any<C, O><<<static_cast<unsigned>(a.T), kThreads, 0, st>>>(a);
+void launch(GatherArgs a, cudaStream_t st) {
+  constexpr int E = 16 / sizeof(C), kItems = 4;
+  int64_t odd = a.D;
+  for (int d = 0; d < 3; ++d) odd |= a.kc[d] | a.vc[d];
+  if (!at16(a.k_cache) || !at16(a.v_cache) || !at16(a.k_out) || !at16(a.v_out) || odd % E != 0) {
+    gather_any<C, O><<<static_cast<unsigned>(a.T), kThreads, 0, st>>>(a);
+    return;
+  }
+  const int vectors = 2 * a.Hkv * (a.D / E);
+  const int x = vectors >= kThreads ? kThreads : (vectors + 31) / 32 * 32, y = kThreads / x;
+  // tokens of a block: no fewer blocks than four for each SM, where there are so many
+  const int64_t share = a.T / (4 * 152);
+  a.tile = static_cast<int32_t>(share < y ? y : share > kTile ? kTile : share);
+  gather_vec<C, O, kItems><<<static_cast<unsigned>((a.T + a.tile - 1) / a.tile), dim3(x, y), 0, st>>>(a);
 }
 template <typename C>
 void launch(const GatherArgs &a, int out_dtype, cudaStream_t st) {

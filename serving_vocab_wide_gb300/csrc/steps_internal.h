@@ -68,6 +68,13 @@ struct AppendNormArgs : AppendArgs {
   float eps;
   int32_t codes;  // 1: the cache is e4m3
   const float *k_scale, *v_scale;  // NULL: 1
+  // set by the launcher
+  float inv_dim;      // 1 / D
+  int32_t lane_bits;  // 2^lane_bits lanes of a warp share a head
+  int32_t kv_tasks;   // tasks of a token's keys, and as many of its values
+  uint32_t tasks;     // and with its queries'
+  uint32_t line;      // of all tokens
+  uint32_t share;     // of a block
 };
 cudaError_t launch_append_norm(const AppendNormArgs &a, int dtype, cudaStream_t stream);
 
@@ -86,6 +93,7 @@ struct GatherArgs {
   int32_t max_pages, n_pages, page_size;
   void *k_out, *v_out;
   int32_t *status;
+  int32_t tile;  // set by the launcher: tokens of a block
 };
 cudaError_t launch_gather(const GatherArgs &a, int cache_dtype, int out_dtype, cudaStream_t stream);
 
