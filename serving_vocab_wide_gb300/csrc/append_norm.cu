@@ -228,7 +228,7 @@ __device__ __forceinline__ void form(const AppendNormArgs &a, const Spot &p, uin
 // with the scale of a code in r.  Heads and rotated parts in multiples of two
 // vectors, everything 16-byte aligned.
 template <typename T, bool kCodes, bool kApart, int kItems>
-__global__ void __launch_bounds__(kThreads, 2) append_norm_vec(const __grid_constant__ AppendNormArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) append_norm_vec(const __grid_constant__ AppendNormArgs a) {
   constexpr int N = Vec<T>::N;
   __shared__ Spot spots[kTokens];
   const uint32_t begin = blockIdx.x * a.share, end = min(begin + a.share, a.line);
@@ -342,8 +342,8 @@ void launch(AppendNormArgs a, cudaStream_t st) {
   const int slots = vec ? a.D / (2 * N) : 64;
   while ((1 << a.lane_bits) < slots) ++a.lane_bits;
   // few tokens: a round a task, the shortest way through
-  const int round = 32 >> a.lane_bits, most = a.Hq > a.Hkv ? a.Hq : a.Hkv;
-  const int items = a.T * (a.Hq + 2 * a.Hkv) < 2 * kSms * kWarps * round * 2 ? 1 : most > 2 * round ? 4 : 2;
+  const int round = 32 >> a.lane_bits;
+  const int items = a.T * (a.Hq + 2 * a.Hkv) < 2 * kSms * kWarps * round * 2 ? 1 : 2;
   const int each = items * std::max(round, 1);
   a.kv_tasks = (a.Hkv + each - 1) / each;
   a.tasks = 2 * a.kv_tasks + (a.Hq + each - 1) / each;
@@ -352,18 +352,16 @@ void launch(AppendNormArgs a, cudaStream_t st) {
     return;
   }
   a.line = static_cast<uint32_t>(a.T * a.tasks);
-  // two blocks an SM at once, of a task a warp at least and of kTokens tokens at most
-  const uint32_t even = (a.line + 2 * kSms - 1) / (2 * kSms);
+  // three blocks an SM at once, of a task a warp at least and of kTokens tokens at most
+  const uint32_t even = (a.line + 3 * kSms - 1) / (3 * kSms);
   a.share = std::min(std::max<uint32_t>(even, kWarps), (kTokens - 1) * a.tasks);
   const unsigned grid = (a.line + a.share - 1) / a.share;
   auto go = [&](auto apart) {
     constexpr bool kApart = decltype(apart)::value;
     if (items == 1)
       append_norm_vec<T, kCodes, kApart, 1><<<grid, kThreads, 0, st>>>(a);
-    else if (items == 2)
-      append_norm_vec<T, kCodes, kApart, 2><<<grid, kThreads, 0, st>>>(a);
     else
-      append_norm_vec<T, kCodes, kApart, 4><<<grid, kThreads, 0, st>>>(a);
+      append_norm_vec<T, kCodes, kApart, 2><<<grid, kThreads, 0, st>>>(a);
   };
   a.interleaved ? go(std::false_type{}) : go(std::true_type{});
 }

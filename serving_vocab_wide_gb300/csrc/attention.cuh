@@ -1000,12 +1000,9 @@ __device__ __forceinline__ float split_query(unsigned char *q, int row) {
     const uint32_t in[8] = {w[c].x, w[c].y, w[c].z, w[c].w, w[c + 1].x, w[c + 1].y, w[c + 1].z, w[c + 1].w};
     uint32_t first[4], second[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = bf16x2_f2(in[i]);
-      uint32_t a, b;
-      split_e4m3x2(f.x * up, f.y * up, a, b);
-      first[i / 2] = (i & 1) ? first[i / 2] | (a << 16) : a;
-      second[i / 2] = (i & 1) ? second[i / 2] | (b << 16) : b;
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = bf16x2_f2(in[2 * i]), g = bf16x2_f2(in[2 * i + 1]);
+      split_e4m3x4(f.x * up, f.y * up, g.x * up, g.y * up, first[i], second[i]);
     }
     *piece(c / 2) = make_uint4(first[0], first[1], first[2], first[3]);
     *piece(kPieces / 2 + c / 2) = make_uint4(second[0], second[1], second[2], second[3]);
@@ -1014,6 +1011,11 @@ __device__ __forceinline__ float split_query(unsigned char *q, int row) {
 }
 
 // ------------------------------- the softmax --------------------------------
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // Of stage s: a thread has one row and all keys of a tile.
 template <int D, bool kWide, bool kF8, bool kInside, typename C>
 __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s, unsigned char *q_ptr,
@@ -1078,9 +1080,11 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
         }
         float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int c = 4; c < Sh::kKeys; c += 4)
+        for (int c = 4; c + 4 < Sh::kKeys; c += 8)
 #pragma unroll
-          for (int v = 0; v < 4; ++v) mx[v] = fmaxf(mx[v], x[c + v]);
+          for (int v = 0; v < 4; ++v) mx[v] = max3(mx[v], x[c + v], x[c + 4 + v]);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) mx[v] = fmaxf(mx[v], x[Sh::kKeys - 4 + v]);
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * k2;
         const bool grow = live && (top > M + Sh::kGrow || (M == -INFINITY && top > M));
         const float f = grow ? (M == -INFINITY ? 0.f : ex2(M - (top - Sh::kLift))) : 1.f;
@@ -1089,6 +1093,7 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
         const float ref = (M == -INFINITY) ? 0.f : M;
         const float2 kk = make_float2(k2, k2), nr = make_float2(-ref, -ref);
         float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+        float2 before = sum0;
         uint32_t w[Sh::kKeys / 2];
 #pragma unroll
         for (int c = 0; c < Sh::kKeys / 2; ++c) {
@@ -1101,10 +1106,10 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
           if constexpr (kF8) {
             // 64 keys: 16 columns of first numbers, four keys each, and 16 of second ones
             const int at = (c / 32) * 32 + (c % 32) / 2;
-            uint32_t first, second;
-            split_e4m3x2(p.x, p.y, first, second);
-            w[at] = (c & 1) ? w[at] | (first << 16) : first;
-            w[at + 16] = (c & 1) ? w[at + 16] | (second << 16) : second;
+            if (c & 1)
+              split_e4m3x4(before.x, before.y, p.x, p.y, w[at], w[at + 16]);
+            else
+              before = p;
             if (!Sh::kApart && (c & 15) == 15) {
               tmem_st8(t_p + u * 64 + (at - 7), w + (at - 7));
               tmem_st8(t_p + u * 64 + (at + 9), w + (at + 9));

@@ -33,20 +33,23 @@ __device__ __forceinline__ float2 f16x2_f2(uint32_t w) {
 }
 __device__ __forceinline__ float2 e4m3x2_f2(uint32_t w) { return f16x2_f2(f16x2_of_e4m3(w)); }
 
-// Two numbers of four bits for each of two: the code nearest to x (as fp16), and
-// the one nearest to what is left.
-__device__ __forceinline__ void split_e4m3x2(float lo, float hi, uint32_t &first, uint32_t &second) {
-  uint16_t a, b;
-  asm("{\n\t.reg .b32 h, r;\n\t"
+// Two numbers of four bits for each of four: the code nearest to x (as fp16),
+// and the one nearest to what is left; a's in the low bytes.
+__device__ __forceinline__ void split_e4m3x4(float a, float b, float c, float d, uint32_t &first, uint32_t &second) {
+  asm("{\n\t.reg .b32 h, r;\n\t.reg .b16 p, q, s, t;\n\t"
       "cvt.rn.f16x2.f32 h, %3, %2;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 %0, h;\n\t"
-      "cvt.rn.f16x2.e4m3x2 r, %0;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 p, h;\n\t"
+      "cvt.rn.f16x2.e4m3x2 r, p;\n\t"
       "sub.rn.f16x2 h, h, r;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 %1, h;\n\t}"
-      : "=&h"(a), "=h"(b)
-      : "f"(lo), "f"(hi));
-  first = a;
-  second = b;
+      "cvt.rn.satfinite.e4m3x2.f16x2 s, h;\n\t"
+      "cvt.rn.f16x2.f32 h, %5, %4;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 q, h;\n\t"
+      "cvt.rn.f16x2.e4m3x2 r, q;\n\t"
+      "sub.rn.f16x2 h, h, r;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 t, h;\n\t"
+      "mov.b32 %0, {p, q};\n\tmov.b32 %1, {s, t};\n\t}"
+      : "=r"(first), "=r"(second)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
 }
 
 // The scale of head h (1 where there are none), NaN where it is not a normal
