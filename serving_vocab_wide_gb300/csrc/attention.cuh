@@ -96,10 +96,12 @@ struct Shape {
   static constexpr int kSoftWarps = kWide ? 8 : 4;         // softmax warps of a worker
   // a unit's fixed cost on the line, in key tiles (one or three: 10 prompts of 1 to 1275 tokens 92 or 83 us instead
   // of 85, 117 requests of 68 tokens 300 or 305 instead of 299; narrow with three, 2220 tokens 452 instead of 448)
-  static constexpr int kUnitCost = 2;
+  static constexpr int kUnitCost = kF8 && !kWide ? 4 : 2;
   static constexpr int kQHalves = D / 64;                  // 128-byte columns of a query tile
   static constexpr int kQTile = kRows * D * 2;             // its bytes
   static constexpr int kQHalf = kRows * 128;               // those of one of its columns
+  // rows of a unit, up to which worker 1's take lanes 64 to 127 of tensor memory, and so other warps than worker 0's
+  static constexpr int kFlip = kF8 && !kWide ? 64 : 0;
   static constexpr int kHalves = kF8 ? 1 : D / 64;         // columns of a key or value tile
   static constexpr int kRowBytes = kF8 ? D : 128;          // of a column's row: the swizzle's width
   static constexpr int kHalf = kKeys * kRowBytes;
@@ -556,7 +558,7 @@ __device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtens
 // products interleaving as they come, 471, since both stages then wait for
 // their products at the same time; taking turns, 435.)
 template <int D, bool kWide, bool kF8, typename C>
-__device__ __forceinline__ void issue_worker(C &sm, int wk, uint32_t q_smem, uint32_t ring, uint32_t tmem) {
+__device__ __forceinline__ void issue_worker(C &sm, int wk, int G, uint32_t q_smem, uint32_t ring, uint32_t tmem) {
   using Sh = Shape<D, kWide, kF8>;
   constexpr uint32_t id_s = idesc(Sh::kKeys, false, kF8), id_o = idesc(D, true, kF8);
   auto &ln = sm.lane[wk];
@@ -574,11 +576,12 @@ __device__ __forceinline__ void issue_worker(C &sm, int wk, uint32_t q_smem, uin
   };
   At kt = {0, 0}, vt = {1, 0};
   int32_t k = 0, sc[2] = {0, 0};
+  uint32_t q_rows = 0;  // the bytes that the tile's rows lie behind the first lane's
   bool ok = true;
   auto wait_ring = [&](const At &t) { return ok = ok && warp_wait(&ln.full[t.slot], t.parity); };
   // by the elected thread: into score buffer u of stage st, from it into the stage's output
   auto scores = [&](int st, int u, const At &t) {
-    const uint64_t qa = sw128(q_smem + (kWide ? st * Sh::kQTile : 0), 16);
+    const uint64_t qa = sw128(q_smem + (kWide ? st * Sh::kQTile : 0) - q_rows, 16);
     const uint32_t ks = ring + t.slot * Sh::kTile;
     if constexpr (kF8 && D == 64) {
       mma_ss_twice(tmem + st * 128 + u * 64, qa, sw64(ks), id_s);
@@ -608,6 +611,7 @@ __device__ __forceinline__ void issue_worker(C &sm, int wk, uint32_t q_smem, uin
     const int sl = k % kSegRing;
     if (!(ok = warp_wait(&ln.seg_full[sl], par(k / kSegRing)))) break;
     const int32_t n = ln.seg[sl].tiles;
+    if (Sh::kFlip) q_rows = (wk == 1 && ln.seg[sl].ntok0 * G <= Sh::kFlip) ? (kRows - Sh::kFlip) * 128 : 0;
     __syncwarp();
     if (n == 0) break;
     if (elect_one()) mbar_arrive(&ln.seg_empty[sl]);
@@ -1025,7 +1029,6 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
   const int row = quad * 32 + lane;
   const int G = a.Hq / a.Hkv;
-  const int tok_of_row = row / G, head_of_row = row - tok_of_row * G;
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t t_s = tmem + lanes + s * 128, t_p = tmem + lanes + Sh::weights(s, 0);
   const uint32_t t_o = tmem + lanes + 256 + s * D;
@@ -1038,6 +1041,8 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
     const Segment g = ln.seg[sl];
     if (g.tiles == 0) break;
     const int tile = kWide ? s : 0;
+    const int q_row = (Sh::kFlip && s == 1 && g.ntok0 * G <= Sh::kFlip) ? row ^ Sh::kFlip : row;  // of the tile
+    const int tok_of_row = q_row / G, head_of_row = q_row - tok_of_row * G;
     const int32_t pos = g.pos0 + tile * a.tile_tokens + tok_of_row;
     int32_t hi = g.kv, lo = first_key(a, pos);
     if (a.causal) hi = min(hi, pos + 1);
@@ -1047,7 +1052,7 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
     if (kF8) {
       if (warp_live) {
         if (!(ok = warp_wait(&sm.q_full[kWide ? 0 : s], par(k)))) break;
-        k2 = a.scale * kLog2e * head_scale(a.k_scale, g.hk, a.status) * split_query<D>(q_ptr, row);
+        k2 = a.scale * kLog2e * head_scale(a.k_scale, g.hk, a.status) * split_query<D>(q_ptr, q_row);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       __syncwarp();
@@ -1171,7 +1176,7 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
       if (bad == 2) l = kNaN;
       const int32_t tok = g.tok0 + tile * a.tile_tokens + tok_of_row;
       const int32_t orow = live ? tok * a.Hq + g.hk * G + head_of_row : -1;  // below 2^31, checked by the host
-      const int64_t prow = static_cast<int64_t>(max(g.part, 0)) * a.part_rows + tile * kRows + row;
+      const int64_t prow = static_cast<int64_t>(max(g.part, 0)) * a.part_rows + tile * kRows + q_row;
       const float vs = kF8 ? head_scale(a.v_scale, g.hk, a.status) : 1.f;
       const float inv = (g.part >= 0) ? 1.f : (l == 0.f ? 0.f : vs / l);
       int32_t to[4];  // the rows of this lane's four, and its piece of each
@@ -1376,7 +1381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t id = static_cast<int64_t>(blockIdx.x) * Sh::kWorkers + wk;
     const uint32_t my_q = q_smem + wk * Sh::kQTile, my_ring = ring + wk * kRingBytes;
     if (warp == 1 || (!kWide && warp == 3))
-      issue_worker<D, kWide, kF8>(sm, wk, my_q, my_ring, tmem);
+      issue_worker<D, kWide, kF8>(sm, wk, a.Hq / a.Hkv, my_q, my_ring, tmem);
     else if (!kWide)
       load_worker<D, kWide, kF8, 0, 2>(tmQ, tmK, tmV, a, sm, wk, static_cast<int>(id), W, line(id), line(id + 1), workers, my_q, my_ring);
     else if (warp == 0)
