@@ -102,6 +102,7 @@ struct Shape {
   static constexpr int kQHalf = kRows * 128;               // those of one of its columns
   // rows of a unit, up to which worker 1's take lanes 64 to 127 of tensor memory, and so other warps than worker 0's
   static constexpr int kFlip = kF8 && !kWide ? 64 : 0;
+  static constexpr bool kOnePiece = kF8 && !kWide;         // outputs and next scores are issued together
   static constexpr int kHalves = kF8 ? 1 : D / 64;         // columns of a key or value tile
   static constexpr int kRowBytes = kF8 ? D : 128;          // of a column's row: the swizzle's width
   static constexpr int kHalf = kKeys * kRowBytes;
@@ -675,6 +676,18 @@ __device__ __forceinline__ void issue_worker(C &sm, int wk, int G, uint32_t q_sm
         if (!(ok = warp_wait(&sm.p_full[2 * st + u], par(sc[kWide ? i : u])))) break;
         ++sc[kWide ? i : u];
         if (j == 0 && k > 0 && !(ok = warp_wait(&sm.o_free[st], par(k - 1)))) break;
+        // narrow, codes: the next keys are there as a rule, and both products go out in one piece
+        if (Sh::kOnePiece && (!more || __all_sync(0xffffffffu, mbar_try_wait(&ln.full[kt.slot], kt.parity)))) {
+          tc_after();
+          if (elect_one()) {
+            output(st, u, vt, j > 0);
+            if (more) scores(st, u, kt);
+            release(vt);
+            if (more) release(kt);
+            if (j == max(0, n - 3)) tc_commit(smem_u32(&sm.q_empty[wk]));
+          }
+          continue;
+        }
         tc_after();
         if (elect_one()) {
           output(st, u, vt, j > 0);
