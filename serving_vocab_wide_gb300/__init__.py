@@ -743,29 +743,29 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, *, scale: 
     return out, lse
 
 
-@functools.lru_cache(maxsize=None)
-def _codes():
-    """The codes of the types that a cache may have."""
-    import torch
-    return {torch.float32: SVW_F32, torch.bfloat16: SVW_BF16, torch.float8_e4m3fn: SVW_E4M3}
+_CACHE_CODES = {}  # of the types that a cache may have
 
 
 def _cache_code(dtype):
-    code = _codes().get(dtype)
+    code = _CACHE_CODES.get(dtype)
     if code is None:
-        raise SvwError(f"the caches must be float32, bfloat16 or float8_e4m3fn, got {dtype}")
+        import torch
+        _CACHE_CODES.update({torch.float32: SVW_F32, torch.bfloat16: SVW_BF16, torch.float8_e4m3fn: SVW_E4M3})
+        code = _CACHE_CODES.get(dtype)
+        if code is None:
+            raise SvwError(f"the caches must be float32, bfloat16 or float8_e4m3fn, got {dtype}")
     return code
 
 
-def _scales(k_scale, v_scale, heads, code, gpu):
-    """k_scale and v_scale are per-head factors of a cache of 8 bits (None: 1)."""
-    if k_scale is None and v_scale is None:
-        return
+def _scale(name, t, heads, code, gpu):
+    """The address of the per-head factors of a cache of 8 bits (None: 1)."""
+    if t is None:
+        return 0
     if code != SVW_E4M3:
-        raise SvwError("k_scale and v_scale come with float8_e4m3fn caches")
-    _need_like(gpu, _torch().float32, ("k_scale", "v_scale"), (k_scale, v_scale))
-    if (k_scale is not None and k_scale.numel() != heads) or (v_scale is not None and v_scale.numel() != heads):
-        raise SvwError(f"k_scale and v_scale must have {heads} elements")
+        raise SvwError(f"{name} comes with float8_e4m3fn caches")
+    if _off(t, _torch().float32, gpu) or t.numel() != heads:
+        raise SvwError(f"{name} must be a contiguous float32 tensor of {heads} elements on cuda:{gpu}")
+    return t.data_ptr()
 
 
 def kv_append_norm(k, v, k_cache, v_cache, block_table, cu_new, kv_len, *, k_weight=None, q_weight=None,
@@ -798,11 +798,10 @@ def kv_append_norm(k, v, k_cache, v_cache, block_table, cu_new, kv_len, *, k_wei
         raise SvwError(f"kv_len must have {N} elements")
     if positions is not None and positions.numel() != T:
         raise SvwError(f"positions must have {T} elements")
-    if _off(k_weight, f32, gpu) or _off(q_weight, f32, gpu):
-        _need_like(gpu, f32, ("k_weight", "q_weight"), (k_weight, q_weight))
-    if (k_weight is not None and k_weight.numel() != dim) or (q_weight is not None and q_weight.numel() != dim):
-        raise SvwError(f"k_weight and q_weight must have {dim} elements")
-    _scales(k_scale, v_scale, heads, code, gpu)
+    for w in (k_weight, q_weight):
+        if w is not None and (_off(w, f32, gpu) or w.numel() != dim):
+            raise SvwError(f"k_weight and q_weight must be contiguous float32 tensors of {dim} elements on cuda:{gpu}")
+    k_scale, v_scale = _scale("k_scale", k_scale, heads, code, gpu), _scale("v_scale", v_scale, heads, code, gpu)
     max_pos = rot = 0
     if cos_sin is not None:
         if _off(cos_sin, f32, gpu) or cos_sin.dim() != 2:
@@ -823,7 +822,7 @@ def kv_append_norm(k, v, k_cache, v_cache, block_table, cu_new, kv_len, *, k_wei
     rc = lib().kv_append_norm(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _addr(q), qs[0], qs[1],
                               _addr(q_out), _dtype_code(k), hq, N, cu_new.data_ptr(), T, kv_len.data_ptr(),
                               _addr(positions), _addr(k_weight), _addr(q_weight), eps, _addr(cos_sin), max_pos, rot,
-                              1 if interleaved else 0, cache, code, _addr(k_scale), _addr(v_scale), _addr(status),
+                              1 if interleaved else 0, cache, code, k_scale, v_scale, _addr(status),
                               _stream_of(stream, gpu))
     if rc:
         _check(rc)
@@ -851,7 +850,8 @@ def kv_gather(k_cache, v_cache, block_table, cu_out, *, first=None, k_scale=None
         _need_like(gpu, i32, ("cu_out", "first", "status"), (cu_out, first, status))
     if first is not None and first.numel() != N:
         raise SvwError(f"first must have {N} elements")
-    _scales(k_scale, v_scale, shape[1], code, gpu)
+    heads = shape[1]
+    k_scale, v_scale = _scale("k_scale", k_scale, heads, code, gpu), _scale("v_scale", v_scale, heads, code, gpu)
     given = k_out if k_out is not None else v_out
     if total_out is None:
         total_out = int(cu_out[-1].item()) if given is None else given.shape[0]
@@ -860,7 +860,7 @@ def kv_gather(k_cache, v_cache, block_table, cu_out, *, first=None, k_scale=None
     out_code = _cache_code(dtype)
     if out_code == SVW_E4M3:
         raise SvwError("k_out and v_out must be bfloat16 or float32")
-    want = (total_out, shape[1], shape[3])
+    want = (total_out, heads, shape[3])
     if k_out is None:
         k_out = _empty(stream, gpu, want, dtype, k_cache.device)
     elif _off(k_out, dtype, gpu) or k_out.shape != want:
@@ -869,7 +869,7 @@ def kv_gather(k_cache, v_cache, block_table, cu_out, *, first=None, k_scale=None
         v_out = _empty(stream, gpu, want, dtype, k_cache.device)
     elif _off(v_out, dtype, gpu) or v_out.shape != want:
         raise SvwError(f"v_out must be a contiguous {dtype} tensor of {want} on cuda:{gpu}")
-    rc = lib().kv_gather(cache, code, _addr(k_scale), _addr(v_scale), N, cu_out.data_ptr(), total_out, _addr(first),
+    rc = lib().kv_gather(cache, code, k_scale, v_scale, N, cu_out.data_ptr(), total_out, _addr(first),
                          k_out.data_ptr(), v_out.data_ptr(), out_code, _addr(status), _stream_of(stream, gpu))
     if rc:
         _check(rc)
@@ -900,7 +900,7 @@ def paged_attention_fp8(q, k_cache, v_cache, block_table, cu_new, kv_len, *, k_s
         _need_like(gpu, i32, ("cu_new", "kv_len", "status"), (cu_new, kv_len, status))
     if kv_len.numel() != N:
         raise SvwError(f"kv_len must have {N} elements")
-    _scales(k_scale, v_scale, heads, SVW_E4M3, gpu)
+    k_scale, v_scale = _scale("k_scale", k_scale, heads, SVW_E4M3, gpu), _scale("v_scale", v_scale, heads, SVW_E4M3, gpu)
     if out is None:
         out = _empty(stream, gpu, qh, bf16, q.device)
     elif _off(out, bf16, gpu) or out.shape != qh:
@@ -916,7 +916,7 @@ def paged_attention_fp8(q, k_cache, v_cache, block_table, cu_new, kv_len, *, k_s
     elif _off(workspace, torch.uint8, gpu):
         raise SvwError(f"workspace must be a contiguous uint8 tensor on cuda:{gpu}")
     rc = lib().paged_attention_fp8(q.data_ptr(), qs[0], qs[1], SVW_BF16, hq, N, cu_new.data_ptr(), T,
-                                   kv_len.data_ptr(), cache, _addr(k_scale), _addr(v_scale),
+                                   kv_len.data_ptr(), cache, k_scale, v_scale,
                                    float(dim ** -0.5 if scale is None else scale), 1 if causal else 0, int(window),
                                    out.data_ptr(), _addr(lse), _addr(status), workspace.data_ptr(), workspace.numel(),
                                    _stream_of(stream, gpu))

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) gather_any(const __grid_constant__ G
 
 template <typename C, typename O>
 void launch(GatherArgs a, cudaStream_t st) {
-  constexpr int E = 16 / sizeof(C), kItems = 4;
+  constexpr int E = 16 / sizeof(C), kItems = 2;
   int64_t odd = a.D;
   for (int d = 0; d < 3; ++d) odd |= a.kc[d] | a.vc[d];
   if (!at16(a.k_cache) || !at16(a.v_cache) || !at16(a.k_out) || !at16(a.v_out) || odd % E != 0) {

@@ -747,3 +747,101 @@ def test_beyond_32_bits_of_the_cache():
     _check_gather(new, [0, 0], table, kc, ks, got)
     assert bool(((got / ks[:, None] - want).abs() <= 1.001 * 2.0 ** -4 * want.abs() + 2.0 ** -10 * 1.001).all())
     _check_attend(new, kv, out, kc, vc, table, ks, vs, {})
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (8, 2, 64), (10, 2, 128), (5, 5, 64)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attend_fp8_units_of_any_number_of_rows(hq, hkv, d, causal):
+    """Requests of 1 to 33 tokens: row tiles on either side of the 64 rows up to
+    which a CTA's second worker takes other lanes, many to a worker."""
+    rng = np.random.default_rng(hq + d)
+    new = [int(n) for n in rng.permutation(np.arange(1, 34)).repeat(3)]
+    kv = [int(n + rng.integers(0, 700)) for n in new]
+    kc, vc, table, ks, vs = _codes(rng, new, kv, hkv, d, 32)
+    q = _queries(rng, new, hq, d)
+    _check_attend(new, kv, q, kc, vc, table, ks, vs, {"causal": causal})
+
+
+@pytest.mark.parametrize("n,kv,hq", [(1, 60000, 8), (20, 30000, 4), (150, 9000, 4)])
+def test_attend_fp8_on_two_streams_without_a_wait(n, kv, hq):
+    """Calls that make their own workspaces, in turn on the current stream and on
+    another, the second before the first has ended: neither disturbs the other."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    rng = np.random.default_rng(n)
+    kc, vc, table, ks, vs = _codes(rng, [n], [kv], 2, 128, 64)
+    rest = (kc, vc, _i32(table), _i32([0, n]), _i32([kv]))
+    qs = [_queries(rng, [n], hq, 128) for _ in range(2)]
+    call = lambda q, **o: svw.paged_attention_fp8(q, *rest, k_scale=ks, v_scale=vs, **o)
+    want = [call(q) for q in qs]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(10):
+        got = [call(qs[0]), call(qs[1], stream=side)]
+        torch.cuda.synchronize()
+        for (o, l), (wo, wl) in zip(got, want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+@pytest.mark.parametrize("new,kv", [([1, 3], [40, 900]), ([300, 20, 1], [300, 500, 9])])
+def test_append_norm_and_gather_captured_and_on_another_stream(new, kv):
+    """Captured and replayed with other tokens, and on another stream: what fresh
+    calls give."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    rng = np.random.default_rng(31)
+    hq, hkv, d = 8, 2, 128
+    kc, vc, table = _cache(rng, [0] * len(new), kv, hkv, d, 16, _dt("e4m3"), fill="nan")
+    q, k, v = _append_inputs(rng, new, hq, hkv, d, _dt("bf16"))
+    ks, vs = _scales(rng, hkv)
+    w, cs = _f32(rng.normal(1, 0.3, d)), _f32(rng.normal(size=(max(kv), d)))
+    where = (kc, vc, _i32(table))
+    cu, lens, first = _i32(_cu(new)), _i32(kv), _i32([t - n for t, n in zip(kv, new)])
+    qo = torch.empty_like(q)
+    ko, vo = (torch.empty(sum(new), hkv, d, device="cuda") for _ in range(2))
+
+    def both(stream=None, caches=where, out=(None, None, None)):
+        kw = dict(k_scale=ks, v_scale=vs, stream=stream)
+        r = svw.kv_append_norm(k, v, *caches, cu, lens, k_weight=w, q_weight=w, cos_sin=cs, q=q, q_out=out[0], **kw)
+        return (r, *svw.kv_gather(*caches, cu, first=first, total_out=sum(new), dtype=torch.float32, k_out=out[1],
+                                  v_out=out[2], **kw))
+
+    both(out=(qo, ko, vo))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        both(out=(qo, ko, vo))
+    side = torch.cuda.Stream()
+    for _ in range(4):
+        for x in (q, k, v):
+            x.mul_(-0.9)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        other = (torch.empty_like(kc), torch.empty_like(vc), where[2])
+        fresh = both(caches=other)
+        torch.cuda.synchronize()
+        beside = both(stream=side, caches=other)
+        torch.cuda.synchronize()
+        for a, b, c in zip((qo, ko, vo), fresh, beside):
+            assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_gather_beyond_31_bits_of_the_outputs():
+    """Outputs whose elements lie beyond 2^31, many tokens from one page."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    hkv, d, page = 16, 128, 16
+    n = (1 << 31) // (hkv * d) + 50
+    rng = np.random.default_rng(1)
+    kc, vc, _ = _cache(rng, [0], [32], hkv, d, page, _dt("e4m3"))
+    pages = -(-n // page)
+    table = np.zeros((1, pages), np.int32)
+    table[0, -2:] = [1, 0]
+    kc[:2], vc[:2] = (torch.randn(2, hkv, page, d, device="cuda").to(_dt("e4m3")) for _ in range(2))
+    k, v = svw.kv_gather(kc, vc, _i32(table), _i32([0, n]), total_out=n)
+    for c, out in ((kc, k), (vc, v)):
+        flat = c[:2].float().transpose(1, 2).to(torch.bfloat16)
+        last = (pages - 2) * page
+        assert torch.equal(out[last:last + page], flat[1]) and torch.equal(out[last + page:], flat[0][:n - last - page])
+        assert torch.equal(out[:page], flat[0])
