@@ -1,5 +1,6 @@
-// attention.cu -- attention of a chunk of new tokens over a paged cache
-// (paged_attention).
+// attention.cuh -- attention of a chunk of new tokens over a paged cache, of bf16
+// (paged_attention, attention.cu) or of e4m3 codes with a scale for each key head
+// (paged_attention_fp8, attention_fp8.cu).
 //
 // New token t of request i and query head h see keys j in [lo, hi):
 //   hi = causal ? min(kv_len, p + 1) : kv_len,  lo = window ? max(0, p + 1 - window) : 0,
@@ -54,6 +55,36 @@
 // and O multiplied by 2^(M - M').  P is rounded to bf16, the operand type of
 // the second product; l sums the unrounded weights in fp32.
 //
+// Codes (kF8).  The products take the codes as they lie (kind::f8f6f4, e4m3 for
+// both operands), so that a tile is loaded as half the bytes and nothing is
+// decoded; with K = k_scale k and V = v_scale v the scales are factors of a
+// row's scores and of its outputs.  A query and a weight have eight bits in bf16,
+// a code four: each enters as two numbers, the code nearest to it and the code
+// nearest to what is left, and both products go into one accumulator.  That is
+// as many products as bf16's, each of twice the elements.  A query's row is
+// brought to [128, 256) by a power of two that its scores are divided by again,
+// so its numbers are exact down to 2^-10 of the largest.  A weight's second
+// number ends at 2^-10, so the reference lies 5 below the maximum when it is set
+// and at most 8.75 later: weights up to 430 of e4m3's 448, and within 2^-15 of
+// the row's largest where eight bits end (error against 64 bits 0.0018 of the
+// output's norm; rounding it to bf16 alone gives 0.0017; the first numbers alone
+// would leave 2^-4 of every weight).  Queries are split in place, by the softmax
+// warps, a row a lane.
+// Measured (us, as above): decoding 130 (5.4 TB/s), 2108 new tokens 319, 17
+// tokens over 131000 keys 68, two prompts 458 to 467 (1340 TFLOP/s), 128 blocks of
+// 16 tokens, 16 heads of 64, over 200 to 2000 keys 88.  What bounds it: the narrow
+// form's chain of products and softmax, no longer the bytes.  One live warp of
+// each worker used to share a scheduler (1660 cycles a tile of 64 keys, 1560 of
+// them that warp's: 146); now the second worker's few rows lie in other lanes
+// (137), and a tile's outputs and the next scores are issued in one piece (130);
+// with half of the score products (and wrong scores) it would take 117, without
+// exponentials 129.  Copies of few rows in all warps' lanes, each warp with its
+// part of a tile's keys, were slower (64 keys a tile 154; 128, with one score
+// buffer, 139, and 2108 tokens 448), as were the next unit's queries split ahead
+// of a unit's outputs (blocks of 16 tokens 93 instead of 88) or by the warps
+// without rows (102; decoding 126).  Wide, the conversions of the weights share the
+// ALU pipe with the maxima (weights 1200 cycles of a tile, bf16's 775).
+//
 // Masks are ranges of places: scores outside [lo, hi) become -inf by
 // selection (their products may be anything), key tiles and pages that no row
 // of the unit sees are never loaded, value rows beyond kv_len in the last tile,
@@ -94,7 +125,8 @@ struct Shape {
   static constexpr int kBufs = kWide ? 1 : 2;              // score buffers of a stage
   static constexpr bool kApart = kWide && D == 64;         // weights in columns of their own, not over their scores
   static constexpr int kSoftWarps = kWide ? 8 : 4;         // softmax warps of a worker
-  // a unit's fixed cost on the line, in key tiles (one or three: 10 prompts of 1 to 1275 tokens 92 or 83 us instead
+  // a unit's fixed cost on the line, in key tiles (codes, narrow: two 339 and 109 us, four 327 and 104, six 332 and 110,
+  // 2108 tokens and blocks of 16; bf16 with one or three: 10 prompts of 1 to 1275 tokens 92 or 83 us instead
   // of 85, 117 requests of 68 tokens 300 or 305 instead of 299; narrow with three, 2220 tokens 452 instead of 448)
   static constexpr int kUnitCost = kF8 && !kWide ? 4 : 2;
   static constexpr int kQHalves = D / 64;                  // 128-byte columns of a query tile

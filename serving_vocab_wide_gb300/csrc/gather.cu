@@ -1,5 +1,9 @@
 // gather.cu -- cached keys and values of many requests read back, packed
 // (kv_gather): out = code x scale of the head in fp32, rounded once.
+//
+// A copy, bound by DRAM for many tokens: 333 k tokens of 8 heads of 128, codes to
+// bf16, 2.04 GB, in 345 us (5.9 TB/s of 6.8; a third of it is read, two thirds
+// written), 777 tokens in 3.9.  (A block per token, entry by entry: 2520.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -84,7 +88,8 @@ __device__ __forceinline__ void put(float *dst, const float (&f)[E]) {
 
 // A block has a tile of tokens: its first warp finds them, then a thread has one
 // 16-byte vector of keys or values (or every blockDim.x-th) of every
-// blockDim.y-th token, kItems of them under way.  Everything 16-byte aligned.
+// blockDim.y-th token, kItems of them under way (two: 345 us, four 355, eight
+// 367).  Everything 16-byte aligned.
 template <typename C, typename O, int kItems>
 __global__ void __launch_bounds__(kThreads) gather_vec(const __grid_constant__ GatherArgs a) {
   constexpr int E = 16 / sizeof(C);
