@@ -354,9 +354,10 @@ void launch(AppendNormArgs a, cudaStream_t st) {
   a.inv_dim = 1.f / static_cast<float>(a.D);
   const int slots = vec ? a.D / (2 * N) : 64;
   while ((1 << a.lane_bits) < slots) ++a.lane_bits;
-  // few tokens, less than two tasks a warp: a round a task, the shortest way through (one token 3.2 us, as with two)
+  // As long as all tasks of one round fit the SMs at once (three blocks each), a round a task is the shortest way
+  // through: of 48 heads of 128, 1 token 3.3 us (rounds in twos 3.8), 300 tokens 4.5 (4.6), 400 5.4 (4.7).
   const int round = 32 >> a.lane_bits;
-  const int items = a.T * (a.Hq + 2 * a.Hkv) < 2 * kSms * kWarps * round * 2 ? 1 : 2;
+  const int items = a.T * (a.Hq + 2 * a.Hkv) < 3 * kSms * kWarps * round ? 1 : 2;
   const int each = items * std::max(round, 1);
   a.kv_tasks = (a.Hkv + each - 1) / each;
   a.tasks = 2 * a.kv_tasks + (a.Hq + each - 1) / each;

@@ -96,6 +96,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cstdint>
 #include <mutex>
 #include <type_traits>
@@ -1098,6 +1099,7 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
       if (warp_live) {
         if (!(ok = warp_wait(&sm.q_full[kWide ? 0 : s], par(k)))) break;
         k2 = a.scale * kLog2e * head_scale(a.k_scale, g.hk, a.status) * split_query<D>(q_ptr, q_row);
+        if (k2 < FLT_MIN) k2 = FLT_MIN;  // zero times a hidden score's infinity; such scores are zero either way
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       __syncwarp();

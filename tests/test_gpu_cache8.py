@@ -845,3 +845,17 @@ def test_gather_beyond_31_bits_of_the_outputs():
         last = (pages - 2) * page
         assert torch.equal(out[last:last + page], flat[1]) and torch.equal(out[last + page:], flat[0][:n - last - page])
         assert torch.equal(out[:page], flat[0])
+
+
+@pytest.mark.parametrize("new,kv", [([3, 1], [300, 70]), ([150, 40], [700, 300])])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attend_fp8_scores_that_vanish(new, kv, d):
+    """Queries of zeros and scales so small that a score's factor would be zero:
+    the hidden keys stay hidden, the weights of the others are equal."""
+    import torch
+    rng = np.random.default_rng(37)
+    kc, vc, table, _, vs = _codes(rng, new, kv, 2, d, 32)
+    q = _queries(rng, new, 4, d)
+    q[::2] = 0
+    q[1::2] *= 1e-37
+    _check_attend(new, kv, q, kc, vc, table, torch.full((2,), 1e-30, device="cuda"), vs, {})
