@@ -1095,10 +1095,13 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
     const bool live = tok_of_row < (tile ? g.ntok1 : g.ntok0);
     const bool warp_live = __any_sync(0xffffffffu, live);
     if (!live) hi = INT32_MAX, lo = 0;  // rows of no token: never masked, never looked at
+    float vs = 1.f;
     if (kF8) {
+      const float ks = head_scale(a.k_scale, g.hk, a.status);
+      vs = head_scale(a.v_scale, g.hk, a.status);
       if (warp_live) {
         if (!(ok = warp_wait(&sm.q_full[kWide ? 0 : s], par(k)))) break;
-        k2 = a.scale * kLog2e * head_scale(a.k_scale, g.hk, a.status) * split_query<D>(q_ptr, q_row);
+        k2 = a.scale * kLog2e * ks * split_query<D>(q_ptr, q_row);
         if (k2 < FLT_MIN) k2 = FLT_MIN;  // zero times a hidden score's infinity; such scores are zero either way
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
@@ -1224,7 +1227,6 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
       const int32_t tok = g.tok0 + tile * a.tile_tokens + tok_of_row;
       const int32_t orow = live ? tok * a.Hq + g.hk * G + head_of_row : -1;  // below 2^31, checked by the host
       const int64_t prow = static_cast<int64_t>(max(g.part, 0)) * a.part_rows + tile * kRows + q_row;
-      const float vs = kF8 ? head_scale(a.v_scale, g.hk, a.status) : 1.f;
       const float inv = (g.part >= 0) ? 1.f : (l == 0.f ? 0.f : vs / l);
       int32_t to[4];  // the rows of this lane's four, and its piece of each
 #pragma unroll
