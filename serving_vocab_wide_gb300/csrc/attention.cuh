@@ -65,7 +65,7 @@
 // brought to [128, 256) by a power of two that its scores are divided by again,
 // so its numbers are exact down to 2^-10 of the largest.  A weight's second
 // number ends at 2^-10, so the reference lies 5 below the maximum when it is set
-// and at most 8.75 later: weights up to 430 of e4m3's 448, and within 2^-15 of
+// and at most 8.5 later: weights up to 362 of e4m3's 448, and within 2^-15 of
 // the row's largest where eight bits end (error against 64 bits 0.0018 of the
 // output's norm; rounding it to bf16 alone gives 0.0017; the first numbers alone
 // would leave 2^-4 of every weight).  Queries are split in place, by the softmax
@@ -118,8 +118,9 @@ constexpr float kNaN = __builtin_nanf("");
 
 template <int D, bool kWide, bool kF8>
 struct Shape {
-  // the reference lies kLift below the maximum when it is set, and at most kGrow below it later (base 2)
-  static constexpr float kLift = kF8 ? 5.f : 0.f, kGrow = kF8 ? 8.75f : 8.f;
+  // the reference lies kLift below the maximum when it is set, and at most kGrow below it later (base 2); codes: a row
+  // whose maximum is beyond kFar is NaN (a score is known to 2^-2 there)
+  static constexpr float kLift = kF8 ? 5.f : 0.f, kGrow = kF8 ? 8.5f : 8.f, kFar = 0x1p22f;
   static constexpr int kWorkers = kWide ? 1 : 2;           // of a CTA
   static constexpr int kKeys = kWide ? 128 : 64;           // keys of a tile
   static constexpr int kTiles = kWide ? 2 : 1;             // row tiles of a unit, at most
@@ -1141,9 +1142,11 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
 #pragma unroll
         for (int v = 0; v < 4; ++v) mx[v] = fmaxf(mx[v], x[Sh::kKeys - 4 + v]);
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * k2;
-        const bool grow = live && (top > M + Sh::kGrow || (M == -INFINITY && top > M));
+        // (codes: by the difference, which is exact; a maximum beyond kFar, whose rounding alone could take the weights
+        // out of their range, is refused: scores rounded as it was, 3 to 8% slower throughout, would have to stand for it)
+        const bool grow = live && ((kF8 ? top - M > Sh::kGrow : top > M + Sh::kGrow) || (M == -INFINITY && top > M));
         const float f = grow ? (M == -INFINITY ? 0.f : ex2(M - (top - Sh::kLift))) : 1.f;
-        if (grow) M = top - Sh::kLift;
+        if (grow) M = (kF8 && fabsf(top) > Sh::kFar) ? kNaN : top - Sh::kLift;
         l *= f;
         const float ref = (M == -INFINITY) ? 0.f : M;
         const float2 kk = make_float2(k2, k2), nr = make_float2(-ref, -ref);

@@ -859,3 +859,30 @@ def test_attend_fp8_scores_that_vanish(new, kv, d):
     q[::2] = 0
     q[1::2] *= 1e-37
     _check_attend(new, kv, q, kc, vc, table, torch.full((2,), 1e-30, device="cuda"), vs, {})
+
+
+@pytest.mark.parametrize("new", [3, 150])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 12, -2.0 ** 12, 2.0 ** 15, -2.0 ** 15, 2.0 ** 100])
+def test_attend_fp8_far_scores(new, d, size):
+    """Scores of millions, thousands apart: the largest alone counts, however its
+    maximum was reached; beyond what the call takes the rows are NaN."""
+    import torch
+    kv, page = 400, 16
+    code = lambda *s: torch.zeros(*s, device="cuda").to(_dt("e4m3"))
+    pages = -(-kv // page)
+    kc, vc = code(pages, 1, page, d), code(pages, 1, page, d)
+    up = torch.arange(pages * page, device="cuda").view(pages, 1, page)
+    at = (448 - 32 * (up * 5 % 7)).float()  # up and down, in steps of e4m3's
+    kc[..., 0] = at.to(_dt("e4m3"))
+    best = at.max() if size > 0 else at.min()
+    vc[..., :] = torch.where(at[..., None] == best, 2.0, 1.0).expand(vc.shape).to(_dt("e4m3"))
+    q = torch.zeros(new, 2, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = size
+    out, lse = _attend([new], [kv], q, kc, vc, np.arange(pages)[None].astype(np.int32), None, None,
+                       {"scale": 1.0, "causal": False})
+    top = float(best) * size
+    if abs(top) > 2.9e6:
+        assert bool(out.isnan().all()) and bool(lse.isnan().all())
+    else:
+        assert bool((out == 2).all()) and bool(((lse - top).abs() <= 2.0 ** -22 * abs(top) + 6).all())
