@@ -83,7 +83,9 @@
 // buffer, 139, and 2108 tokens 448), as were the next unit's queries split ahead
 // of a unit's outputs (blocks of 16 tokens 93 instead of 88) or by the warps
 // without rows (102; decoding 126).  Wide, the conversions of the weights share the
-// ALU pipe with the maxima (weights 1200 cycles of a tile, bf16's 775).
+// ALU pipe with the maxima (weights 1200 cycles of a tile, bf16's 775); half of a
+// tile's outputs issued beside the other half's softmax took 457 instead of 464,
+// not worth its barriers.
 //
 // Masks are ranges of places: scores outside [lo, hi) become -inf by
 // selection (their products may be anything), key tiles and pages that no row
