@@ -603,8 +603,8 @@ svw_status paged_attention(const void *q, int64_t q_token_stride, int64_t q_head
  *   k_scale, v_scale  device float [n_kv_heads], normal numbers > 0; NULL: 1.
  *                Another number: the query heads of that key head become NaN,
  *                and SVW_DEV_BAD_INPUT.
- * A query with a NaN or an infinity becomes NaN throughout, as does one whose
- * largest score is beyond 2.9 million in magnitude.  Scores and sums are
+ * A query with a NaN or an infinity becomes NaN throughout, as one with scores
+ * beyond 2.9 million in magnitude may (and does if its largest is).  Scores and sums are
  * fp32; a query enters its products as two e4m3 numbers under a scale of its
  * own, which is exact down to 2^-10 of its largest element (and within 2^-17 of
  * that one below), and the weights as two, which is as near as bf16 down to 2^-7
