@@ -55,37 +55,37 @@
 // and O multiplied by 2^(M - M').  P is rounded to bf16, the operand type of
 // the second product; l sums the unrounded weights in fp32.
 //
-// Codes (kF8).  The products take the codes as they lie (kind::f8f6f4, e4m3 for
-// both operands), so that a tile is loaded as half the bytes and nothing is
-// decoded; with K = k_scale k and V = v_scale v the scales are factors of a
-// row's scores and of its outputs.  A query and a weight have eight bits in bf16,
-// a code four: each enters as two numbers, the code nearest to it and the code
-// nearest to what is left, and both products go into one accumulator.  That is
-// as many products as bf16's, each of twice the elements.  A query's row is
+// Codes (kF8).  With K = k_scale k and V = v_scale v the scales are factors of a
+// row's scores and of its outputs.  The first product takes the keys' codes as
+// they lie (kind::f8f6f4, e4m3 for both operands).  A query has eight bits in
+// bf16, a code four: it enters as two numbers, the code nearest to it and the
+// code nearest to what is left, and both products go into one accumulator.  That
+// is as many products as bf16's, each of twice the elements.  A query's row is
 // brought to [128, 256) by a power of two that its scores are divided by again,
-// so its numbers are exact down to 2^-10 of the largest.  A weight's second
-// number ends at 2^-10, so the reference lies 5 below the maximum when it is set
-// and at most 8.5 later: weights up to 362 of e4m3's 448, and within 2^-15 of
-// the row's largest where eight bits end (error against 64 bits 0.0018 of the
-// output's norm; rounding it to bf16 alone gives 0.0017; the first numbers alone
-// would leave 2^-4 of every weight).  Queries are split in place, by the softmax
-// warps, a row a lane.
-// Measured (us, as above): decoding 130 (5.4 TB/s), 2108 new tokens 319, 17
-// tokens over 131000 keys 68, two prompts 458 to 467 (1340 TFLOP/s), 128 blocks of
-// 16 tokens, 16 heads of 64, over 200 to 2000 keys 88.  What bounds it: the narrow
-// form's chain of products and softmax, no longer the bytes.  One live warp of
+// so its numbers are exact down to 2^-9 of the largest (2^-10 where that is near
+// 256).  Queries are split in place, by the softmax warps, a row a lane.
+// The second product takes fp16 (kind::f16): a value's code is exact in it, and
+// is decoded in shared memory, by warps of their own, two tiles ahead.  A weight
+// has 11 bits in fp16 as far down as 2^-14, and steps of 2^-24 below: the
+// reference lies 7 below the maximum when it is set and at most 15 later, so a
+// weight keeps 11 bits down to 2^-21 of the row's largest and is off by 2^-32 of
+// it below, which 2^17 keys add up to 2^-15.  (Weights as two e4m3 numbers, which
+// multiply the codes as they lie, end at 2^-15 of the largest: a first key 11
+// nats above 16000 others lost 0.4 of the output, and the second number in e5m2
+// keeps three bits there, 2^-4 of a tail of equal weights.)
+// Measured (us, as above): decoding 129 (5.4 TB/s), 2108 new tokens 299 to 310, 17
+// tokens over 131000 keys 66 to 68, two prompts 397 to 401 (1545 TFLOP/s), 128
+// blocks of 16 tokens, 16 heads of 64, over 200 to 2000 keys 88.  What bounds the narrow
+// form: its chain of products and softmax, no longer the bytes.  One live warp of
 // each worker used to share a scheduler (1660 cycles a tile of 64 keys, 1560 of
-// them that warp's: 146); now the second worker's few rows lie in other lanes
-// (137), and a tile's outputs and the next scores are issued in one piece (130);
-// with half of the score products (and wrong scores) it would take 117, without
-// exponentials 129.  Copies of few rows in all warps' lanes, each warp with its
-// part of a tile's keys, were slower (64 keys a tile 154; 128, with one score
-// buffer, 139, and 2108 tokens 448), as were the next unit's queries split ahead
-// of a unit's outputs (blocks of 16 tokens 93 instead of 88) or by the warps
-// without rows (102; decoding 126).  Wide, the conversions of the weights share the
-// ALU pipe with the maxima (weights 1200 cycles of a tile, bf16's 775); half of a
-// tile's outputs issued beside the other half's softmax took 457 instead of 464,
-// not worth its barriers.
+// them that warp's); now the second worker's few rows lie in other lanes, a tile's
+// outputs and the next scores are issued in one piece (146 us otherwise), and the
+// decoders keep off their worker's issuer (one on its scheduler 138 us). Two
+// decoders a worker take 128.7, 310, 66 and 87.6 us, one 130.6, 305, 68 and 93.
+// (Decoding by shifts and masks, 36 instructions instead of the 8 conversions of
+// 16 codes, took 194 us, loads and stores that take turns 172.)  Copies of few rows
+// in all warps' lanes, each warp with its part of a tile's keys, were slower, as
+// were the next unit's queries split ahead of a unit's outputs.
 //
 // Masks are ranges of places: scores outside [lo, hi) become -inf by
 // selection (their products may be anything), key tiles and pages that no row
@@ -95,6 +95,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -113,26 +114,28 @@ namespace {
 
 constexpr int kRows = 128;     // rows of a score tile (the MMA's M)
 constexpr int kSegRing = 4;
-constexpr int kThreads = 384;  // loaders and issuers; two softmax warpgroups, one a stage
 constexpr int kMaxGrid = 152;  // CTAs: one per SM
 
 constexpr float kNaN = __builtin_nanf("");
 
 template <int D, bool kWide, bool kF8>
 struct Shape {
-  // the reference lies kLift below the maximum when it is set, and at most kGrow below it later (base 2); codes: a row
-  // whose maximum is beyond kFar is NaN (a score is known to 2^-2 there)
-  static constexpr float kLift = kF8 ? 5.f : 0.f, kGrow = kF8 ? 8.5f : 8.f, kFar = 0x1p22f;
+  // the reference lies kLift below the maximum when it is set, and at most kGrow below it later (base 2; codes: fp16
+  // ends below 2^16); codes: a row whose maximum is beyond kFar is NaN (a score is known to 2^-2 there)
+  static constexpr float kLift = kF8 ? 7.f : 0.f, kGrow = kF8 ? 15.f : 8.f, kFar = 0x1p22f;
   static constexpr int kWorkers = kWide ? 1 : 2;           // of a CTA
   static constexpr int kKeys = kWide ? 128 : 64;           // keys of a tile
   static constexpr int kTiles = kWide ? 2 : 1;             // row tiles of a unit, at most
   static constexpr int kBufs = kWide ? 1 : 2;              // score buffers of a stage
   static constexpr bool kApart = kWide && D == 64;         // weights in columns of their own, not over their scores
   static constexpr int kSoftWarps = kWide ? 8 : 4;         // softmax warps of a worker
-  // a unit's fixed cost on the line, in key tiles (codes, narrow: two 339 and 109 us, four 327 and 104, six 332 and 110,
+  static constexpr int kDecoders = !kF8 ? 0 : kWide ? 1 : 2;  // warps of a worker that decode values
+  // loaders and issuers (wide, codes: and the decoder); two softmax warpgroups, one a stage; narrow, codes: the decoders
+  static constexpr int kThreads = kF8 && !kWide ? 512 : 384;
+  // a unit's fixed cost on the line, in key tiles (codes, narrow: three 315 and 96 us, four 313 and 92, six 311 and 88,
   // 2108 tokens and blocks of 16; bf16 with one or three: 10 prompts of 1 to 1275 tokens 92 or 83 us instead
   // of 85, 117 requests of 68 tokens 300 or 305 instead of 299; narrow with three, 2220 tokens 452 instead of 448)
-  static constexpr int kUnitCost = kF8 && !kWide ? 4 : 2;
+  static constexpr int kUnitCost = kF8 && !kWide ? 6 : 2;
   static constexpr int kQHalves = D / 64;                  // 128-byte columns of a query tile
   static constexpr int kQTile = kRows * D * 2;             // its bytes
   static constexpr int kQHalf = kRows * 128;               // those of one of its columns
@@ -143,9 +146,13 @@ struct Shape {
   static constexpr int kRowBytes = kF8 ? D : 128;          // of a column's row: the swizzle's width
   static constexpr int kHalf = kKeys * kRowBytes;
   static constexpr int kTile = kHalves * kHalf;
-  static constexpr int kRing = ((D == 128) ? 5 : 11) * (kF8 ? 2 : 1);  // key and value tiles in flight of a worker
+  static constexpr int kVHalf = kKeys * 128;               // a column of a value tile as the product takes it
+  static constexpr int kVTile = D / 64 * kVHalf;
+  static constexpr int kVBufs = kF8 ? 2 : 0;               // decoded value tiles of a worker
+  static constexpr int kRing = D == 128 ? (kF8 ? 6 : 5) : (kF8 ? 18 : 11);  // key and value tiles in flight of a worker
+  static constexpr int kWorkerBytes = kRing * kTile + kVBufs * kVTile;
   static constexpr int kControl = (D == 128 ? 3 : 4) << 10;  // a whole number of swizzle atoms
-  static constexpr int kSmem = kControl + 2 * kQTile + kWorkers * kRing * kTile;
+  static constexpr int kSmem = kControl + 2 * kQTile + kWorkers * kWorkerBytes;
   // columns of tensor memory: scores of stage st, buffer u at st * 128 + u * 64; outputs at 256 + st * D; weights:
   __host__ __device__ static constexpr int weights(int st, int u) { return kApart ? 384 + st * 64 : st * 128 + u * 64; }
 };
@@ -186,6 +193,7 @@ struct Control {
   Lane<kRing> lane[kWorkers];
   unsigned long long q_full[2], q_empty[2];
   unsigned long long q_ready[2];            // by stage (codes): its queries are split
+  unsigned long long v_full[4], v_empty[4];  // 2 * worker + buffer (codes): decoded values
   unsigned long long s_full[4], p_full[4];  // 2 * stage + score buffer
   unsigned long long s_read[2];             // by stage (apart): the scores are in registers
   unsigned long long o_full[2], o_free[2], o_step[2];  // by stage: a segment's outputs; read; each tile's (narrow, apart)
@@ -286,22 +294,6 @@ __device__ __forceinline__ void mma_ts_x4(uint32_t d, uint32_t a, uint64_t b, ui
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-// over 64 keys of codes: A's first numbers, then its second ones, in 16 columns each; kRows32 16-byte units are 32 rows of B
-template <int kRows32>
-__device__ __forceinline__ void mma_ts_twice(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b32 x;\n\t.reg .b64 y;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tmov.b32 x, %1;\n\tadd.s64 y, %2, %5;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [x], %2, %3, p;\n\t"
-      "add.u32 x, x, 8;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [x], y, %3, 1;\n\t"
-      "add.u32 x, x, 8;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [x], %2, %3, 1;\n\t"
-      "add.u32 x, x, 8;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [x], y, %3, 1;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc), "n"(kRows32)
-      : "memory");
-}
 // one thread of a converged warp, always the same
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -351,7 +343,7 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // offset >> 4 (32-45), version (46), swizzle mode 2 = 128-byte (61-63).
 // K-major (queries, keys: rows of 64 elements of the head): the stride offset
 // is the 1024 bytes between eight-row atoms, the leading one is not used.
-// MN-major (values: rows of 64 elements along N, eight keys an atom): the
+// MN-major (values, codes' as fp16: rows of 64 elements along N, eight keys an atom): the
 // stride offset is the 1024 bytes between atoms along K (the keys), the
 // leading one the distance of the halves along N.
 // A tile of 64 codes a row is 64-byte-swizzled (mode 4), its atoms 512 bytes.
@@ -363,15 +355,21 @@ __device__ __forceinline__ uint64_t sw128(uint32_t saddr, uint32_t lead) {
   return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
          (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
-// Instruction descriptor: fp32 D (bits 4-5), A and B (7-9, 10-12; bf16 is 1 of
-// kind::f16, e4m3 0 of kind::f8f6f4), B MN-major (16), N >> 3 (17-22), M >> 4 (24-28).
-__host__ __device__ constexpr uint32_t idesc(int N, bool b_mn, bool f8) {
-  return (1u << 4) | (f8 ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? (1u << 16) : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+// Instruction descriptor: fp32 D (bits 4-5), A and B (7-9, 10-12; bf16 is 1 and
+// fp16 0 of kind::f16, e4m3 0 of kind::f8f6f4), B MN-major (16), N >> 3 (17-22), M >> 4 (24-28).
+__host__ __device__ constexpr uint32_t idesc(int N, bool b_mn, bool bf16) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? (1u << 16) : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(kRows >> 4) << 24);
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
@@ -597,7 +595,8 @@ __device__ __forceinline__ void load_worker(const CUtensorMap &tmQ, const CUtens
 template <int D, bool kWide, bool kF8, typename C>
 __device__ __forceinline__ void issue_worker(C &sm, int wk, int G, uint32_t q_smem, uint32_t ring, uint32_t tmem) {
   using Sh = Shape<D, kWide, kF8>;
-  constexpr uint32_t id_s = idesc(Sh::kKeys, false, kF8), id_o = idesc(D, true, kF8);
+  constexpr uint32_t id_s = idesc(Sh::kKeys, false, !kF8), id_o = idesc(D, true, !kF8);
+  const uint32_t decoded = ring + Sh::kRing * Sh::kTile;
   auto &ln = sm.lane[wk];
   // a place in the ring: slot and parity of its next completion
   struct At {
@@ -612,10 +611,15 @@ __device__ __forceinline__ void issue_worker(C &sm, int wk, int G, uint32_t q_sm
     }
   };
   At kt = {0, 0}, vt = {1, 0};
-  int32_t k = 0, sc[2] = {0, 0};
+  int32_t k = 0, vc = 0, sc[2] = {0, 0};  // segments; value tiles; score tiles
   uint32_t q_rows = 0;  // the bytes that the tile's rows lie behind the first lane's
   bool ok = true;
   auto wait_ring = [&](const At &t) { return ok = ok && warp_wait(&ln.full[t.slot], t.parity); };
+  auto wait_values = [&] { return kF8 ? (ok = ok && warp_wait(&sm.v_full[2 * wk + (vc & 1)], par(vc >> 1))) : wait_ring(vt); };
+  auto next_values = [&] {
+    ++vc;
+    vt.two_on();
+  };
   // by the elected thread: into score buffer u of stage st, from it into the stage's output
   auto scores = [&](int st, int u, const At &t) {
     const uint64_t qa = sw128(q_smem + (kWide ? st * Sh::kQTile : 0) - q_rows, 16);
@@ -630,20 +634,16 @@ __device__ __forceinline__ void issue_worker(C &sm, int wk, int G, uint32_t q_sm
     }
     tc_commit(smem_u32(&sm.s_full[2 * st + u]));
   };
-  auto output = [&](int st, int u, const At &t, bool acc) {
-    const uint32_t vs = ring + t.slot * Sh::kTile;
-    const uint64_t va = (kF8 && D == 64) ? sw64(vs) : sw128(vs, kF8 ? 16 : Sh::kHalf);
+  auto output = [&](int st, int u, bool acc) {
+    const uint32_t vs = kF8 ? decoded + (vc & 1) * Sh::kVTile : ring + vt.slot * Sh::kTile;
+    const uint64_t va = sw128(vs, Sh::kVHalf);
 #pragma unroll
-    for (int h = 0; h < Sh::kKeys / 64; ++h) {  // a row's weights of 64 keys take 32 columns
-      const uint32_t o = tmem + 256 + st * D, w = tmem + Sh::weights(st, u) + h * 32, more = (acc || h > 0) ? 1u : 0u;
-      if constexpr (kF8)
-        mma_ts_twice<2 * Sh::kRowBytes>(o, w, va + h * 4 * Sh::kRowBytes, id_o, more);
-      else
-        mma_ts_x4(o, w, va + h * 512, id_o, more);
-    }
+    for (int h = 0; h < Sh::kKeys / 64; ++h)  // a row's weights of 64 keys take 32 columns
+      mma_ts_x4(tmem + 256 + st * D, tmem + Sh::weights(st, u) + h * 32, va + h * 512, id_o, (acc || h > 0) ? 1u : 0u);
     if (!kWide || Sh::kApart) tc_commit(smem_u32(&sm.o_step[st]));
   };
   auto release = [&](const At &t) { tc_commit(smem_u32(&ln.empty[t.slot])); };
+  auto release_values = [&] { tc_commit(smem_u32(kF8 ? &sm.v_empty[2 * wk + (vc & 1)] : &ln.empty[vt.slot])); };
   while (ok) {
     const int sl = k % kSegRing;
     if (!(ok = warp_wait(&ln.seg_full[sl], par(k / kSegRing)))) break;
@@ -688,7 +688,7 @@ __device__ __forceinline__ void issue_worker(C &sm, int wk, int G, uint32_t q_sm
             if (i == 1 && j == max(0, n - 2)) tc_commit(smem_u32(&sm.q_empty[0]));
           }
         }
-        if (!ok || !wait_ring(vt)) break;
+        if (!ok || !wait_values()) break;
 #pragma unroll
         for (int i = 0; i < 2 && ok; ++i) {
           if (!(ok = warp_wait(&sm.p_full[2 * i], par(sc[i])))) break;
@@ -696,15 +696,15 @@ __device__ __forceinline__ void issue_worker(C &sm, int wk, int G, uint32_t q_sm
           if (j == 0 && k > 0 && !(ok = warp_wait(&sm.o_free[i], par(k - 1)))) break;
           tc_after();
           if (elect_one()) {
-            output(i, 0, vt, j > 0);
-            if (i == 1) release(vt);
+            output(i, 0, j > 0);
+            if (i == 1) release_values();
           }
         }
-        vt.two_on();
+        next_values();
         if (more) kt.two_on();
         continue;
       }
-      if (!wait_ring(vt)) break;
+      if (!wait_values()) break;
       if (kWide && more && !wait_ring(kt)) break;  // there long before; narrow: its values' weights come first
 #pragma unroll
       for (int i = 0; i < (kWide ? 2 : 1); ++i) {
@@ -716,9 +716,9 @@ __device__ __forceinline__ void issue_worker(C &sm, int wk, int G, uint32_t q_sm
         if (Sh::kOnePiece && (!more || __all_sync(0xffffffffu, mbar_try_wait(&ln.full[kt.slot], kt.parity)))) {
           tc_after();
           if (elect_one()) {
-            output(st, u, vt, j > 0);
+            output(st, u, j > 0);
             if (more) scores(st, u, kt);
-            release(vt);
+            release_values();
             if (more) release(kt);
             if (j == max(0, n - 3)) tc_commit(smem_u32(&sm.q_empty[wk]));
           }
@@ -726,8 +726,8 @@ __device__ __forceinline__ void issue_worker(C &sm, int wk, int G, uint32_t q_sm
         }
         tc_after();
         if (elect_one()) {
-          output(st, u, vt, j > 0);
-          if (!kWide || i == 1) release(vt);
+          output(st, u, j > 0);
+          if (!kWide || i == 1) release_values();
           if (kWide && more) {
             scores(st, 0, kt);
             if (i == 1) release(kt);
@@ -747,7 +747,7 @@ __device__ __forceinline__ void issue_worker(C &sm, int wk, int G, uint32_t q_sm
           }
         }
       }
-      vt.two_on();
+      next_values();
       if (more) kt.two_on();
     }
     if (!ok) break;
@@ -761,6 +761,85 @@ __device__ __forceinline__ void issue_worker(C &sm, int wk, int G, uint32_t q_sm
     ++k;
   }
   if (!ok && elect_one()) atomicOr(&sm.err, 1);
+}
+
+// ----------------------- the values' decoder (codes) ------------------------
+// Warps of a worker: each value tile of the ring as fp16 (exact), laid out as
+// the second product takes it (128-byte-swizzled columns of 64 elements), rows
+// beyond the request's keys as zeros; warp d has the d-th part of its rows.
+// A lane has 16 codes, two pieces of 16 bytes, of each load.  Eight lanes have
+// four loads of two rows, of rows of 128 codes r and r ^ 5, so that neither their
+// loads (bit 2) nor their stores (bit 0) meet a bank twice.
+template <int D, bool kWide, typename C>
+__device__ __forceinline__ void decode_worker(C &sm, int wk, int d, unsigned char *ring_ptr) {
+  using Sh = Shape<D, kWide, true>;
+  constexpr int kMine = Sh::kKeys / 8 / Sh::kDecoders;  // atoms of eight rows
+  constexpr int kRounds = D / 64;                       // the warp's loads of an atom
+  constexpr int kAhead = kWide ? 8 : 4;                 // loads under way
+  auto &ln = sm.lane[wk];
+  const int lane = threadIdx.x & 31, p = lane & 3;
+  unsigned char *decoded = ring_ptr + Sh::kRing * Sh::kTile;
+  int from[kRounds], to[kRounds][2];  // in an atom
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int h = D == 128 ? (lane >> 3) & 1 : 0;                                       // column
+    const int x = D == 128 ? ((lane >> 4) + 2 * i) ^ ((lane & 4) ? 5 : 0) : lane >> 2;  // row
+    from[i] = x * D + (((h * 4 + p) ^ (D == 128 ? x : x >> 1)) << 4);
+    for (int s = 0; s < 2; ++s) to[i][s] = h * Sh::kVHalf + x * 128 + (((2 * p + s) ^ x) << 4);
+  }
+  int32_t count = 0, k = 0;
+  bool ok = true;
+  while (true) {
+    const int sl = k % kSegRing;
+    if (!(ok = warp_wait(&ln.seg_full[sl], par(k / kSegRing)))) break;
+    const int32_t tiles = ln.seg[sl].tiles, key0 = ln.seg[sl].key0, kv = ln.seg[sl].kv;
+    __syncwarp();
+    if (tiles == 0) break;
+    if (lane == 0) mbar_arrive(&ln.seg_empty[sl]);
+    for (int32_t j = 0; j < tiles && ok; ++j, ++count) {
+      const int32_t t = 2 * count + 1, slot = t % Sh::kRing;
+      unsigned long long *empty = &sm.v_empty[2 * wk + (count & 1)], *full = &sm.v_full[2 * wk + (count & 1)];
+      if (!(ok = warp_wait(&ln.full[slot], par(t / Sh::kRing)))) break;
+      if (!(ok = count < 2 || warp_wait(empty, par((count >> 1) - 1)))) break;
+      const unsigned char *in = ring_ptr + slot * Sh::kTile + d * kMine * 8 * D;
+      unsigned char *out = decoded + (count & 1) * Sh::kVTile + d * kMine * 1024;
+      uint4 w[kAhead];
+      auto load = [&](int n, int q) { w[q] = *reinterpret_cast<const uint4 *>(in + n / kRounds * 8 * D + from[n % kRounds]); };
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) load(q, q);
+#pragma unroll 1
+      for (int n0 = 0; n0 < kMine * kRounds; n0 += kAhead) {
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+          const int n = n0 + q;
+          const uint4 a = make_uint4(f16x2_of_e4m3(w[q].x), f16x2_of_e4m3(w[q].x >> 16), f16x2_of_e4m3(w[q].y),
+                                     f16x2_of_e4m3(w[q].y >> 16));
+          const uint4 b = make_uint4(f16x2_of_e4m3(w[q].z), f16x2_of_e4m3(w[q].z >> 16), f16x2_of_e4m3(w[q].w),
+                                     f16x2_of_e4m3(w[q].w >> 16));
+          if (n0 + kAhead < kMine * kRounds) load(n + kAhead, q);
+          unsigned char *at = out + n / kRounds * 1024;
+          *reinterpret_cast<uint4 *>(at + to[n % kRounds][0]) = a;
+          *reinterpret_cast<uint4 *>(at + to[n % kRounds][1]) = b;
+        }
+      }
+      const int32_t have = max(0, kv - (key0 + j * Sh::kKeys) - d * kMine * 8);  // rows of the request's keys
+      if (have < kMine * 8) {
+        __syncwarp();
+        for (int r = have * 8 + lane; r < kMine * 64; r += 32)
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h) *reinterpret_cast<uint4 *>(out + h * Sh::kVHalf + r * 16) = make_uint4(0, 0, 0, 0);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(full);
+        mbar_arrive(&ln.empty[slot]);
+      }
+    }
+    if (!ok) break;
+    ++k;
+  }
+  if (!ok && lane == 0) atomicOr(&sm.err, 1);
 }
 
 // ---------------------------------------------------------------------------
@@ -888,7 +967,7 @@ __device__ __forceinline__ bool mark_and_join(const AttendArgs &a, const Segment
   named_sync(1 + s, kRows);
   if (*reinterpret_cast<volatile int32_t *>(complete) == 0) return true;
   __threadfence();
-  join_rows<D, kF8, 8>(a, jt, g.first, row >> 5, kRows / 32);
+  join_rows<D, kF8, kF8 ? 4 : 8>(a, jt, g.first, row >> 5, kRows / 32);
   for (int q = row; q < n; q += kRows) a.marks[part_of(g.first, q)] = 0;
   return true;
 }
@@ -1007,7 +1086,7 @@ __device__ __noinline__ bool redo_rows(const AttendArgs &a, uint32_t again, bool
       for (int u = 0; u < kMany; ++u) {
         if (j0 + u >= end) break;
         float p = ex2(fmaf(s[u], k2, -ref));
-        if (!kF8) p = __bfloat162float(__float2bfloat16_rn(p));  // as the product takes it
+        p = kF8 ? __half2float(__float2half_rn(p)) : __bfloat162float(__float2bfloat16_rn(p));  // as the product takes it
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = fmaf(p, v[u][e], acc[e]);
       }
@@ -1153,7 +1232,6 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
         const float ref = (M == -INFINITY) ? 0.f : M;
         const float2 kk = make_float2(k2, k2), nr = make_float2(-ref, -ref);
         float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-        float2 before = sum0;
         uint32_t w[Sh::kKeys / 2];
 #pragma unroll
         for (int c = 0; c < Sh::kKeys / 2; ++c) {
@@ -1163,21 +1241,8 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
             sum1 = __fadd2_rn(sum1, p);
           else
             sum0 = __fadd2_rn(sum0, p);
-          if constexpr (kF8) {
-            // 64 keys: 16 columns of first numbers, four keys each, and 16 of second ones
-            const int at = (c / 32) * 32 + (c % 32) / 2;
-            if (c & 1)
-              split_e4m3x4(before.x, before.y, p.x, p.y, w[at], w[at + 16]);
-            else
-              before = p;
-            if (!Sh::kApart && (c & 15) == 15) {
-              tmem_st8(t_p + u * 64 + (at - 7), w + (at - 7));
-              tmem_st8(t_p + u * 64 + (at + 9), w + (at + 9));
-            }
-          } else {
-            w[c] = pack_bf16(p.x, p.y);
-            if (!Sh::kApart && (c & 7) == 7) tmem_st8(t_p + u * 64 + (c - 7), w + (c - 7));
-          }
+          w[c] = kF8 ? pack_f16(p.x, p.y) : pack_bf16(p.x, p.y);
+          if (!Sh::kApart && (c & 7) == 7) tmem_st8(t_p + u * 64 + (c - 7), w + (c - 7));
         }
         const float2 t = __fadd2_rn(sum0, sum1);
         l += t.x + t.y;
@@ -1207,12 +1272,12 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
         // no further ahead than the others: two arrivals of a warp must not fall into one phase of p_full
         if (j > 0 && !(ok = warp_wait(&sm.o_step[s], par(steps + j - 1)))) break;
       }
-      if (key + Sh::kKeys > g.kv) {
+      if (!kF8 && key + Sh::kKeys > g.kv) {
         // value rows beyond the request's keys: whatever is there must not meet a weight of zero
         const int32_t vt = count + 2 * j + 1;
         if (!(ok = warp_wait(&ln.full[vt % Sh::kRing], par(vt / Sh::kRing)))) break;
         unsigned char *v = ring_ptr + (vt % Sh::kRing) * Sh::kTile;
-        for (int w = max(0, g.kv - key) * (Sh::kRowBytes / 16) + row; w < Sh::kHalf / 16; w += kRows)
+        for (int w = max(0, g.kv - key) * 8 + row; w < Sh::kHalf / 16; w += kRows)
 #pragma unroll
           for (int q = 0; q < Sh::kHalves; ++q) *reinterpret_cast<uint4 *>(v + q * Sh::kHalf + w * 16) = make_uint4(0, 0, 0, 0);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1312,13 +1377,13 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
 
 // kInside: narrow, units joined by the last worker
 template <int D, bool kWide, bool kInside, bool kF8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<D, kWide, kF8>::kThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttendArgs a) {
   using Sh = Shape<D, kWide, kF8>;
   using C = Control<Sh::kRing, Sh::kWorkers>;
   static_assert(sizeof(C) <= Sh::kControl, "control block");
-  constexpr int kWarps = kThreads / 32;
+  constexpr int kThreads = Sh::kThreads, kWarps = kThreads / 32;
   extern __shared__ __align__(1024) unsigned char dyn[];
   C &sm = *reinterpret_cast<C *>(dyn);
   const uint32_t base = smem_u32(dyn);
@@ -1335,11 +1400,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto &ln = sm.lane[w];
       for (int s = 0; s < Sh::kRing; ++s) {
         mbar_init(&ln.full[s], 1);
-        mbar_init(&ln.empty[s], 1);
+        mbar_init(&ln.empty[s], kF8 && (s & 1) ? Sh::kDecoders : 1);  // codes: the ring is even, values lie in odd slots
       }
       for (int s = 0; s < kSegRing; ++s) {
         mbar_init(&ln.seg_full[s], 1);
-        mbar_init(&ln.seg_empty[s], Sh::kSoftWarps + 1);
+        mbar_init(&ln.seg_empty[s], Sh::kSoftWarps + 1 + Sh::kDecoders);
       }
       ln.issued[0] = ln.issued[1] = 0;
       ln.q_issued = 0;
@@ -1359,6 +1424,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 4; ++s) {
       mbar_init(&sm.s_full[s], 1);
       mbar_init(&sm.p_full[s], 4);
+      mbar_init(&sm.v_full[s], max(1, Sh::kDecoders));
+      mbar_init(&sm.v_empty[s], 1);
     }
     sm.err = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1425,15 +1492,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_after();
   const uint32_t tmem = sm.tmem;
   const uint32_t q_smem = base + Sh::kControl, ring = q_smem + 2 * Sh::kQTile;
-  constexpr int kRingBytes = Sh::kRing * Sh::kTile;
-
-  // loaders and an issuer per worker; softmax warps from the fifth on
+  // loaders and an issuer per worker (wide, codes: a decoder); softmax warps from the fifth on; narrow, codes: decoders
   if (warp < 4) {
     // the launch has 168 registers for each of 384 threads: 128 * 72 + 256 * 216
     if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int wk = kWide ? 0 : warp >> 1;
     const int64_t id = static_cast<int64_t>(blockIdx.x) * Sh::kWorkers + wk;
-    const uint32_t my_q = q_smem + wk * Sh::kQTile, my_ring = ring + wk * kRingBytes;
+    const uint32_t my_q = q_smem + wk * Sh::kQTile, my_ring = ring + wk * Sh::kWorkerBytes;
     if (warp == 1 || (!kWide && warp == 3))
       issue_worker<D, kWide, kF8>(sm, wk, a.Hq / a.Hkv, my_q, my_ring, tmem);
     else if (!kWide)
@@ -1442,11 +1507,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_worker<D, kWide, kF8, 0, 1>(tmQ, tmK, tmV, a, sm, wk, static_cast<int>(id), W, line(id), line(id + 1), workers, my_q, my_ring);
     else if (warp == 2)
       load_worker<D, kWide, kF8, 1, 2>(tmQ, tmK, tmV, a, sm, wk, static_cast<int>(id), W, line(id), line(id + 1), workers, my_q, my_ring);
+    else if (kF8)
+      decode_worker<D, kWide>(sm, wk, 0, dyn + (my_ring - base));
+  } else if (warp >= 12) {
+    // on other schedulers than the worker's issuer and its first softmax warp (the second worker's rows lie 64 lanes on)
+    const int wk = 1 - ((warp - 12) >> 1);
+    decode_worker<D, kWide>(sm, wk, warp & 1, dyn + (ring - base) + wk * Sh::kWorkerBytes);
   } else {
     if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int st = (warp - 4) >> 2;
     softmax_stage<D, kWide, kF8, kInside>(a, sm, st, dyn + Sh::kControl + st * Sh::kQTile,
-                                          dyn + (ring - base) + (kWide ? 0 : st * kRingBytes), tmem);
+                                          dyn + (ring - base) + (kWide ? 0 : st * Sh::kWorkerBytes), tmem);
   }
   __syncthreads();
   if (sm.err) {
@@ -1569,7 +1640,7 @@ cudaError_t launch(AttendArgs a, cudaStream_t st) {
   const int P = sms[dev] < kMaxGrid ? sms[dev] : kMaxGrid;
   a.part_rows = kWide ? 2 * kRows : narrow_rows(a.T, G);
   void *tm = timer_before(kF8 ? "paged_attention_fp8" : "paged_attention", st);
-  paged_attention_kernel<D, kWide, kInside, kF8><<<P, kThreads, Sh::kSmem, st>>>(mq, mk, mv, a);
+  paged_attention_kernel<D, kWide, kInside, kF8><<<P, Sh::kThreads, Sh::kSmem, st>>>(mq, mk, mv, a);
   timer_after(tm, st);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || kInside) return e;
