@@ -601,8 +601,9 @@ svw_status paged_attention(const void *q, int64_t q_token_stride, int64_t q_head
  *   cache        codes of one byte; caches 16-byte aligned, strides positive
  *                multiples of 16.
  *   k_scale, v_scale  device float [n_kv_heads], normal numbers > 0; NULL: 1.
- *                Another number: the query heads of that key head become NaN,
- *                and SVW_DEV_BAD_INPUT.
+ *                Another number: the query heads of that key head become NaN
+ *                (out and lse; v_scale: out), whether they see a key or not, and
+ *                SVW_DEV_BAD_INPUT.
  * A query with a NaN or an infinity becomes NaN throughout, as one with scores
  * beyond 2.9 million in magnitude may (and does if its largest is).  Scores and sums are
  * fp32; a query enters its products as two e4m3 numbers under a scale of its

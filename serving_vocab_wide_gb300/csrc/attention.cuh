@@ -913,7 +913,8 @@ __device__ __forceinline__ void join_rows(const AttendArgs &a, const Joint &jt, 
     }
     const int tok = jt.tok0 + tile * a.tile_tokens + in_tile / G;
     const int64_t orow = static_cast<int64_t>(tok) * a.Hq + jt.hk * G + in_tile % G;
-    const float inv = (l == 0.f) ? 0.f : (kF8 ? head_scale(a.v_scale, jt.hk, a.status) : 1.f) / l;
+    const float vs = kF8 ? head_scale(a.v_scale, jt.hk, a.status) : 1.f;
+    const float inv = (l == 0.f) ? 0.f * vs : vs / l;  // no key: 0, NaN under a scale that is none
     uint32_t *dst = reinterpret_cast<uint32_t *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + orow * D + lane * E);
 #pragma unroll
     for (int u = 0; u < E / 2; ++u) dst[u] = pack_bf16(acc[2 * u] * inv, acc[2 * u + 1] * inv);
@@ -1297,7 +1298,7 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
       const int32_t tok = g.tok0 + tile * a.tile_tokens + tok_of_row;
       const int32_t orow = live ? tok * a.Hq + g.hk * G + head_of_row : -1;  // below 2^31, checked by the host
       const int64_t prow = static_cast<int64_t>(max(g.part, 0)) * a.part_rows + tile * kRows + q_row;
-      const float inv = (g.part >= 0) ? 1.f : (l == 0.f ? 0.f : vs / l);
+      const float inv = (g.part >= 0) ? 1.f : (l == 0.f ? 0.f * vs : vs / l);
       int32_t to[4];  // the rows of this lane's four, and its piece of each
 #pragma unroll
       for (int q = 0; q < 4; ++q) to[q] = __shfl_sync(0xffffffffu, orow, (lane & ~3) + q);

@@ -1,0 +1,42 @@
+"""kv_append_norm, kv_gather and paged_attention_fp8 at the ends of what they accept."""
+import math
+
+import numpy as np
+import pytest
+
+from test_gpu_cache8 import _as_bytes, _attend, _codes, _compare_attend, _f32, _queries
+from test_gpu_paged import _append_inputs, _cache, _cu, _i32, _lib  # noqa: F401 (a fixture)
+
+pytestmark = pytest.mark.gpu
+
+FLT_MIN, FLT_MAX = 2.0 ** -126, float(np.finfo(np.float32).max)
+
+
+# ---------------------------------------------------------------------------
+# paged_attention_fp8
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("new,kv,causal", [
+    ([2, 3], [0, 40], True), ([4, 1], [2, 300], True), ([100], [99], True), ([300], [299], True), ([2, 3], [0, 40], False),
+    ([300, 2], [0, 40], False)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_bad_scale_reaches_rows_that_see_no_key(new, kv, causal, d):
+    """Rows without keys are 0 and -inf, and NaN like all others under a scale that is none."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    rng = np.random.default_rng(d + sum(kv))
+    hq, hkv = 6, 3
+    kc, vc, table, ks, vs = _codes(rng, new, kv, hkv, d, 16)
+    q = _queries(rng, new, hq, d)
+    kw = {"causal": causal}
+    good = _attend(new, kv, q, kc, vc, table, ks, vs, kw)
+    place = np.concatenate([np.arange(k - n, k) if causal else np.full(n, k - 1) for n, k in zip(new, kv)])
+    none = torch.from_numpy(place < 0).cuda()
+    assert bool(none.any()) and bool((good[0][none] == 0).all()) and bool((good[1][none] == -math.inf).all())
+    for bad in (0.0, float("nan"), float("inf"), 1e-40):
+        k2, v2 = ks.clone(), vs.clone()
+        k2[0], v2[2] = bad, bad
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = _attend(new, kv, q, kc, vc, table, k2, v2, kw, status)
+        assert int(status) == svw.SVW_DEV_BAD_INPUT
+        assert bool(out[:, [0, 1, 4, 5]].isnan().all()) and bool(lse[:, :2].isnan().all())
+        assert torch.equal(out[:, 2:4], good[0][:, 2:4]) and torch.equal(lse[:, 2:], good[1][:, 2:])
