@@ -1046,7 +1046,7 @@ __device__ __noinline__ bool redo_rows(const AttendArgs &a, uint32_t again, bool
   if (!odd_values<D, kF8>(a, table, hk, key0, min(lo_most, key1)) &&
       !odd_values<D, kF8>(a, table, hk, max(hi_least, key0), key1))
     return spoilt;
-  const float k2 = a.scale * kLog2e * (kF8 ? head_scale(a.k_scale, hk, a.status) : 1.f);
+  const float k2 = a.scale * kLog2e, ks = kF8 ? head_scale(a.k_scale, hk, a.status) : 1.f;
   auto load = [&](const auto *p, float *x) {
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
@@ -1068,6 +1068,10 @@ __device__ __noinline__ bool redo_rows(const AttendArgs &a, uint32_t again, bool
     load(static_cast<const __nv_bfloat16 *>(a.q) + row / a.Hq * a.q_ts + row % a.Hq * a.q_hs, q);
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    if (kF8) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) q[e] *= ks;
+    }
     for (int32_t j0 = begin; j0 < end; j0 += kMany) {
       float k[kMany][E], v[kMany][E], s[kMany];
 #pragma unroll
@@ -1184,7 +1188,8 @@ __device__ __forceinline__ void softmax_stage(const AttendArgs &a, C &sm, int s,
       vs = head_scale(a.v_scale, g.hk, a.status);
       if (warp_live) {
         if (!(ok = warp_wait(&sm.q_full[kWide ? 0 : s], par(k)))) break;
-        k2 = a.scale * kLog2e * ks * split_query<D>(q_ptr, q_row);
+        // the keys' scale by the queries' power of two first: each may lie at an end of fp32's range
+        k2 = ks * split_query<D>(q_ptr, q_row) * (a.scale * kLog2e);
         if (k2 < FLT_MIN) k2 = FLT_MIN;  // zero times a hidden score's infinity; such scores are zero either way
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }

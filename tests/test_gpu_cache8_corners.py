@@ -40,3 +40,37 @@ def test_a_bad_scale_reaches_rows_that_see_no_key(new, kv, causal, d):
         assert int(status) == svw.SVW_DEV_BAD_INPUT
         assert bool(out[:, [0, 1, 4, 5]].isnan().all()) and bool(lse[:, :2].isnan().all())
         assert torch.equal(out[:, 2:4], good[0][:, 2:4]) and torch.equal(lse[:, 2:], good[1][:, 2:])
+
+
+@pytest.mark.parametrize("new,kv", [([3, 1], [300, 20000]), ([150, 40], [700, 300])])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scales_and_queries_at_opposite_ends(new, kv, d):
+    """A score is formed of factors that may be large and small; none of the steps leaves fp32's range."""
+    import torch
+    rng = np.random.default_rng(19)
+    kc, vc, table, ks, vs = _codes(rng, new, kv, 2, d, 32)
+    q = torch.zeros(sum(new), 4, d, dtype=torch.bfloat16, device="cuda")
+    most = torch.full_like(ks, FLT_MAX)
+    _compare_attend(new, kv, q, kc, vc, table, most, vs, {"scale": 10.0}, *_attend(new, kv, q, kc, vc, table, most, vs, {"scale": 10.0}))
+    # the least scale, the largest queries
+    q = _queries(rng, new, 4, d, 1).clamp(-3, 3) * 2.0 ** 125
+    least = torch.full_like(ks, FLT_MIN)
+    kw = {"scale": 1.3 * 2.0 ** -13 / math.sqrt(d)}
+    _compare_attend(new, kv, q, kc, vc, table, least, vs, kw, *_attend(new, kv, q, kc, vc, table, least, vs, kw))
+
+
+def test_a_hidden_value_beside_scales_and_queries_at_opposite_ends():
+    """Rows that are formed again are formed in the same range."""
+    import torch
+    rng = np.random.default_rng(20)
+    new, kv, d = [20], [500], 128
+    kc, vc, table, ks, vs = _codes(rng, new, kv, 1, d, 16)
+    q = _queries(rng, new, 2, d, 1).clamp(-3, 3) * 2.0 ** 125
+    least, kw = torch.full_like(ks, FLT_MIN), {"scale": 1.3 * 2.0 ** -13 / math.sqrt(d)}
+    odd = vc.clone()
+    _as_bytes(odd)[int(table[0, 499 // 16]), 0, 499 % 16] = 0x7f  # the last token's values: no other sees them
+    out, lse = _attend(new, kv, q, kc, odd, table, least, vs, kw)
+    assert bool(out[19].isnan().all())
+    clean = _attend(new, kv, q, kc, vc, table, least, vs, kw)
+    out[19] = clean[0][19]
+    _compare_attend(new, kv, q, kc, vc, table, least, vs, kw, out, lse)
