@@ -213,12 +213,16 @@ __device__ __forceinline__ void form(const AppendNormArgs &a, const Spot &p, uin
         to2(g, e, __fmul2_rn(at2(g, e), at2(cb, e)));
       }
     }
-    if (kCode) r = __fmul_rn(r, __frcp_rn(head_scale(kClass == kKeysOf ? a.k_scale : a.v_scale, h, a.status)));
+    auto times = [&](float by) {
 #pragma unroll
-    for (int e = 0; e < N; e += 2) {
-      to2(f, e, __fmul2_rn(at2(f, e), make_float2(r, r)));
-      to2(g, e, __fmul2_rn(at2(g, e), make_float2(r, r)));
-    }
+      for (int e = 0; e < N; e += 2) {
+        to2(f, e, __fmul2_rn(at2(f, e), make_float2(by, by)));
+        to2(g, e, __fmul2_rn(at2(g, e), make_float2(by, by)));
+      }
+    };
+    // one after the other: r is 1000 for a head of zeros, and with the reciprocal of a small scale infinite
+    if (kClass != kValuesOf) times(r);
+    if (kCode) times(__frcp_rn(head_scale(kClass == kKeysOf ? a.k_scale : a.v_scale, h, a.status)));
     float o[2 * N];
     shut<N, kApart>(f, g, o);
     if constexpr (kCode) {
@@ -237,8 +241,8 @@ __device__ __forceinline__ void form(const AppendNormArgs &a, const Spot &p, uin
 // head; each has one slot of it, two vectors (both halves of its pairs), and adds
 // the squares up by exchange.  What is the same for all heads of a class, the
 // weights times cosines and sines, is formed once a task:
-//   a' = r (a (w_a c) - b (w_b s)),  b' = r (b (w_b c) + a (w_a s)),
-// with the scale of a code in r.  Heads and rotated parts in multiples of two
+//   a' = r (a (w_a c) - b (w_b s)),  b' = r (b (w_b c) + a (w_a s)).
+// Heads and rotated parts in multiples of two
 // vectors, everything 16-byte aligned.
 template <typename T, bool kCodes, bool kApart, int kItems>
 __global__ void __launch_bounds__(kThreads, 3) append_norm_vec(const __grid_constant__ AppendNormArgs a) {

@@ -74,3 +74,32 @@ def test_a_hidden_value_beside_scales_and_queries_at_opposite_ends():
     clean = _attend(new, kv, q, kc, vc, table, least, vs, kw)
     out[19] = clean[0][19]
     _compare_attend(new, kv, q, kc, vc, table, least, vs, kw, out, lse)
+
+
+# ---------------------------------------------------------------------------
+# kv_append_norm
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("tokens", [3, 400])
+@pytest.mark.parametrize("d", [64, 40])
+@pytest.mark.parametrize("scale", [FLT_MIN, 1e-37, 1e-30])
+def test_zeros_under_a_small_scale_are_zero(tokens, d, scale):
+    """The norm's factor (1000 of a head of zeros) and a scale's reciprocal meet nowhere."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    rng = np.random.default_rng(7)
+    new, kv, hkv = [tokens], [tokens], 2
+    kc, vc, table = _cache(rng, new, kv, hkv, d, 16, torch.float8_e4m3fn)
+    q, k, v = _append_inputs(rng, new, 2, hkv, d, torch.bfloat16)
+    k, v = k.clone(), v.clone()
+    k[1] = 0
+    k[2, :, 1:] = 0
+    v[1] = 0
+    s = _f32([scale] * hkv)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    svw.kv_append_norm(k, v, kc, vc, _i32(table), _i32(_cu(new)), _i32(kv), k_weight=_f32(np.ones(d)), eps=1e-6, k_scale=s,
+                       v_scale=s, status=status)
+    assert int(status) == 0
+    page = int(table[0, 0])
+    assert bool((kc[page, :, 1].float() == 0).all()) and bool((vc[page, :, 1].float() == 0).all())
+    assert bool((kc[page, :, 2, 1:].float() == 0).all()) and bool((kc[page, :, 2, 0].float().abs() == 448).all())
+    assert not bool(kc[page, :, :3].float().isnan().any()) and not bool(vc[page, :, :3].float().isnan().any())
