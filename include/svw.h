@@ -503,9 +503,11 @@ svw_status kv_append(const void *k, int64_t k_token_stride, int64_t k_head_strid
  *   y_e = x_e k_weight_e / sqrt(mean_e x_e^2 + eps)       (k_weight NULL: y = x)
  * its pairs rotated as kv_append's are.  Into a cache of SVW_E4M3 a key of head
  * h is written as the code nearest to y / k_scale[h], a value as the one nearest
- * to v / v_scale[h] (ties to even; beyond +-448, infinities too: +-448; NaN:
- * NaN), so that code x scale stands for it; into a cache of dtype as it is.
- * Rounded once.
+ * to v / v_scale[h] (the quotients in fp32; ties to even; beyond +-448,
+ * infinities too: +-448; NaN: NaN), so that code x scale stands for it; into a
+ * cache of dtype as it is.  Rounded once.  Shapes and alignments that take the
+ * scalar path add and multiply in another order: a normed or rotated number may
+ * differ there by fp32's roundings, and so by a step of its type.
  *
  * Arguments and results as for kv_append, except:
  *   k_weight, q_weight  device float [head_dim]; NULL: no norm.  q_weight needs q.

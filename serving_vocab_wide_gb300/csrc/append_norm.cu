@@ -4,7 +4,7 @@
 //
 //   y_e = x_e w_e / sqrt(mean_e x_e^2 + eps);  pairs (a, b) of y become
 //   (a c - b s, b c + a s);  code = e4m3(y / scale of the head)
-// in fp32, rounded once.
+// in fp32, the quotient too, rounded once.
 //
 // Bound by instructions and by its chain of dependent loads (offsets and lengths
 // -> block table, cosines -> stores) rather than by its bytes.  A kernel like
@@ -13,8 +13,8 @@
 // 2196 tokens of 32 query and 8 key heads of 128, 50.6 MB into codes); warps of
 // one class, which form the products of weights, cosines and sines once, take
 // 197 (18 us), and finding the tokens once a block instead of once a warp does
-// the rest.  Device time: 14.9 us there (3.4 TB/s), 29.5 on 14 k tokens of 48
-// heads of 64 (4.9 TB/s), 14.9 on 1742 tokens of 40 and 8 heads into bf16, 3.2 for
+// the rest.  Device time: 14.8 us there (3.4 TB/s), 30.6 on 14 k tokens of 48
+// heads of 64 (4.7 TB/s), 14.8 on 1742 tokens of 40 and 8 heads into bf16, 3.3 for
 // one token.  Rounds in fours 16.0 and 40, one at a time 16.4 and 34; two blocks
 // an SM 17.5 and 34, four 15.6 and 32; loads staged through shared memory two
 // tasks ahead 14.6 and 39.
@@ -73,18 +73,38 @@ __device__ __forceinline__ void put(T *dst, const float *f) {
   for (int q = 0; q < Vec<T>::N / 4; ++q) Vec<T>::put(u, q, make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]));
   *reinterpret_cast<uint4 *>(dst) = u;
 }
-template <int N>
-__device__ __forceinline__ void put_codes(uint8_t *dst, const float *f) {
-  uint32_t c[N / 4];
-#pragma unroll
-  for (int q = 0; q < N / 4; ++q) c[q] = e4m3x4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
-  if constexpr (N == 8)
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(c[0], c[1]);
-  else
-    *reinterpret_cast<uint32_t *>(dst) = c[0];
-}
 __device__ __forceinline__ float2 at2(const float *f, int e) { return make_float2(f[e], f[e + 1]); }
 __device__ __forceinline__ void to2(float *f, int e, const float2 &v) { f[e] = v.x, f[e + 1] = v.y; }
+
+// The four codes nearest to quotients in fp32, of any size.
+__device__ __noinline__ uint32_t codes_of_quotients(float a, float b, float c, float d, float s) {
+  return e4m3x4(__fdiv_rn(a, s), __fdiv_rn(b, s), __fdiv_rn(c, s), __fdiv_rn(d, s));
+}
+// The codes nearest to x / s, that quotient in fp32, of E numbers.  A product
+// with a rounded 1 / s is off by an ulp or two, which at a tie is another code (19
+// of 1920 bf16 numbers under 7 / 512), so 1 / s comes as two numbers, 47 bits.
+// Neither is zero or negative: an infinity stays one, and a zero keeps its sign.
+// (Beside a product with the rounded one: 14.5 and 30.5 us instead of 14.8 and 30.6
+// on the two cases above; the product corrected by its remainder 15.1 and 32.1.)
+template <int E>
+__device__ __forceinline__ void codes(const float *x, float s, uint32_t *c) {
+  if (s >= 0x1p-60f && s <= 0x1p60f) {
+    const float inv = __frcp_rd(s), rest = fmaxf(fmaf(-s, inv, 1.f) * inv, inv * 0x1p-40f);
+#pragma unroll
+    for (int q = 0; q < E / 4; ++q) {
+      float2 m[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 y = at2(x, 4 * q + 2 * i);
+        m[i] = __ffma2_rn(y, make_float2(inv, inv), __fmul2_rn(y, make_float2(rest, rest)));
+      }
+      c[q] = e4m3x4(m[0].x, m[0].y, m[1].x, m[1].y);
+    }
+  } else {  // a scale near the ends of fp32's range, or none
+#pragma unroll
+    for (int q = 0; q < E / 4; ++q) c[q] = codes_of_quotients(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3], s);
+  }
+}
 
 // where a token goes
 struct Spot {
@@ -213,21 +233,25 @@ __device__ __forceinline__ void form(const AppendNormArgs &a, const Spot &p, uin
         to2(g, e, __fmul2_rn(at2(g, e), at2(cb, e)));
       }
     }
-    auto times = [&](float by) {
+    if (kClass != kValuesOf) {  // (no norm: by 1, which is faster than a branch)
 #pragma unroll
       for (int e = 0; e < N; e += 2) {
-        to2(f, e, __fmul2_rn(at2(f, e), make_float2(by, by)));
-        to2(g, e, __fmul2_rn(at2(g, e), make_float2(by, by)));
+        to2(f, e, __fmul2_rn(at2(f, e), make_float2(r, r)));
+        to2(g, e, __fmul2_rn(at2(g, e), make_float2(r, r)));
       }
-    };
-    // one after the other: r is 1000 for a head of zeros, and with the reciprocal of a small scale infinite
-    if (kClass != kValuesOf) times(r);
-    if (kCode) times(__frcp_rn(head_scale(kClass == kKeysOf ? a.k_scale : a.v_scale, h, a.status)));
+    }
     float o[2 * N];
     shut<N, kApart>(f, g, o);
     if constexpr (kCode) {
-      put_codes<N>(dst + x, o);
-      put_codes<N>(dst + y, o + N);
+      uint32_t c[N / 2];
+      codes<2 * N>(o, head_scale(kClass == kKeysOf ? a.k_scale : a.v_scale, h, a.status), c);
+      if constexpr (N == 8) {
+        *reinterpret_cast<uint2 *>(dst + x) = make_uint2(c[0], c[1]);
+        *reinterpret_cast<uint2 *>(dst + y) = make_uint2(c[2], c[3]);
+      } else {
+        *reinterpret_cast<uint32_t *>(dst + x) = c[0];
+        *reinterpret_cast<uint32_t *>(dst + y) = c[1];
+      }
     } else {
       put<T>(dst + x, o);
       put<T>(dst + y, o + N);
@@ -311,13 +335,13 @@ __global__ void __launch_bounds__(kThreads) append_norm_any(const __grid_constan
     const T *src;
     head_rows<T>(a, t, h, src);
     const float *weight = is_q ? a.q_weight : (is_v ? nullptr : a.k_weight);
-    float r = 1.f, inv = 1.f;
+    float r = 1.f, scale = 1.f;
     if (weight) {
       float ss = 0.f;
       for (int e = lane; e < D; e += 32) ss = fmaf(ld_f(src + e), ld_f(src + e), ss);
       r = rsqrtf(fmaf(warp_sum(ss), a.inv_dim, a.eps));
     }
-    if (kCodes && !is_q) inv = __frcp_rn(head_scale(is_v ? a.v_scale : a.k_scale, hh, a.status));
+    if (kCodes && !is_q) scale = head_scale(is_v ? a.v_scale : a.k_scale, hh, a.status);
     auto get = [&](int e) { return weight ? __fmul_rn(__fmul_rn(ld_f(src + e), r), __ldg(weight + e)) : ld_f(src + e); };
     T *q_out = reinterpret_cast<T *>(a.q_out) + (t * a.Hq + hh) * D;
     const int64_t at = is_v ? p.page * a.vc[0] + hh * a.vc[1] + p.row * a.vc[2]
@@ -327,7 +351,7 @@ __global__ void __launch_bounds__(kThreads) append_norm_any(const __grid_constan
       if (is_q)
         st_f(q_out + e, y);
       else if (kCodes)
-        static_cast<uint8_t *>(cache)[at + e] = static_cast<uint8_t>(e4m3x2(__fmul_rn(y, inv), 0.f));
+        static_cast<uint8_t *>(cache)[at + e] = static_cast<uint8_t>(e4m3x2(__fdiv_rn(y, scale), 0.f));
       else
         st_f(static_cast<T *>(cache) + at + e, y);
     };

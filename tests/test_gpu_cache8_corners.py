@@ -103,3 +103,45 @@ def test_zeros_under_a_small_scale_are_zero(tokens, d, scale):
     assert bool((kc[page, :, 1].float() == 0).all()) and bool((vc[page, :, 1].float() == 0).all())
     assert bool((kc[page, :, 2, 1:].float() == 0).all()) and bool((kc[page, :, 2, 0].float().abs() == 448).all())
     assert not bool(kc[page, :, :3].float().isnan().any()) and not bool(vc[page, :, :3].float().isnan().any())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d,shift", [(64, 0), (128, 0), (40, 0), (64, 1)])  # the last two: entry by entry
+def test_codes_are_nearest_to_the_quotient(dtype, d, shift):
+    """The nearest code to x / scale, that quotient in fp32: ties too, of which scales like 7 / 512 have many, and
+    at the ends of fp32's range.  Without a norm and a rotation nothing else rounds."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    dt = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype]
+    scales = [7 / 512, 0.7, 1 / 3, 5 / 448, 0.03, 1.0, 2.0 ** -60, 1.1 * 2.0 ** -61, 1.9 * 2.0 ** 60, 1.7 * 2.0 ** 100,
+              FLT_MIN, 1.5 * FLT_MIN, FLT_MAX, 3e38, 1.3 * 2.0 ** -100, 2.0 ** -149 * (2 ** 24 - 1)]
+    hkv, page = len(scales), 16
+    s = torch.tensor(scales, dtype=torch.float32)
+    gen = torch.Generator().manual_seed(3)
+    # per head: every bf16 number of the codes' range and beyond, of its scale; ties of fp32; anything at all
+    mant = torch.arange(128, 256, dtype=torch.float64) / 128
+    some = (mant[None] * 2.0 ** torch.arange(-12, 11, dtype=torch.float64)[:, None]).flatten()
+    near = 2.0 ** torch.floor(torch.log2(s.double()))
+    x = some[None] * near[:, None]
+    codes = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    ties = (codes[1:] + codes[:-1])[None] / 2 * s.double()[:, None]
+    wild = torch.randint(0, 1 << 31, (hkv, 3000), generator=gen, dtype=torch.int32).view(torch.float32).double()
+    ends = torch.tensor([0.0, math.inf, math.nan, FLT_MAX, FLT_MIN, 2.0 ** -133, 2.0 ** -149], dtype=torch.float64).expand(hkv, -1)
+    x = torch.cat((x, ties, wild, ends), 1).float()
+    x = torch.cat((x, -x), 1).to(dt)
+    tokens = -(-x.shape[1] // d)
+    x = torch.nn.functional.pad(x, (0, tokens * d - x.shape[1])).view(hkv, tokens, d).transpose(0, 1).contiguous()
+    want = (x.float() / s[None, :, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+    store = torch.zeros(x.numel() + 1, dtype=dt, device="cuda")
+    store[shift:shift + x.numel()] = x.flatten().cuda()
+    y = store[shift:shift + x.numel()].view(x.shape)
+    pages = -(-tokens // page)
+    kc, vc = torch.zeros(2, pages, hkv, page, d, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    svw.kv_append_norm(y, y, kc, vc, table, _i32([0, tokens]), _i32([tokens]), k_scale=s.cuda(), v_scale=s.cuda())
+    for c in (kc, vc):
+        got = c.view(torch.uint8).transpose(1, 2).reshape(-1, hkv, d)[:tokens].cpu().view(torch.float8_e4m3fn).float()
+        w = want.float()
+        same = (got == w) | (got.isnan() & w.isnan())
+        assert bool(same.all()), [(float(x[tuple(i)]), scales[int(i[1])], float(got[tuple(i)]), float(w[tuple(i)]))
+                                  for i in (~same).nonzero()[:5]] + [int((~same).sum())]
