@@ -161,8 +161,8 @@ void launch(const AppendArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_append(const AppendArgs &a, int dtype, cudaStream_t st) {
-  void *tm = timer_before("kv_append", st);
+cudaError_t launch_append(const AppendArgs &a, int dtype, cudaStream_t st, const char *name) {
+  void *tm = timer_before(name, st);
   if (dtype == SVW_BF16)
     launch<__nv_bfloat16>(a, st);
   else

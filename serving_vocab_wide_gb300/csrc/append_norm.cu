@@ -411,7 +411,7 @@ void launch(AppendNormArgs a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_append_norm(const AppendNormArgs &a, int dtype, cudaStream_t st) {
-  if (!a.codes && !a.k_weight && !a.q_weight) return launch_append(a, dtype, st);
+  if (!a.codes && !a.k_weight && !a.q_weight) return launch_append(a, dtype, st, "kv_append_norm");
   void *tm = timer_before("kv_append_norm", st);
   if (dtype == SVW_BF16)
     a.codes ? launch<__nv_bfloat16, true>(a, st) : launch<__nv_bfloat16, false>(a, st);

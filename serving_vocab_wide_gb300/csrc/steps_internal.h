@@ -60,7 +60,8 @@ struct AppendArgs {
   int32_t max_pages, n_pages, page_size;
   int32_t *status;
 };
-cudaError_t launch_append(const AppendArgs &a, int dtype, cudaStream_t stream);
+// name: the call whose timer it is
+cudaError_t launch_append(const AppendArgs &a, int dtype, cudaStream_t stream, const char *name = "kv_append");
 
 // kv_append_norm (append_norm.cu)
 struct AppendNormArgs : AppendArgs {

@@ -145,3 +145,21 @@ def test_codes_are_nearest_to_the_quotient(dtype, d, shift):
         same = (got == w) | (got.isnan() & w.isnan())
         assert bool(same.all()), [(float(x[tuple(i)]), scales[int(i[1])], float(got[tuple(i)]), float(w[tuple(i)]))
                                   for i in (~same).nonzero()[:5]] + [int((~same).sum())]
+
+
+@pytest.mark.parametrize("codes,weight", [(False, False), (False, True), (True, False), (True, True)])
+def test_the_timer_of_its_name_fires(codes, weight):
+    """Whatever kernel serves a call, a timer armed for kv_append_norm records around it."""
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    rng = np.random.default_rng(8)
+    kc, vc, table = _cache(rng, [5], [5], 2, 64, 16, torch.float8_e4m3fn if codes else torch.bfloat16)
+    q, k, v = _append_inputs(rng, [5], 2, 2, 64, torch.bfloat16)
+    start, begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(3))
+    start.record()
+    svw.time_next_launch("kv_append_norm", begin, end)
+    torch.cuda._sleep(20_000_000)  # some 10 ms
+    svw.kv_append_norm(k, v, kc, vc, _i32(table), _i32([0, 5]), _i32([5]), k_weight=_f32(np.ones(64)) if weight else None)
+    torch.cuda.synchronize()
+    svw.time_next_launch(None)
+    assert start.elapsed_time(begin) > 2 and begin.elapsed_time(end) > 0
