@@ -830,9 +830,11 @@ def kv_append_norm(k, v, k_cache, v_cache, block_table, cu_new, kv_len, *, k_wei
 
 
 def kv_gather(k_cache, v_cache, block_table, cu_out, *, first=None, k_scale=None, v_scale=None,
-              total_out: int | None = None, dtype=None, k_out=None, v_out=None, status=None, stream=None):
+              total_out: int | None = None, dtype=None, k_out=None, v_out=None, want_k: bool = True,
+              want_v: bool = True, status=None, stream=None):
     """Cached keys and values read back, packed.  Returns (k, v): [total_out,
-    heads, head_dim] of `dtype` (bfloat16 or float32; bfloat16 by default).
+    heads, head_dim] of `dtype` (bfloat16 or float32; bfloat16 by default), None
+    for the one that is not wanted.
 
     The caches, of float32, bfloat16 or float8_e4m3fn with k_scale and v_scale, and
     block_table as for kv_append_norm; cu_out: int32 [N + 1] offsets of the
@@ -852,6 +854,8 @@ def kv_gather(k_cache, v_cache, block_table, cu_out, *, first=None, k_scale=None
         raise SvwError(f"first must have {N} elements")
     heads = shape[1]
     k_scale, v_scale = _scale("k_scale", k_scale, heads, code, gpu), _scale("v_scale", v_scale, heads, code, gpu)
+    if not (want_k or want_v) or (k_out is not None and not want_k) or (v_out is not None and not want_v):
+        raise SvwError("keys or values must be wanted, and those whose output is given")
     given = k_out if k_out is not None else v_out
     if total_out is None:
         total_out = int(cu_out[-1].item()) if given is None else given.shape[0]
@@ -862,15 +866,17 @@ def kv_gather(k_cache, v_cache, block_table, cu_out, *, first=None, k_scale=None
         raise SvwError("k_out and v_out must be bfloat16 or float32")
     want = (total_out, heads, shape[3])
     if k_out is None:
-        k_out = _empty(stream, gpu, want, dtype, k_cache.device)
+        if want_k:
+            k_out = _empty(stream, gpu, want, dtype, k_cache.device)
     elif _off(k_out, dtype, gpu) or k_out.shape != want:
         raise SvwError(f"k_out must be a contiguous {dtype} tensor of {want} on cuda:{gpu}")
     if v_out is None:
-        v_out = _empty(stream, gpu, want, dtype, k_cache.device)
+        if want_v:
+            v_out = _empty(stream, gpu, want, dtype, k_cache.device)
     elif _off(v_out, dtype, gpu) or v_out.shape != want:
         raise SvwError(f"v_out must be a contiguous {dtype} tensor of {want} on cuda:{gpu}")
     rc = lib().kv_gather(cache, code, k_scale, v_scale, N, cu_out.data_ptr(), total_out, _addr(first),
-                         k_out.data_ptr(), v_out.data_ptr(), out_code, _addr(status), _stream_of(stream, gpu))
+                         _addr(k_out), _addr(v_out), out_code, _addr(status), _stream_of(stream, gpu))
     if rc:
         _check(rc)
     return k_out, v_out

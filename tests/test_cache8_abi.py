@@ -187,3 +187,20 @@ def test_scales_come_with_codes(calls):
         with pytest.raises(m.SvwError):
             call()
     assert len(h.calls) == 2
+
+
+def test_gather_of_one_side(calls):
+    """No memory is taken, and no address handed over, for the side that is not wanted."""
+    import serving_vocab_wide_gb300 as m
+    h, make = calls
+    gather = make()["kv_gather"]
+    k, v = gather(want_v=False)
+    assert v is None and k.shape == (9, 2, 64) and len(h.made) == 1
+    assert h.calls[-1][1][8] == 0x10000 and h.calls[-1][1][9] == 0
+    given = Tensor((9, 2, 64), F32)
+    assert gather(want_k=False, v_out=given) == (None, given) and len(h.made) == 1
+    assert h.calls[-1][1][8] == 0 and h.calls[-1][1][9] == 0x10000
+    for o in ({"want_k": False, "want_v": False}, {"want_k": False, "k_out": given}, {"want_v": False, "v_out": given}):
+        with pytest.raises(m.SvwError):
+            gather(**o)
+    assert len(h.calls) == 2

@@ -163,3 +163,24 @@ def test_the_timer_of_its_name_fires(codes, weight):
     torch.cuda.synchronize()
     svw.time_next_launch(None)
     assert start.elapsed_time(begin) > 2 and begin.elapsed_time(end) > 0
+
+
+# ---------------------------------------------------------------------------
+# kv_gather
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("cache", ["e4m3", "bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 24])
+def test_one_side_alone(cache, d):
+    import serving_vocab_wide_gb300 as svw
+    import torch
+    rng = np.random.default_rng(4)
+    dt = {"e4m3": torch.float8_e4m3fn, "bf16": torch.bfloat16, "fp32": torch.float32}[cache]
+    n = [20, 7]
+    kc, vc, table = _cache(rng, n, n, 2, d, 16, dt)
+    args = kc, vc, _i32(table), _i32(_cu(n))
+    both = svw.kv_gather(*args)
+    k, none = svw.kv_gather(*args, want_v=False)
+    assert none is None and torch.equal(k, both[0])
+    given = torch.empty(27, 2, d, device="cuda")
+    none, v = svw.kv_gather(*args, want_k=False, v_out=given)
+    assert none is None and v is given and torch.equal(v.bfloat16(), both[1])
