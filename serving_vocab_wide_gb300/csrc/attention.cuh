@@ -26,8 +26,9 @@
 // issues the products (tcgen05.mma, fp32 accumulators in tensor memory):
 //   scores  S[128 rows, keys] = Q K^T, both K-major from shared memory;
 //   softmax running reference M and sum l of each row in base 2;
-//   output  O[128 rows, D] += P V with P (bf16) written over S in tensor
-//           memory and V read as it lies, keys along K (MN-major).
+//   output  O[128 rows, D] += P V with P (bf16; codes: fp16) written over S in
+//           tensor memory and V read as it lies (codes: decoded), keys along K
+//           (MN-major).
 // Two ways to use the stages, by the rows that a request brings on average:
 //   narrow  (up to 128: decoding, verifying; bound by the bytes of the keys) a
 //           stage is a worker: its own units, its own loads, key tiles of 64,
@@ -46,14 +47,14 @@
 // Measured (us; 32 query heads, 8 key heads of 128; of 6.78 TB/s and 1898
 // TFLOP/s): 64 decoding requests over 1000 to 16000 keys 209 (98%); 2220 new
 // tokens of 256 requests over 512 to 8192 keys 448 (95%); 17 tokens over 131000
-// keys 95 (83%); two prompts of 2048 over 8192 keys 371 to 391 in short runs
-// (1580 to 1670 TFLOP/s, 83 to 88%) and 417 to 432 in long ones, at the power
-// limit (75 to 78%).
+// keys 95 (83%); two prompts of 2048 over 8192 keys 383 to 386 in short runs
+// (1600 to 1615 TFLOP/s, 85%) and 403 to 419 in long ones, at the power limit
+// (1475 to 1535, 78 to 81%).
 // The reference: exp2(x - M) is exact algebra for any M, so M follows the
 // row's maximum only when that has outgrown it by more than 8 (a factor 256:
-// far from overflow, and the same relative rounding of P); only then are l
-// and O multiplied by 2^(M - M').  P is rounded to bf16, the operand type of
-// the second product; l sums the unrounded weights in fp32.
+// far from overflow, and the same relative rounding of P; codes: see below);
+// only then are l and O multiplied by 2^(M - M').  P is rounded to the operand
+// type of the second product; l sums the unrounded weights in fp32.
 //
 // Codes (kF8).  With K = k_scale k and V = v_scale v the scales are factors of a
 // row's scores and of its outputs.  The first product takes the keys' codes as
@@ -72,20 +73,24 @@
 // it below, which 2^17 keys add up to 2^-15.  (Weights as two e4m3 numbers, which
 // multiply the codes as they lie, end at 2^-15 of the largest: a first key 11
 // nats above 16000 others lost 0.4 of the output, and the second number in e5m2
-// keeps three bits there, 2^-4 of a tail of equal weights.)
-// Measured (us, as above): decoding 129 (5.4 TB/s), 2108 new tokens 299 to 310, 17
-// tokens over 131000 keys 66 to 68, two prompts 397 to 401 (1545 TFLOP/s), 128
-// blocks of 16 tokens, 16 heads of 64, over 200 to 2000 keys 88.  What bounds the narrow
+// keeps three bits there, off by up to 2^-3 of a tail of equal weights.)
+// Measured (us, as above): decoding 129 to 131 (5.4 TB/s), 2108 new tokens 299 to
+// 311, 17 tokens over 131000 keys 66, two prompts 397 to 404 (1530 to 1555
+// TFLOP/s), one token over 777 keys 15.5 (bf16 12.9), 128 blocks of 16 tokens, 16 heads of 64, over 200 to 2000 keys 88.  What bounds the narrow
 // form: its chain of products and softmax, no longer the bytes.  One live warp of
 // each worker used to share a scheduler (1660 cycles a tile of 64 keys, 1560 of
 // them that warp's); now the second worker's few rows lie in other lanes, a tile's
 // outputs and the next scores are issued in one piece (146 us otherwise), and the
-// decoders keep off their worker's issuer (one on its scheduler 138 us). Two
+// decoders keep off their worker's issuer (one on its scheduler 138 us).  Two
 // decoders a worker take 128.7, 310, 66 and 87.6 us, one 130.6, 305, 68 and 93.
 // (Decoding by shifts and masks, 36 instructions instead of the 8 conversions of
-// 16 codes, took 194 us, loads and stores that take turns 172.)  Copies of few rows
+// 16 codes, took 194 us, loads and stores that take turns 172.)  The decoders' 24 KB
+// of a tile come beside the 56 KB that its products read of shared memory, most of
+// them the query tile: blocks of 16 tokens with heads of 128 take 133 us, without
+// decoding 112.  Copies of few rows
 // in all warps' lanes, each warp with its part of a tile's keys, were slower, as
-// were the next unit's queries split ahead of a unit's outputs.
+// were the next unit's queries split ahead of a unit's outputs.  The narrow form
+// has 128 registers a thread, so its own join has six parts under way, not eight.
 //
 // Masks are ranges of places: scores outside [lo, hi) become -inf by
 // selection (their products may be anything), key tiles and pages that no row
@@ -968,7 +973,7 @@ __device__ __forceinline__ bool mark_and_join(const AttendArgs &a, const Segment
   named_sync(1 + s, kRows);
   if (*reinterpret_cast<volatile int32_t *>(complete) == 0) return true;
   __threadfence();
-  join_rows<D, kF8, kF8 ? 4 : 8>(a, jt, g.first, row >> 5, kRows / 32);
+  join_rows<D, kF8, kF8 ? 6 : 8>(a, jt, g.first, row >> 5, kRows / 32);
   for (int q = row; q < n; q += kRows) a.marks[part_of(g.first, q)] = 0;
   return true;
 }
