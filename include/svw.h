@@ -612,8 +612,9 @@ svw_status paged_attention(const void *q, int64_t q_token_stride, int64_t q_head
  * own, which is exact down to 2^-9 of its largest element (and within 2^-17 of
  * that one below); the weights enter the second product in fp16: within 2^-11 of
  * themselves down to 2^-21 of the largest, and within 2^-32 of that one below.
- * Beside the scores' and sums' fp32 rounding and its own to bf16, an output is so
- * within 2^-11 of sum_j w_j |v_j| and, for each key, 2^-32 of the largest w |v|.
+ * Beside the scores' and sums' fp32 roundings and its own to bf16, an output is so
+ * within 2^-11 of sum_j w_j |v_j| and 2^-32 of the largest weight times sum_j |v_j|
+ * (w normalised).
  */
 svw_status paged_attention_fp8(const void *q, int64_t q_token_stride, int64_t q_head_stride, svw_dtype dtype,
                                int32_t n_q_heads, int32_t N, const int32_t *cu_new, int64_t total_new,
